@@ -1,7 +1,7 @@
 """Python binding of the MI355X descriptor-driven tile mover.
 
 Argument marshalling only: every function here forwards to the C ABI declared
-in ``include/tmap.h`` (same names), implemented by hand-written gfx950 HIP
+in ``include/tmap.h`` and ``include/kvcache.h`` (same names), implemented by hand-written gfx950 HIP
 kernels in ``libatt_amd.so``.  There is no fallback: if the library has not
 been built, every call raises ``NativeLibraryMissing``.
 
@@ -29,7 +29,10 @@ OOB = {"zero": 0, "nan": 1}
 STATUS = {0: "OK", 1: "ERR_NULL", 2: "ERR_RANK", 3: "ERR_DTYPE", 4: "ERR_ALIGN",
           5: "ERR_DIM", 6: "ERR_STRIDE", 7: "ERR_BOX", 8: "ERR_ESTRIDE",
           9: "ERR_SWIZZLE_WIDTH", 10: "ERR_OOB_FILL_DTYPE", 11: "ERR_LDS_CAPACITY",
-          12: "ERR_UNSUPPORTED", 13: "ERR_HIP", 14: "ERR_TIMEOUT", 15: "ERR_DEVICE_CHECK"}
+          12: "ERR_UNSUPPORTED", 13: "ERR_HIP", 14: "ERR_TIMEOUT", 15: "ERR_DEVICE_CHECK",
+          16: "ERR_PAGE"}
+ROPE_LAYOUT = {"half": 0, "interleaved": 1}
+ROPE_SCALING = {"none": 0, "linear": 1, "base": 2, "ramp": 3}
 
 
 class NativeLibraryMissing(RuntimeError):
@@ -57,6 +60,17 @@ class tmap_info_t(ctypes.Structure):
                 ("lds_extent", ctypes.c_uint32 * 5), ("box_bytes", ctypes.c_uint32),
                 ("row_bytes", ctypes.c_uint32), ("atom_bytes", ctypes.c_uint32),
                 ("base", ctypes.c_uint64)]
+
+
+class rope_t(ctypes.Structure):
+    """Opaque plan of a rotation (copied bytewise by the library)."""
+    _fields_ = [("opaque", ctypes.c_uint8 * 1072)]
+
+
+class page_table_t(ctypes.Structure):
+    _fields_ = [("d_table", ctypes.c_void_p), ("d_lens", ctypes.c_void_p), ("d_refs", ctypes.c_void_p),
+                ("pitch", ctypes.c_uint64), ("rows", ctypes.c_uint32), ("row_pages", ctypes.c_uint32),
+                ("pages", ctypes.c_uint32), ("slots", ctypes.c_uint32)]
 
 
 _lib = None
@@ -111,6 +125,22 @@ def lib():
                      "txbar_selftest", "txbar_selftest_ex", "tile_device_status",
                      "lds_bank_probe", "hbm_probe", "hbm_probe_copy_ex", "hbm_probe_box_copy", "gemm_bf16", "gemm_bf16_ex", "gemm_bf16_f32"):
             getattr(L, name).restype = _I32
+        rp, pp, F64, U64 = _P(rope_t), _P(page_table_t), ctypes.c_double, ctypes.c_uint64
+        L.rope_encode.argtypes = [rp, _U32, _I32, F64, _I32, F64, _U32, F64, F64, F64]
+        L.rope_apply.argtypes = [rp, tp, tp, _V, _I32, _V]
+        L.rope_append.argtypes = [rp, tp, tp, tp, tp, tp, tp, pp, _V, _V, _V, _V]
+        L.page_workspace.argtypes = [pp, _U32]
+        L.page_copy.argtypes = [tp, _U32, _V, _V, _U32, _V]
+        L.page_extend.argtypes = [pp, _V, _V, _U32, _V, _V, U64, _V]
+        L.page_fork.argtypes = [pp, tp, _U32, _V, _V, _U32, _V, _V, U64, _V]
+        L.page_free.argtypes = [pp, _V, _U32, _V]
+        L.page_compact.argtypes = [pp, pp, tp, _U32, _V, _V, U64, _V]
+        L.attn_workspace.argtypes = [tp, tp, _U32, _U32]
+        L.attn_shared_prefix.argtypes = [tp, tp, tp, pp, _U32, _U32, _V, _U32, ctypes.c_float, tp, _V, _V, U64, _V]
+        for name in ("rope_encode", "rope_apply", "rope_append", "page_copy", "page_extend", "page_fork", "page_free",
+                     "page_compact", "attn_shared_prefix"):
+            getattr(L, name).restype = _I32
+        L.page_workspace.restype = L.attn_workspace.restype = U64
         _lib = L
     return _lib
 
@@ -290,3 +320,116 @@ def gemm_bf16_ex(A: tmap_t, B: tmap_t, d_C, M: int, N: int, K: int, ldc: int, st
     _check(lib().gemm_bf16_ex(ctypes.byref(A), ctypes.byref(B), _addr(d_C), int(M), int(N), int(K),
                               int(ldc), int(stages), int(group_m), int(xcd), int(mfma), _addr(stream)),
            "gemm_bf16_ex")
+
+
+# ---- a paged key / value cache (include/kvcache.h) ----------------------------
+
+
+def _ref(m):
+    return None if m is None else ctypes.byref(m)
+
+
+def _nbytes(ws) -> int:
+    """Bytes of a workspace given as a tensor (or any object with numel and
+    element_size), else 0."""
+    return int(ws.numel()) * int(ws.element_size()) if hasattr(ws, "numel") else 0
+
+
+def tmap_array(maps):
+    """Maps as one array, for the calls that take several pools."""
+    maps = list(maps)
+    return (tmap_t * len(maps))(*maps)
+
+
+def _pool_array(pools):
+    if pools is None:
+        return None, 0
+    if not isinstance(pools, ctypes.Array):
+        pools = tmap_array([pools] if isinstance(pools, tmap_t) else pools)
+    return pools, len(pools)
+
+
+def rope_encode(rot_dim: int, layout="half", base: float = 10000.0, scaling="none", factor: float = 1.0,
+                original_len: int = 0, slow: float = 1.0, fast: float = 32.0, magnitude: float = 1.0) -> rope_t:
+    """Plan of a rotation: layout "half" or "interleaved", scaling "none",
+    "linear", "base" or "ramp" (or the ROPE_* values)."""
+    r = rope_t()
+    lay = ROPE_LAYOUT[layout] if isinstance(layout, str) else int(layout)
+    sc = ROPE_SCALING[scaling] if isinstance(scaling, str) else int(scaling)
+    _check(lib().rope_encode(ctypes.byref(r), int(rot_dim), lay, float(base), sc, float(factor), int(original_len),
+                             float(slow), float(fast), float(magnitude)), "rope_encode")
+    return r
+
+
+def rope_apply(r: rope_t, x: tmap_t, y: tmap_t, d_pos, inverse=False, stream=0) -> None:
+    _check(lib().rope_apply(ctypes.byref(r), ctypes.byref(x), ctypes.byref(y), _addr(d_pos), int(inverse),
+                            _addr(stream)), "rope_apply")
+
+
+def rope_append(r, q, q_out, k: tmap_t, v: tmap_t, k_pool: tmap_t, v_pool: tmap_t, pt: page_table_t, d_rows, d_at,
+                d_pos, stream=0) -> None:
+    """r, and q with q_out, may be None (see kvcache.h)."""
+    _check(lib().rope_append(_ref(r), _ref(q), _ref(q_out), _ref(k), _ref(v), _ref(k_pool), _ref(v_pool), _ref(pt),
+                             _addr(d_rows), _addr(d_at), _addr(d_pos), _addr(stream)), "rope_append")
+
+
+def page_table(d_table, d_lens, d_refs, pages: int, slots: int, rows: int = 0, row_pages: int = 0,
+               pitch: int = 0) -> page_table_t:
+    """The struct of a table, lengths and counts.  rows, row_pages and pitch
+    come from d_table where it is a 2-D tensor whose columns lie side by side,
+    unless they are given."""
+    shape = getattr(d_table, "shape", None)
+    if shape is not None and len(shape) == 2:
+        if d_table.stride(1) != 1 and shape[1] > 1:
+            raise ValueError("page_table: the table's columns have to lie side by side")
+        rows, row_pages = rows or int(shape[0]), row_pages or int(shape[1])
+        pitch = pitch or int(d_table.stride(0))
+    for name, t in (("d_table", d_table), ("d_lens", d_lens), ("d_refs", d_refs)):
+        if hasattr(t, "element_size") and (t.element_size() != 4 or t.is_floating_point()):
+            raise TypeError(f"page_table: {name} has to be int32")
+    return page_table_t(_addr(d_table), _addr(d_lens), _addr(d_refs), pitch or row_pages, rows, row_pages,
+                        int(pages), int(slots))
+
+
+def page_workspace(pt: page_table_t, n: int) -> int:
+    return int(lib().page_workspace(ctypes.byref(pt), int(n)))
+
+
+def page_copy(pools, d_src, d_dst, n: int, stream=0) -> None:
+    arr, k = _pool_array(pools)
+    _check(lib().page_copy(arr, k, _addr(d_src), _addr(d_dst), int(n), _addr(stream)), "page_copy")
+
+
+def page_extend(pt: page_table_t, d_rows, d_add, n: int, d_ok, d_ws, stream=0, ws_bytes: int = 0) -> None:
+    """d_ws is a tensor, or an address with ws_bytes; so in the calls below."""
+    _check(lib().page_extend(_ref(pt), _addr(d_rows), _addr(d_add), int(n), _addr(d_ok), _addr(d_ws),
+                             ws_bytes or _nbytes(d_ws), _addr(stream)), "page_extend")
+
+
+def page_fork(pt: page_table_t, pools, d_src, d_dst, n: int, d_ok, d_ws, stream=0, ws_bytes: int = 0) -> None:
+    """pools: a map, several, or a tmap_array of them; None for the tables alone."""
+    arr, k = _pool_array(pools)
+    _check(lib().page_fork(_ref(pt), arr, k, _addr(d_src), _addr(d_dst), int(n), _addr(d_ok), _addr(d_ws),
+                           ws_bytes or _nbytes(d_ws), _addr(stream)), "page_fork")
+
+
+def page_free(pt: page_table_t, d_rows, n: int, stream=0) -> None:
+    _check(lib().page_free(_ref(pt), _addr(d_rows), int(n), _addr(stream)), "page_free")
+
+
+def page_compact(pt: page_table_t, pt_to: page_table_t, pools, d_used, d_ws, stream=0, ws_bytes: int = 0) -> None:
+    arr, k = _pool_array(pools)
+    _check(lib().page_compact(_ref(pt), _ref(pt_to), arr, k, _addr(d_used), _addr(d_ws),
+                              ws_bytes or _nbytes(d_ws), _addr(stream)), "page_compact")
+
+
+def attn_workspace(q: tmap_t, k_pool: tmap_t, prefix_len: int, suffix_hint: int) -> int:
+    return int(lib().attn_workspace(_ref(q), _ref(k_pool), int(prefix_len), int(suffix_hint)))
+
+
+def attn_shared_prefix(q: tmap_t, k_pool: tmap_t, v_pool: tmap_t, pt: page_table_t, prefix_row: int,
+                       prefix_len: int, d_rows, suffix_hint: int, scale: float, o: tmap_t, d_lse, d_ws, stream=0,
+                       ws_bytes: int = 0) -> None:
+    _check(lib().attn_shared_prefix(_ref(q), _ref(k_pool), _ref(v_pool), _ref(pt), int(prefix_row), int(prefix_len),
+                                    _addr(d_rows), int(suffix_hint), float(scale), _ref(o), _addr(d_lse),
+                                    _addr(d_ws), ws_bytes or _nbytes(d_ws), _addr(stream)), "attn_shared_prefix")

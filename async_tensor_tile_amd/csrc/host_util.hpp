@@ -12,6 +12,11 @@ tmap_status hip_fail(hipError_t e, const char* where);
 int esize_of(int32_t dtype);
 TmapImpl load_map(const tmap_t* m);
 
+// Device error word (kernels_tile.hip) and the bit that the cache kernels set
+// in it: a row, position or page out of range was skipped.
+enum : uint32_t { DEVERR_PAGE = 8u };
+tmap_status device_error_word(uint32_t** out);
+
 inline hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }
 
 // LDS bytes one workgroup may use on the current device.

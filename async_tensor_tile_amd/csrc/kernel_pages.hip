@@ -1,0 +1,661 @@
+// kernel_pages.hip -- the pages of the cache: handing out, sharing, giving
+// back, copying and compacting.
+//
+// A page's use count says how many rows hold it.  Handing pages out takes a
+// rank over the free pages (lowest index first) and a running sum over the
+// entries that ask (in their order), so the result does not depend on timing.
+// Both are taken by one workgroup: the counts of 64 Ki pages are read with all
+// of its loads in flight, turned into one 64-bit word of busy bits per thread
+// and ranked with population counts.  That is latency, not bandwidth: the
+// tables of a cache are small beside its pages.  Moving pages is bandwidth:
+// those kernels spread 16 KiB parts of pages over the whole GPU.
+#include <hip/hip_runtime.h>
+
+#include <cstring>
+
+#include "cache_util.hpp"
+
+namespace att {
+
+constexpr uint32_t kScanThreads = 1024;
+constexpr uint32_t kSweep = 64u * kScanThreads;   // pages one sweep of the workgroup covers
+constexpr uint32_t kCopyThreads = 256;
+constexpr uint32_t kPartChunks = 4u * kCopyThreads;   // 16-byte chunks of one part of a page (16 KiB)
+constexpr uint32_t kMaxPools = 256;
+
+struct Table {
+    int32_t* table;
+    int32_t* lens;
+    int32_t* refs;
+    uint64_t pitch;
+    uint32_t rows, row_pages, pages, slots;
+};
+
+static Table table_of(const page_table_t* pt) {
+    return {pt->d_table, pt->d_lens, pt->d_refs, pt->pitch, pt->rows, pt->row_pages, pt->pages, pt->slots};
+}
+
+// The pools of one geometry: a page is n2 x n1 rows of row_bytes (dimensions
+// that lie packed are merged, so a page without gaps is one row).
+struct Pools {
+    uint64_t base[kMaxPools];
+    int64_t page;                 // bytes from one page to the next
+    int64_t s1, s2;
+    uint32_t npool, n1, n2;
+    uint32_t row_bytes, row_chunks, chunks, parts;
+    uint32_t magic_row, magic_n1; // multiply-high divisors, 0 for 1
+};
+
+// ---- copying -------------------------------------------------------------------
+
+// Division by an invariant for numerators below 2^24 (chunks of a page).
+__device__ __forceinline__ uint32_t div_by(uint32_t n, uint32_t d, uint32_t magic) {
+    const uint32_t q = fdiv(n, magic);
+    return q * d > n ? q - 1 : q;
+}
+
+// One part (16 KiB) of one page, by 256 threads: the loads of a thread's four
+// chunks are in flight together.
+__device__ __forceinline__ void copy_part(const Pools& p, uint32_t pool, int64_t from, int64_t to, uint32_t part) {
+    const gbyte* src = gptr(p.base[pool]) + from * p.page;
+    gbyte* dst = gptr(p.base[pool]) + to * p.page;
+    u32x4 v[4];
+    int64_t off[4];
+    uint32_t left[4];
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i) {
+        const uint32_t c = part * kPartChunks + i * kCopyThreads + threadIdx.x;
+        left[i] = 0;
+        if (c < p.chunks) {
+            const uint32_t row = div_by(c, p.row_chunks, p.magic_row), k = c - row * p.row_chunks;
+            const uint32_t r2 = div_by(row, p.n1, p.magic_n1);
+            off[i] = (int64_t)r2 * p.s2 + (int64_t)(row - r2 * p.n1) * p.s1 + (int64_t)k * 16;
+            left[i] = p.row_bytes - k * 16u;
+            if (left[i] >= 16u) v[i] = *(const ATT_GLOBAL u32x4*)(src + off[i]);
+        }
+    }
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i) {
+        if (left[i] >= 16u) *(ATT_GLOBAL u32x4*)(dst + off[i]) = v[i];
+        else for (uint32_t b = 0; b < left[i]; ++b) dst[off[i] + b] = src[off[i] + b];   // a row's last bytes
+    }
+}
+
+__global__ __launch_bounds__(kCopyThreads) void k_page_copy(const Pools p, const int32_t* src, const int32_t* dst,
+                                                            uint32_t pages, uint32_t* err) {
+    const uint32_t i = blockIdx.x / p.parts, part = blockIdx.x - i * p.parts;
+    const int32_t from = src[i], to = dst[i];
+    if (from < 0 || to < 0) return;
+    if ((uint32_t)from >= pages || (uint32_t)to >= pages) {
+        if (threadIdx.x == 0) record_page_error(err);
+        return;
+    }
+    copy_part(p, blockIdx.y, from, to, part);
+}
+
+// ---- ranks ---------------------------------------------------------------------
+
+// Exclusive sum of v over the workgroup's kScanThreads threads, and the total.
+__device__ __forceinline__ uint32_t scan_block(uint32_t v, uint32_t* total) {
+    __shared__ uint32_t part[kScanThreads / 64];
+    const uint32_t lane = lane_id(), wave = threadIdx.x / 64u;
+    uint32_t x = v;
+#pragma unroll
+    for (uint32_t d = 1; d < 64; d <<= 1) {
+        const uint32_t y = __shfl_up(x, d);
+        if (lane >= d) x += y;
+    }
+    __syncthreads();                     // the previous call's readers are done
+    if (lane == 63) part[wave] = x;
+    __syncthreads();
+    uint32_t before = 0, all = 0;
+#pragma unroll
+    for (uint32_t w = 0; w < kScanThreads / 64; ++w) {
+        const uint32_t s = part[w];
+        before += w < wave ? s : 0u;
+        all += s;
+    }
+    *total = all;
+    return before + x - v;
+}
+
+// Busy bits (count above 0) of the 64 pages from base + 64 * thread on; pages
+// past the last are busy.  Reads are coalesced (lane after lane 16 bytes), the
+// bits change hands in LDS.
+__device__ __forceinline__ uint64_t busy_word(const int32_t* refs, uint32_t base, uint32_t pages) {
+    typedef int32_t i32x4 __attribute__((ext_vector_type(4), aligned(4)));
+    __shared__ uint8_t nibble[kSweep / 4];
+    i32x4 v[16];
+#pragma unroll
+    for (uint32_t u = 0; u < 16; ++u) {
+        const uint32_t p = base + (u * kScanThreads + threadIdx.x) * 4u;
+        v[u] = (i32x4)(1);
+        if (p + 4 <= pages) {
+            v[u] = *(const ATT_GLOBAL i32x4*)(gptr(refs) + (uint64_t)p * 4u);
+        } else {
+            for (uint32_t k = 0; k < 4; ++k)
+                if (p + k < pages) v[u][k] = refs[p + k];
+        }
+    }
+    __syncthreads();                     // the previous sweep's readers are done
+#pragma unroll
+    for (uint32_t u = 0; u < 16; ++u) {
+        nibble[u * kScanThreads + threadIdx.x] =
+            (uint8_t)((v[u][0] > 0) | (v[u][1] > 0) << 1 | (v[u][2] > 0) << 2 | (v[u][3] > 0) << 3);
+    }
+    __syncthreads();
+    uint64_t word = 0;
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(nibble) + threadIdx.x * 4u;
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i) {
+        uint32_t x = w[i];                               // four nibbles, one in each byte
+        x = (x | x >> 4) & 0x00FF00FFu;
+        x = (x | x >> 8) & 0xFFFFu;
+        word |= (uint64_t)x << (16 * i);
+    }
+    return word;
+}
+
+// ---- extend and fork -------------------------------------------------------------
+
+// Workspace of extend and fork: the running need before each entry, each
+// entry's need, the length its row started from, and the free pages.
+struct AllocWs {
+    int32_t* start;      // [n]
+    int32_t* need;       // [n], -1: not served whatever is free
+    int32_t* held;       // [n]
+    int32_t* fresh;      // [pages]
+};
+
+// Entry i's need of pages, and the length of the row it starts from.  -1 for
+// an entry that cannot be served.
+template <bool FORK>
+__device__ __forceinline__ int32_t entry_need(const Table& t, const int32_t* a, const int32_t* b, uint32_t i,
+                                              int32_t* held, uint32_t* err) {
+    *held = 0;
+    const uint32_t src = (uint32_t)a[i];
+    if (src >= t.rows) {
+        record_page_error(err);
+        return -1;
+    }
+    const int64_t len = t.lens[src], room = (int64_t)t.slots * t.row_pages;
+    if (len < 0 || len > room) {
+        record_page_error(err);
+        return -1;
+    }
+    *held = (int32_t)len;
+    if (FORK) {
+        const uint32_t dst = (uint32_t)b[i];
+        if (dst >= t.rows || t.lens[dst] != 0) {
+            record_page_error(err);
+            return -1;
+        }
+        return len % t.slots != 0;
+    }
+    const int64_t add = b[i];
+    if (add < 0) {
+        record_page_error(err);
+        return -1;
+    }
+    if (len + add > room) return -1;
+    return (int32_t)((uint32_t)(len + add + t.slots - 1) / t.slots - (uint32_t)(len + t.slots - 1) / t.slots);
+}
+
+// One workgroup hands out the lowest free pages.  Extend finishes here; fork
+// leaves the rows and the data to k_fork_rows.
+template <bool FORK>
+__global__ __launch_bounds__(kScanThreads) void k_hand_out(const Table t, const int32_t* a, const int32_t* b,
+                                                           uint32_t n, int32_t* ok, AllocWs ws, uint32_t* err) {
+    const uint32_t tid = threadIdx.x;
+    uint64_t want = 0;                                    // pages asked for by the entries so far
+    for (uint32_t i0 = 0; i0 < n; i0 += kScanThreads) {
+        const uint32_t i = i0 + tid;
+        int32_t held = 0, need = 0;
+        if (i < n) need = entry_need<FORK>(t, a, b, i, &held, err);
+        uint32_t all;
+        const uint32_t before = scan_block(need > 0 ? (uint32_t)need : 0u, &all);   // a need is below 2^21
+        if (i < n) {
+            const uint64_t s = want + before;
+            ws.start[i] = (int32_t)(s < 0x7FFFFFFFull ? s : 0x7FFFFFFFull);
+            ws.need[i] = need;
+            ws.held[i] = held;
+        }
+        want += all;
+    }
+    uint32_t found = 0;
+    for (uint32_t base = 0; base < t.pages && found < want; base += kSweep) {
+        uint64_t open = ~busy_word(t.refs, base, t.pages);
+        uint32_t all;
+        uint32_t rank = found + scan_block((uint32_t)__popcll(open), &all);
+        while (open && rank < want) {
+            const int k = __ffsll((unsigned long long)open) - 1;
+            open &= open - 1;
+            ws.fresh[rank++] = (int32_t)(base + tid * 64u + (uint32_t)k);
+        }
+        found += all;
+    }
+    __syncthreads();                                      // the lists are written
+    // An entry that needs no page is still served only while those before it are.
+    for (uint32_t i = tid; i < n; i += kScanThreads) {
+        const int32_t need = ws.need[i];
+        const uint64_t start = (uint32_t)ws.start[i];
+        const bool served = need >= 0 && start + (uint32_t)need <= found;
+        ok[i] = served;
+        if (FORK) {
+            const int32_t page = served && need ? ws.fresh[start] : -1;
+            if (page >= 0) t.refs[page] = 1;
+            ws.need[i] = served ? page : -2;              // for k_fork_rows: the new page, -1 none, -2 not served
+        } else if (served) {
+            const uint32_t row = (uint32_t)a[i];
+            t.lens[row] = ws.held[i] + b[i];
+        }
+    }
+    if (!FORK) {
+        // the new pages: a wave for an entry, a lane for a page
+        const uint32_t lane = lane_id();
+        for (uint32_t i = tid / 64u; i < n; i += kScanThreads / 64u) {
+            const int32_t need = ws.need[i];
+            const uint64_t start = (uint32_t)ws.start[i];
+            if (need <= 0 || start + (uint32_t)need > found) continue;
+            const uint32_t first = ((uint32_t)ws.held[i] + t.slots - 1) / t.slots;
+            int32_t* row = t.table + (uint64_t)(uint32_t)a[i] * t.pitch + first;
+            for (uint32_t k = lane; k < (uint32_t)need; k += 64u) {
+                const int32_t page = ws.fresh[start + k];
+                row[k] = page;
+                t.refs[page] = 1;
+            }
+        }
+    }
+}
+
+// Rows and data of a fork, after k_hand_out.  blockIdx.x: the entry; y: pieces
+// of 1024 table entries first, then parts of the unfinished page, pool after
+// pool.
+__global__ __launch_bounds__(kCopyThreads) void k_fork_rows(const Table t, const Pools p, const int32_t* src,
+                                                            const int32_t* dst, AllocWs ws, uint32_t pieces,
+                                                            uint32_t* err) {
+    const uint32_t i = blockIdx.x;
+    const int32_t fresh = ws.need[i];
+    if (fresh == -2) return;
+    const int32_t held = ws.held[i];
+    const uint32_t full = (uint32_t)held / t.slots;
+    const int32_t* from = t.table + (uint64_t)(uint32_t)src[i] * t.pitch;
+    if (blockIdx.y < pieces) {
+        int32_t* to = t.table + (uint64_t)(uint32_t)dst[i] * t.pitch;
+        if (blockIdx.y == 0 && threadIdx.x == 0) t.lens[(uint32_t)dst[i]] = held;
+        for (uint32_t k = 0; k < 4; ++k) {
+            const uint32_t c = blockIdx.y * 4u * kCopyThreads + k * kCopyThreads + threadIdx.x;
+            if (c >= t.row_pages) break;
+            int32_t page = -1;
+            if (c < full) {
+                page = from[c];
+                if ((uint32_t)page < t.pages) atomicAdd(&t.refs[page], 1);
+                else record_page_error(err);
+            } else if (c == full) {
+                page = fresh;
+            }
+            to[c] = page;
+        }
+        return;
+    }
+    if (fresh < 0) return;
+    const uint32_t at = blockIdx.y - pieces, pool = at / p.parts, part = at - pool * p.parts;
+    const int32_t last = from[full];
+    if ((uint32_t)last >= t.pages) {
+        if (threadIdx.x == 0 && at == 0) record_page_error(err);
+        return;
+    }
+    copy_part(p, pool, last, fresh, part);
+}
+
+// ---- free ------------------------------------------------------------------------
+
+// blockIdx.x: the entry; y: pieces of 1024 table entries.  A page is taken
+// out of the table with an exchange, so a row listed twice gives it back once.
+__global__ __launch_bounds__(kCopyThreads) void k_page_free(const Table t, const int32_t* rows, uint32_t* err) {
+    const uint32_t row = (uint32_t)rows[blockIdx.x];
+    if (row >= t.rows) {
+        if (threadIdx.x == 0) record_page_error(err);
+        return;
+    }
+    int32_t* at = t.table + (uint64_t)row * t.pitch;
+    if (blockIdx.y == 0 && threadIdx.x == 0) t.lens[row] = 0;
+    for (uint32_t k = 0; k < 4; ++k) {
+        const uint32_t c = blockIdx.y * 4u * kCopyThreads + k * kCopyThreads + threadIdx.x;
+        if (c >= t.row_pages) break;
+        if (at[c] == -1) continue;
+        const int32_t page = atomicExch(&at[c], -1);
+        if (page == -1) continue;
+        if ((uint32_t)page < t.pages) atomicSub(&t.refs[page], 1);
+        else record_page_error(err);
+    }
+}
+
+// ---- compact ----------------------------------------------------------------------
+
+struct CompactWs {
+    uint64_t* busy;       // [words]: busy bits of 64 pages each
+    uint32_t* before;     // [words]: busy pages before the word
+    int32_t* hole;        // [pages]: free pages below U, ascending
+    int32_t* mover;       // [pages]: busy pages at or above U, ascending
+    uint32_t* count;      // U, how many move, busy pages below U
+};
+
+__global__ __launch_bounds__(kScanThreads) void k_compact_plan(const Table t, CompactWs ws, int32_t* used) {
+    const uint32_t tid = threadIdx.x;
+    uint32_t total = 0;
+    for (uint32_t base = 0; base < t.pages; base += kSweep) {
+        uint64_t busy = busy_word(t.refs, base, t.pages);
+        const uint32_t p = base + tid * 64u;
+        // pages past the last are not in use here
+        if (p + 64u > t.pages) busy &= p < t.pages ? (~0ull >> (p + 64u - t.pages)) : 0ull;
+        uint32_t all;
+        const uint32_t rank = total + scan_block((uint32_t)__popcll(busy), &all);
+        if (p < t.pages) {
+            ws.busy[p / 64u] = busy;
+            ws.before[p / 64u] = rank;
+        }
+        total += all;
+    }
+    __syncthreads();                                      // busy and before are written (by their own threads)
+    __shared__ uint32_t below;                            // busy pages below U
+    if (tid == 0) below = total;
+    __syncthreads();
+    const uint32_t U = total;
+    if (tid == 0 && U < t.pages)
+        below = ws.before[U / 64u] + (uint32_t)__popcll(ws.busy[U / 64u] & ((1ull << (U % 64u)) - 1ull));
+    __syncthreads();
+    const uint32_t kept = below;
+    for (uint32_t w = tid; w < (t.pages + 63u) / 64u; w += kScanThreads) {
+        const uint64_t busy = ws.busy[w];
+        const uint32_t p = w * 64u, rank = ws.before[w];
+        // free pages of this word below U
+        const uint64_t low = p + 64u <= U ? ~0ull : p < U ? (1ull << (U - p)) - 1ull : 0ull;
+        uint32_t r = p - rank;
+        for (uint64_t x = ~busy & low; x; x &= x - 1)
+            ws.hole[r++] = (int32_t)(p + (uint32_t)__ffsll((unsigned long long)x) - 1u);
+        r = rank + (uint32_t)__popcll(busy & low) - kept;  // busy pages at or above U before the word's first
+        for (uint64_t x = busy & ~low; x; x &= x - 1)
+            ws.mover[r++] = (int32_t)(p + (uint32_t)__ffsll((unsigned long long)x) - 1u);
+    }
+    if (tid == 0) {
+        ws.count[0] = U;
+        ws.count[1] = U - kept;
+        if (used) *used = (int32_t)U;
+    }
+}
+
+// Where a page goes: itself below U, its rank's hole above, -1 if it is free there.
+__device__ __forceinline__ int32_t new_place(const CompactWs& ws, uint32_t page, uint32_t U, uint32_t moves) {
+    if (page < U) return (int32_t)page;
+    const uint64_t word = ws.busy[page / 64u], bit = 1ull << (page % 64u);
+    if (!(word & bit)) return -1;
+    const uint32_t rank = ws.before[page / 64u] + (uint32_t)__popcll(word & (bit - 1ull));
+    return ws.hole[rank - (U - moves)];
+}
+
+// The first table_blocks workgroups rewrite the table and the counts, the
+// others move the pages.
+__global__ __launch_bounds__(kCopyThreads) void k_compact_move(const Table t, int32_t* table_out, uint64_t pitch_out,
+                                                               int32_t* refs_out, const Pools p, CompactWs ws,
+                                                               uint32_t table_blocks, uint32_t* err) {
+    const uint32_t U = ws.count[0], moves = ws.count[1];
+    if (blockIdx.x < table_blocks) {
+        const uint64_t step = (uint64_t)table_blocks * kCopyThreads, at = (uint64_t)blockIdx.x * kCopyThreads + threadIdx.x;
+        for (uint64_t i = at; i < (uint64_t)t.rows * t.row_pages; i += step) {
+            const uint32_t row = (uint32_t)(i / t.row_pages), c = (uint32_t)(i - (uint64_t)row * t.row_pages);
+            int32_t page = t.table[(uint64_t)row * t.pitch + c];
+            if (page >= 0) {
+                if ((uint32_t)page < t.pages) page = new_place(ws, (uint32_t)page, U, moves);
+                else record_page_error(err);
+            }
+            table_out[(uint64_t)row * pitch_out + c] = page;
+        }
+        for (uint64_t i = at; i < moves; i += step) {
+            const int32_t h = ws.hole[i], m = ws.mover[i];
+            const int32_t count = t.refs[m];
+            refs_out[h] = count;
+            refs_out[m] = 0;
+        }
+        if (refs_out != t.refs) {                         // the others keep theirs
+            for (uint64_t i = at; i < t.pages; i += step) {
+                const bool busy = ws.busy[i / 64u] >> (i % 64u) & 1u;
+                if (busy == (i < U)) refs_out[i] = t.refs[i];
+            }
+        }
+        return;
+    }
+    const uint64_t work = (uint64_t)moves * p.npool * p.parts;
+    for (uint64_t i = blockIdx.x - table_blocks; i < work; i += gridDim.x - table_blocks) {
+        const uint32_t part = (uint32_t)(i % p.parts);
+        const uint64_t r = i / p.parts;
+        const uint32_t m = (uint32_t)(r % moves), pool = (uint32_t)(r / moves);
+        copy_part(p, pool, ws.mover[m], ws.hole[m], part);
+    }
+}
+
+// ---- host ------------------------------------------------------------------------
+
+static tmap_status pools_of(const tmap_t* maps, uint32_t npool, const page_table_t* pt, Pools* out, uint32_t* pages) {
+    std::memset(out, 0, sizeof(*out));
+    out->npool = npool;
+    out->parts = 1;
+    if (npool == 0) return TMAP_OK;
+    if (!maps) return TMAP_ERR_NULL;
+    if (npool > kMaxPools) return TMAP_ERR_UNSUPPORTED;
+    View v;
+    int32_t type = 0;
+    for (uint32_t i = 0; i < npool; ++i) {
+        View w;
+        int32_t wt;
+        const tmap_status st = view_of(maps + i, 4, &w, &wt);
+        if (st) return st;
+        if (i == 0) {
+            v = w;
+            type = wt;
+        }
+        if (wt != type || !same_dims(v, w)) return TMAP_ERR_UNSUPPORTED;
+        for (int d = 0; d < 4; ++d)
+            if (v.stride[d] != w.stride[d]) return TMAP_ERR_UNSUPPORTED;
+        out->base[i] = w.base;
+    }
+    if (v.dim[3] > 0x7FFFFFFF) return TMAP_ERR_UNSUPPORTED;
+    if (pt && ((uint64_t)v.dim[1] != pt->slots || (uint64_t)v.dim[3] != pt->pages)) return TMAP_ERR_UNSUPPORTED;
+    uint64_t row = (uint64_t)v.dim[0] * (uint64_t)v.stride[0], n1 = (uint64_t)v.dim[1], n2 = (uint64_t)v.dim[2];
+    int64_t s1 = v.stride[1], s2 = v.stride[2];
+    if (s2 < s1 || n1 == 1) {                             // the closer dimension first
+        const int64_t s = s1;
+        const uint64_t n = n1;
+        s1 = s2, n1 = n2, s2 = s, n2 = n;
+    }
+    if (n1 == 1 || (uint64_t)s1 == row) {
+        row *= n1;
+        n1 = n2, s1 = s2, n2 = 1, s2 = 0;
+        if (n1 == 1 || (uint64_t)s1 == row) {
+            row *= n1;
+            n1 = 1, s1 = 0;
+        }
+    }
+    const uint64_t row_chunks = (row + 15) / 16, chunks = row_chunks * n1 * n2;
+    if (chunks > (1ull << 24)) return TMAP_ERR_UNSUPPORTED;   // 256 MiB of one page
+    out->page = v.stride[3];
+    out->s1 = s1;
+    out->s2 = s2;
+    out->n1 = (uint32_t)n1;
+    out->n2 = (uint32_t)n2;
+    out->row_bytes = (uint32_t)row;
+    out->row_chunks = (uint32_t)row_chunks;
+    out->chunks = (uint32_t)chunks;
+    out->parts = (uint32_t)((chunks + kPartChunks - 1) / kPartChunks);
+    out->magic_row = magic_for(out->row_chunks);
+    out->magic_n1 = magic_for(out->n1);
+    *pages = (uint32_t)v.dim[3];
+    return TMAP_OK;
+}
+
+static uint64_t align16(uint64_t x) { return (x + 15) & ~15ull; }
+
+static uint64_t alloc_bytes(uint32_t pages, uint32_t n) { return 3 * align16(4ull * n) + align16(4ull * pages); }
+
+static AllocWs alloc_ws(void* ws, uint32_t n) {
+    uint8_t* p = static_cast<uint8_t*>(ws);
+    const uint64_t list = align16(4ull * n);
+    return {(int32_t*)p, (int32_t*)(p + list), (int32_t*)(p + 2 * list), (int32_t*)(p + 3 * list)};
+}
+
+static uint64_t compact_bytes(uint32_t pages) {
+    const uint64_t words = ((uint64_t)pages + 63) / 64;
+    return align16(8 * words) + align16(4 * words) + 2 * align16(4ull * pages) + 16;
+}
+
+static CompactWs compact_ws(void* ws, uint32_t pages) {
+    const uint64_t words = ((uint64_t)pages + 63) / 64;
+    uint8_t* p = static_cast<uint8_t*>(ws);
+    CompactWs w;
+    w.busy = (uint64_t*)p;
+    p += align16(8 * words);
+    w.before = (uint32_t*)p;
+    p += align16(4 * words);
+    w.hole = (int32_t*)p;
+    p += align16(4ull * pages);
+    w.mover = (int32_t*)p;
+    p += align16(4ull * pages);
+    w.count = (uint32_t*)p;
+    return w;
+}
+
+static tmap_status check_ws(const void* ws, uint64_t bytes, uint64_t need) {
+    if (!ws) return TMAP_ERR_NULL;
+    if (reinterpret_cast<uintptr_t>(ws) % 16 != 0) return TMAP_ERR_ALIGN;
+    return bytes < need ? TMAP_ERR_UNSUPPORTED : TMAP_OK;
+}
+
+}  // namespace att
+
+using namespace att;
+
+extern "C" uint64_t page_workspace(const page_table_t* pt, uint32_t n) {
+    if (!pt) return 0;
+    const uint64_t a = alloc_bytes(pt->pages, n), c = compact_bytes(pt->pages);
+    return a > c ? a : c;
+}
+
+extern "C" tmap_status page_copy(const tmap_t* pools, uint32_t npool, const int32_t* d_src, const int32_t* d_dst,
+                                 uint32_t n, void* stream) {
+    if (!pools) return TMAP_ERR_NULL;
+    if (npool == 0) return TMAP_ERR_UNSUPPORTED;
+    Pools p;
+    uint32_t pages = 0;
+    tmap_status st = pools_of(pools, npool, nullptr, &p, &pages);
+    if (st) return st;
+    if (n == 0) return TMAP_OK;
+    if (!d_src || !d_dst) return TMAP_ERR_NULL;
+    if ((uint64_t)n * p.parts > 0x7FFFFFFFull) return TMAP_ERR_UNSUPPORTED;
+    uint32_t* err = nullptr;
+    st = device_error_word(&err);
+    if (st) return st;
+    hipLaunchKernelGGL(k_page_copy, dim3(n * p.parts, npool), dim3(kCopyThreads), 0, as_stream(stream), p, d_src,
+                       d_dst, pages, err);
+    return check_launch("page_copy");
+}
+
+extern "C" tmap_status page_extend(const page_table_t* pt, const int32_t* d_rows, const int32_t* d_add, uint32_t n,
+                                   int32_t* d_ok, void* d_ws, uint64_t ws_bytes, void* stream) {
+    tmap_status st = check_table(pt);
+    if (st) return st;
+    if (!pt->d_lens || !pt->d_refs) return TMAP_ERR_NULL;
+    if (n == 0) return TMAP_OK;
+    if (!d_rows || !d_add || !d_ok) return TMAP_ERR_NULL;
+    st = check_ws(d_ws, ws_bytes, alloc_bytes(pt->pages, n));
+    if (st) return st;
+    uint32_t* err = nullptr;
+    st = device_error_word(&err);
+    if (st) return st;
+    hipLaunchKernelGGL(k_hand_out<false>, dim3(1), dim3(kScanThreads), 0, as_stream(stream), table_of(pt), d_rows,
+                       d_add, n, d_ok, alloc_ws(d_ws, n), err);
+    return check_launch("page_extend");
+}
+
+extern "C" tmap_status page_fork(const page_table_t* pt, const tmap_t* pools, uint32_t npool, const int32_t* d_src,
+                                 const int32_t* d_dst, uint32_t n, int32_t* d_ok, void* d_ws, uint64_t ws_bytes,
+                                 void* stream) {
+    tmap_status st = check_table(pt);
+    if (st) return st;
+    if (!pt->d_lens || !pt->d_refs) return TMAP_ERR_NULL;
+    Pools p;
+    uint32_t pages = 0;
+    st = pools_of(pools, npool, pt, &p, &pages);
+    if (st) return st;
+    if (n == 0) return TMAP_OK;
+    if (!d_src || !d_dst || !d_ok) return TMAP_ERR_NULL;
+    st = check_ws(d_ws, ws_bytes, alloc_bytes(pt->pages, n));
+    if (st) return st;
+    const uint32_t pieces = (pt->row_pages + 4 * kCopyThreads - 1) / (4 * kCopyThreads);
+    const uint64_t gy = (uint64_t)pieces + (uint64_t)npool * p.parts;
+    if (gy > 65535 || n > 0x7FFFFFFFu) return TMAP_ERR_UNSUPPORTED;
+    uint32_t* err = nullptr;
+    st = device_error_word(&err);
+    if (st) return st;
+    const AllocWs ws = alloc_ws(d_ws, n);
+    hipLaunchKernelGGL(k_hand_out<true>, dim3(1), dim3(kScanThreads), 0, as_stream(stream), table_of(pt), d_src,
+                       d_dst, n, d_ok, ws, err);
+    st = check_launch("page_fork");
+    if (st) return st;
+    hipLaunchKernelGGL(k_fork_rows, dim3(n, (uint32_t)gy), dim3(kCopyThreads), 0, as_stream(stream), table_of(pt), p,
+                       d_src, d_dst, ws, pieces, err);
+    return check_launch("page_fork");
+}
+
+extern "C" tmap_status page_free(const page_table_t* pt, const int32_t* d_rows, uint32_t n, void* stream) {
+    tmap_status st = check_table(pt);
+    if (st) return st;
+    if (!pt->d_lens || !pt->d_refs) return TMAP_ERR_NULL;
+    if (n == 0) return TMAP_OK;
+    if (!d_rows) return TMAP_ERR_NULL;
+    const uint32_t pieces = (pt->row_pages + 4 * kCopyThreads - 1) / (4 * kCopyThreads);
+    if (pieces > 65535 || n > 0x7FFFFFFFu) return TMAP_ERR_UNSUPPORTED;
+    uint32_t* err = nullptr;
+    st = device_error_word(&err);
+    if (st) return st;
+    hipLaunchKernelGGL(k_page_free, dim3(n, pieces), dim3(kCopyThreads), 0, as_stream(stream), table_of(pt), d_rows,
+                       err);
+    return check_launch("page_free");
+}
+
+extern "C" tmap_status page_compact(const page_table_t* from, const page_table_t* to, const tmap_t* pools,
+                                    uint32_t npool, int32_t* d_used, void* d_ws, uint64_t ws_bytes, void* stream) {
+    tmap_status st = check_table(from);
+    if (st == TMAP_OK) st = check_table(to);
+    if (st) return st;
+    if (!from->d_refs || !to->d_refs) return TMAP_ERR_NULL;
+    if (from->rows != to->rows || from->row_pages != to->row_pages || from->pages != to->pages ||
+        from->slots != to->slots)
+        return TMAP_ERR_UNSUPPORTED;
+    if (from->d_table == to->d_table && from->pitch != to->pitch) return TMAP_ERR_UNSUPPORTED;
+    Pools p;
+    uint32_t pages = 0;
+    st = pools_of(pools, npool, from, &p, &pages);
+    if (st) return st;
+    st = check_ws(d_ws, ws_bytes, compact_bytes(from->pages));
+    if (st) return st;
+    uint32_t* err = nullptr;
+    st = device_error_word(&err);
+    if (st) return st;
+    uint32_t cus = 0;
+    st = device_cu_count(&cus);
+    if (st) return st;
+    const CompactWs ws = compact_ws(d_ws, from->pages);
+    hipLaunchKernelGGL(k_compact_plan, dim3(1), dim3(kScanThreads), 0, as_stream(stream), table_of(from), ws, d_used);
+    st = check_launch("page_compact");
+    if (st) return st;
+    // how many pages move is known on the device alone: as many workgroups as keep the GPU full, at most one for
+    // each part that could move (half of the pages)
+    const uint64_t entries = (uint64_t)from->rows * from->row_pages + from->pages;
+    const uint64_t tb = (entries + 4 * kCopyThreads - 1) / (4 * kCopyThreads);
+    const uint32_t table_blocks = (uint32_t)(tb < 4ull * cus ? tb : 4ull * cus);
+    const uint64_t most = ((uint64_t)from->pages / 2) * npool * p.parts;
+    const uint32_t movers = (uint32_t)(most < 8ull * cus ? most : 8ull * cus);
+    hipLaunchKernelGGL(k_compact_move, dim3(table_blocks + movers), dim3(kCopyThreads), 0, as_stream(stream),
+                       table_of(from), to->d_table, to->pitch, to->d_refs, p, ws, table_blocks, err);
+    return check_launch("page_compact");
+}

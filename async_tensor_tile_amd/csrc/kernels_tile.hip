@@ -8,6 +8,7 @@
 // "TMA store" / "TMA reduce" would, and the image is dumped or consumed.
 #include <hip/hip_runtime.h>
 
+#include <atomic>
 #include <cstring>
 
 #include "host_util.hpp"
@@ -23,6 +24,7 @@ constexpr uint32_t kBatchThreads = 256;
 // ATT_DEBUG, a box whose waves issued other than its byte count or a barrier
 // found in the wrong state when its box was consumed.  Read and cleared by
 // tile_device_status.
+// DEVERR_PAGE (host_util.hpp) is recorded by the cache kernels.
 enum : uint32_t { DEVERR_TIMEOUT = 1u, DEVERR_BYTES = 2u, DEVERR_PHASE = 4u };
 static __device__ uint32_t g_dev_error;
 
@@ -296,6 +298,23 @@ __global__ __launch_bounds__(64) void k_lds_bank_probe(int32_t layout, uint32_t 
 
 // The caller's descriptor by value for a kernel argument; copied bytewise,
 // since the caller's 128 bytes need not sit at tmap_t's 64-byte alignment.
+// The address of the error word on the current device, for kernels of other
+// source files.  It never changes, so it is looked up once per device.
+tmap_status device_error_word(uint32_t** out) {
+    static std::atomic<uint32_t*> known[64];
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
+    const bool keep = dev >= 0 && dev < 64;
+    if (keep && (*out = known[dev].load(std::memory_order_acquire))) return TMAP_OK;
+    void* p = nullptr;
+    e = hipGetSymbolAddress(&p, HIP_SYMBOL(g_dev_error));
+    if (e != hipSuccess) return hip_fail(e, "hipGetSymbolAddress");
+    *out = static_cast<uint32_t*>(p);
+    if (keep) known[dev].store(*out, std::memory_order_release);
+    return TMAP_OK;
+}
+
 static tmap_t map_value(const tmap_t* m) {
     tmap_t v;
     std::memcpy(&v, m, sizeof(v));
@@ -419,7 +438,8 @@ extern "C" tmap_status tile_device_status(void* stream) {
     const uint32_t zero = 0;
     e = hipMemcpyToSymbol(HIP_SYMBOL(g_dev_error), &zero, sizeof(zero), 0, hipMemcpyHostToDevice);
     if (e != hipSuccess) return hip_fail(e, "hipMemcpyToSymbol");
-    return (bits & DEVERR_TIMEOUT) ? TMAP_ERR_TIMEOUT : TMAP_ERR_DEVICE_CHECK;
+    if (bits & DEVERR_TIMEOUT) return TMAP_ERR_TIMEOUT;
+    return (bits & (DEVERR_BYTES | DEVERR_PHASE)) ? TMAP_ERR_DEVICE_CHECK : TMAP_ERR_PAGE;
 }
 
 extern "C" tmap_status lds_bank_probe(int32_t layout, uint32_t iters, int32_t* d_hist, void* stream) {

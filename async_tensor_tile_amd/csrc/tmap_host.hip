@@ -257,6 +257,7 @@ extern "C" const char* tmap_strerror(tmap_status s) {
     case TMAP_ERR_HIP: return "HIP runtime error";
     case TMAP_ERR_TIMEOUT: return "a bounded barrier wait in a kernel gave up; the box it guarded is not valid";
     case TMAP_ERR_DEVICE_CHECK: return "a device-side check of the debug build failed";
+    case TMAP_ERR_PAGE: return "a kernel skipped a row, position or page that is out of range";
     default: return "unknown status";
     }
 }

@@ -96,8 +96,11 @@ enum {
     TMAP_ERR_TIMEOUT = 14,        /* a bounded barrier wait inside a kernel
                                      gave up: the box it guarded is not valid
                                      (reported by tile_device_status)        */
-    TMAP_ERR_DEVICE_CHECK = 15    /* a check of a debug build failed on the
+    TMAP_ERR_DEVICE_CHECK = 15,   /* a check of a debug build failed on the
                                      device (tile_device_status)             */
+    TMAP_ERR_PAGE = 16            /* a kernel of kvcache.h met a row, position
+                                     or page out of range and skipped it
+                                     (reported by tile_device_status)        */
 };
 
 /* Largest box image (bytes) a map may describe: the 160 KiB of LDS per CU
@@ -311,13 +314,15 @@ tmap_status txbar_selftest_ex(const tmap_t* m, const int32_t* d_coords, uint32_t
                               void* d_lds_image_out, void* stream);
 
 /* Device-side status of the batch calls (tile_load, tile_load_im2col,
- * txbar_selftest[_ex]): their kernels never trap; a barrier wait that gives
+ * txbar_selftest[_ex]) and of the calls of kvcache.h: their kernels never trap; a barrier wait that gives
  * up (a box whose bytes never all arrived) or, in a debug build (ATT_DEBUG),
  * a failed device check is recorded in a per-device error word instead.
  * This call synchronises `stream`, reads that word on the current device
  * and clears it: TMAP_OK if nothing was recorded since the last call,
  * TMAP_ERR_TIMEOUT if a wait gave up, TMAP_ERR_DEVICE_CHECK for a debug
- * check, TMAP_ERR_HIP on a runtime error.  Not for use under graph
+ * check, TMAP_ERR_PAGE for a row, position or page out of range that a
+ * kernel of kvcache.h skipped (the first of these that holds),
+ * TMAP_ERR_HIP on a runtime error.  Not for use under graph
  * capture (it synchronises). */
 tmap_status tile_device_status(void* stream);
 
