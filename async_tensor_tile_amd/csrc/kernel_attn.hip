@@ -1,5 +1,22 @@
 // kernel_attn.hip -- attention of a batch behind a shared prefix, over a
 // paged cache.
+//
+// The queries of one key / value head, all sequences and the group's heads
+// together, are the rows of one tall product with the prefix: it is read for
+// 128 rows at a time.  Each sequence's own tokens are read for its rows alone.
+// Both kinds of work are cut along the keys into parts that run in one launch
+// (the first is bound by the matrix cores, the second by HBM, and they share
+// the compute units); each part leaves the largest score, the sum of weights
+// and the weighted sum of values of its rows, and a second launch joins them:
+//   m = max_i m_i, w_i = exp(m_i - m), o = sum_i w_i o_i / sum_i w_i l_i.
+//
+// A wave holds 32 queries.  Scores are computed transposed, keys x queries
+// (A = keys from LDS, B = queries in registers), so that a lane owns one query
+// and the maximum and the sum over keys stay inside it, up to one exchange
+// with the lane 32 further.  The weights, rounded to the element type, then
+// already lie as the second product's B operand (values transposed x weights)
+// if that product takes its keys in the order 0-3, 8-11 | 4-7, 12-15, which
+// the transposing LDS read of the values delivers for free.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -10,6 +27,40 @@
 namespace att {
 
 constexpr uint32_t kThreads = 256;
+constexpr uint32_t kWaves = kThreads / 64;
+constexpr uint32_t kRows = 32;                    // queries of a wave
+constexpr uint32_t kWgRows = kWaves * kRows;      // queries of a workgroup on the prefix
+constexpr uint32_t kTile = 64;                    // keys of a shared tile
+constexpr uint32_t kOwnTile = 32;                 // keys of a wave's own tile
+constexpr uint32_t kSegment = 256;                // keys whose addresses are worked out together
+constexpr float kLazy = 8.0f;                     // powers of two by which a weight may pass 1
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+template <typename T>
+struct Vec;
+template <>
+struct Vec<__bf16> {
+    typedef __bf16 v8 __attribute__((ext_vector_type(8)));
+    typedef __bf16 v4 __attribute__((ext_vector_type(4)));
+    static constexpr uint32_t kExp = 0x7F80u;     // exponent bits: all set for infinities and NaN
+};
+template <>
+struct Vec<_Float16> {
+    typedef _Float16 v8 __attribute__((ext_vector_type(8)));
+    typedef _Float16 v4 __attribute__((ext_vector_type(4)));
+    static constexpr uint32_t kExp = 0x7C00u;
+};
+
+__device__ __forceinline__ f32x16 mfma(Vec<__bf16>::v8 a, Vec<__bf16>::v8 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 mfma(Vec<_Float16>::v8 a, Vec<_Float16>::v8 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
 
 struct AttnArgs {
     View q, o, k, v;                 // q, o {dim, heads, q_len, batch}; pools {dim, slots, heads, pages}
@@ -17,97 +68,697 @@ struct AttnArgs {
     const int32_t* lens;
     const int32_t* rows;
     uint64_t pitch;
-    uint32_t table_rows, row_pages, pages, slots;
-    uint32_t prefix_row, prefix_len;
-    float scale;
     float* lse;
     uint32_t* err;
+    f32x4* part_o;                   // partial results: prefix parts, then the sequences' own
+    float2* part_ml;
+    uint32_t table_rows, row_pages, pages, slots;
+    uint32_t prefix_row, prefix_len, hint;
+    uint32_t dim, q_len, group, kv;
+    uint32_t rows_own, rows_all;     // rows of a key / value head: of one sequence, of all
+    uint32_t blocks_all, blocks_own; // the same in blocks of 32
+    uint32_t parts_all, parts_own;   // parts along the keys
+    uint32_t wg_all, units_all;      // prefix: workgroups; (head, part) pairs
+    uint32_t shared;                 // prefix tiles shared by a workgroup's four waves
+    uint32_t own_first;              // partial results of the prefix
+    uint32_t direct;                 // one part in all: it writes the result
+    float scale;                     // |scale| * log2(e), never 0
+    uint32_t flip;                   // sign bits to turn in the queries (scale below 0)
 };
 
-// One workgroup for one query: a thread for a key, then a thread for an element.
-template <typename T>
-__global__ __launch_bounds__(kThreads) void k_attn(const AttnArgs a) {
-    __shared__ float q[256], p[kThreads], red[kThreads];
-    __shared__ int64_t voff[kThreads];
-    const uint32_t tid = threadIdx.x, D = (uint32_t)a.q.dim[0];
-    const uint32_t h = blockIdx.x, j = blockIdx.y, b = blockIdx.z;
-    const uint32_t kvh = h / (uint32_t)(a.q.dim[1] / a.k.dim[2]);
-    const uint32_t row = a.rows ? (uint32_t)a.rows[b] : b;
-    int64_t own = 0;
-    if (row < a.table_rows) {
-        own = a.lens[row];
-        const int64_t room = (int64_t)a.slots * a.row_pages;
-        if (own < 0 || own > room) {
-            if (tid == 0) record_page_error(a.err);
-            own = own < 0 ? 0 : room;
-        }
-    } else if (tid == 0) {
-        record_page_error(a.err);
+// LDS image of a tile: rows of DP elements (dim rounded up), the 16-byte
+// chunks of a row XORed by a key of the row.  64 banks of 4 bytes serve 16
+// lanes x 16 bytes or 32 lanes x 8 bytes at once:
+//   keys    16 rows at one chunk: the key runs through the chunks of 256 bytes
+//           that 16 rows would otherwise share
+//   values  4 rows x 4 neighbouring chunks (the transposing read): the key
+//           moves groups of 4 chunks
+template <uint32_t DP>
+struct Geo {
+    static constexpr uint32_t cpr = DP / 8;                                   // chunks of a row
+    static constexpr uint32_t bits = cpr % 16 == 0 ? 4 : cpr % 8 == 0 ? 3 : 2;
+    static constexpr uint32_t period = 16u >> bits;                            // rows that already differ in their banks
+    static constexpr uint32_t tile_bytes = kTile * DP * 2;
+    static constexpr uint32_t own_bytes = kOwnTile * DP * 2;
+    static constexpr uint32_t ring_bytes = 4 * tile_bytes;                     // two stages of keys and values
+    static_assert(ring_bytes == kWaves * 2 * own_bytes, "a tile of keys and one of values for each wave");
+    static __device__ __forceinline__ uint32_t key_k(uint32_t row) { return (row / period) & ((1u << bits) - 1u); }
+    static __device__ __forceinline__ uint32_t key_v(uint32_t row) {
+        return bits == 4 ? (row & 3u) << 2 : bits == 3 ? ((row >> 1) & 1u) << 2 : 0u;
     }
-    own = own - (int64_t)a.q.dim[2] + 1 + j;
-    if (own < 0) own = 0;
-    const uint32_t total = a.prefix_len + (uint32_t)own;
-    const gbyte* qp = gptr(a.q.base) + h * a.q.stride[1] + j * a.q.stride[2] + b * a.q.stride[3];
-    if (tid < D) q[tid] = (float)((const ATT_GLOBAL T*)qp)[tid];
-    float top = -INFINITY, sum = 0.0f, acc = 0.0f;
-    for (uint32_t base = 0; base < total; base += kThreads) {
-        __syncthreads();
-        const uint32_t n = base + tid;
-        float s = -INFINITY;
-        voff[tid] = -1;
-        if (n < total) {
-            const uint32_t at = n < a.prefix_len ? n : n - a.prefix_len, r = n < a.prefix_len ? a.prefix_row : row;
-            const int32_t page = a.table[(uint64_t)r * a.pitch + at / a.slots];
-            if ((uint32_t)page < a.pages) {
-                const int64_t slot = at % a.slots;
-                const ATT_GLOBAL T* kp = (const ATT_GLOBAL T*)(gptr(a.k.base) + page * a.k.stride[3] +
-                                                               slot * a.k.stride[1] + kvh * a.k.stride[2]);
-                voff[tid] = page * a.v.stride[3] + slot * a.v.stride[1] + kvh * a.v.stride[2];
-                s = 0.0f;
-                for (uint32_t d = 0; d < D; ++d) s += q[d] * (float)kp[d];
-                s *= a.scale;
-            } else {
-                record_page_error(a.err);
-            }
-        }
-        red[tid] = s;
-        __syncthreads();
-        for (uint32_t w = kThreads / 2; w; w /= 2) {
-            if (tid < w) red[tid] = fmaxf(red[tid], red[tid + w]);
-            __syncthreads();
-        }
-        const float next = fmaxf(top, red[0]), at0 = next == -INFINITY ? 0.0f : next;
-        const float fade = expf(top - at0);
-        const float e = expf(s - at0);
-        p[tid] = e;
-        __syncthreads();
-        red[tid] = e;
-        __syncthreads();
-        for (uint32_t w = kThreads / 2; w; w /= 2) {
-            if (tid < w) red[tid] += red[tid + w];
-            __syncthreads();
-        }
-        sum = sum * fade + red[0];
-        acc *= fade;
-        top = next;
-        if (tid < D)
-            for (uint32_t i = 0; i < kThreads; ++i)
-                if (voff[i] >= 0) acc += p[i] * (float)((const ATT_GLOBAL T*)(gptr(a.v.base) + voff[i]))[tid];
-    }
-    if (tid < D) {
-        gbyte* op = gptr(a.o.base) + h * a.o.stride[1] + j * a.o.stride[2] + b * a.o.stride[3];
-        ((ATT_GLOBAL T*)op)[tid] = (T)(sum > 0.0f ? acc / sum : 0.0f);
-    }
-    if (tid == 0 && a.lse)
-        a.lse[((uint64_t)b * a.q.dim[2] + j) * a.q.dim[1] + h] = sum > 0.0f ? top + logf(sum) : -INFINITY;
+};
+
+// One asynchronous 16-byte copy per active lane; the caller waits on vmcnt.
+__device__ __forceinline__ void copy16(uint64_t src, uint32_t lds_group) {
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "{m0}"(lds_group) : "memory");
 }
 
-static uint64_t workspace(const View&, const View&, uint32_t, uint32_t) { return 16; }
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ uint64_t uniform64(uint64_t x) {
+    return (uint64_t)uniform((uint32_t)(x >> 32)) << 32 | uniform((uint32_t)x);
+}
+
+__device__ __forceinline__ uint32_t part_begin(uint32_t n, uint32_t part, uint32_t per) {
+    const uint64_t at = (uint64_t)part * per;
+    return at < n ? (uint32_t)at : n;
+}
+// Keys of one of `parts` parts of n, whole tiles.
+__device__ __forceinline__ uint32_t part_keys(uint32_t n, uint32_t parts, uint32_t tile) {
+    const uint32_t per = (n + parts - 1u) / parts;
+    return (per + tile - 1u) / tile * tile;
+}
+
+// The larger, and the sum, of a lane's value and that of the lane 32 further.
+struct Halves { float low, high; };
+__device__ __forceinline__ Halves halves(float x) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, x);
+    const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    const uint32_t low = r[0], high = r[1];               // bit_cast of r[1] itself would read r[0]
+    return {__builtin_bit_cast(float, low), __builtin_bit_cast(float, high)};
+}
+__device__ __forceinline__ float max_halves(float x) {
+    const Halves h = halves(x);
+    return fmaxf(h.low, h.high);
+}
+__device__ __forceinline__ float add_halves(float x) {
+    const Halves h = halves(x);
+    return h.low + h.high;
+}
+
+template <uint32_t DP>
+struct Shared {
+    uint8_t ring[Geo<DP>::ring_bytes];
+    int64_t koff[2 * kSegment];       // byte offset of each key's row in the pools, -1: not there
+    int64_t voff[2 * kSegment];
+    uint64_t there[2 * kSegment / 64];
+};
+
+// A wave's 32 queries and what it has summed for them.  Lane l: query l % 32,
+// half l / 32 of each group of 8 keys (scores) or 8 elements (result).
+template <typename T, uint32_t DP>
+struct Wave {
+    typedef typename Vec<T>::v8 v8;
+    typedef typename Vec<T>::v4 v4;
+    static constexpr uint32_t NK = DP / 16, NO = DP / 32;
+    v8 q[NK];
+    f32x16 o[NO];
+    float m, l;                      // largest score seen in powers of two (or below by kLazy at most), sum of weights
+
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (uint32_t i = 0; i < NO; ++i) o[i] = (f32x16)(0.0f);
+        m = -INFINITY;
+        l = 0.0f;
+    }
+
+    // The lane's query (row r of the head's rows; none past `rows`).
+    __device__ __forceinline__ void load(const AttnArgs& a, uint32_t head, uint32_t r, bool valid) {
+        const uint32_t lane = lane_id();
+        const uint32_t b = r / a.rows_own, in = r - b * a.rows_own, j = in / a.group, g = in - j * a.group;
+        const gbyte* p = gptr(a.q.base) + (int64_t)b * a.q.stride[3] + (int64_t)j * a.q.stride[2] +
+                         (int64_t)(head * a.group + g) * a.q.stride[1];
+#pragma unroll
+        for (uint32_t k = 0; k < NK; ++k) {
+            const uint32_t d = k * 16u + (lane / 32u) * 8u;
+            u32x4 x = (u32x4)(0u);
+            if (valid && d < a.dim) x = *(const ATT_GLOBAL u32x4*)(p + d * 2u) ^ a.flip;
+            q[k] = __builtin_bit_cast(v8, x);
+        }
+        clear();
+    }
+
+    // Scores of NB blocks of 32 keys.
+    template <uint32_t NB>
+    __device__ __forceinline__ void scores(const uint8_t* keys, f32x16 (&s)[NB]) const {
+        const uint32_t lane = lane_id(), row = lane % 32u, key = Geo<DP>::key_k(row);
+#pragma unroll
+        for (uint32_t n = 0; n < NB; ++n) s[n] = (f32x16)(0.0f);
+#pragma unroll
+        for (uint32_t k = 0; k < NK; ++k) {
+#pragma unroll
+            for (uint32_t n = 0; n < NB; ++n) {
+                const uint32_t c = (2u * k + lane / 32u) ^ key;
+                const v8 x = *reinterpret_cast<const v8*>(keys + (n * 32u + row) * (DP * 2u) + c * 16u);
+                s[n] = mfma(x, q[k], s[n]);
+            }
+        }
+    }
+
+    // Keys that this lane's query does not see, or that are not there, weigh
+    // nothing.  `limit` counts from the tile's first key.
+    template <uint32_t NB>
+    __device__ __forceinline__ static void mask(f32x16 (&s)[NB], int32_t limit, uint64_t there) {
+        const uint32_t hh = lane_id() / 32u;
+#pragma unroll
+        for (uint32_t n = 0; n < NB; ++n)
+#pragma unroll
+            for (uint32_t i = 0; i < 16; ++i) {
+                const uint32_t key = n * 32u + 8u * (i / 4u) + 4u * hh + i % 4u;
+                if ((int32_t)key >= limit || !(there >> key & 1u)) s[n][i] = -INFINITY;
+            }
+    }
+
+    // Weights of the scores, in place.  The sums are only rescaled when a
+    // score passes the largest of before by 2^kLazy; weights then stay below
+    // 2^kLazy, which both types hold.
+    template <uint32_t NB>
+    __device__ __forceinline__ void weights(const AttnArgs& a, f32x16 (&s)[NB]) {
+        float top = s[0][0];
+#pragma unroll
+        for (uint32_t n = 0; n < NB; ++n)
+#pragma unroll
+            for (uint32_t i = 0; i < 16; ++i) top = fmaxf(top, s[n][i]);
+        top = max_halves(top) * a.scale;
+        if (__any(top > m + kLazy)) {
+            const float next = fmaxf(m, top), fade = next == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - next);
+            m = next;
+            l *= fade;
+#pragma unroll
+            for (uint32_t i = 0; i < NO; ++i) o[i] *= fade;
+        }
+        const float at = m == -INFINITY ? 0.0f : m;
+        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (uint32_t n = 0; n < NB; ++n)
+#pragma unroll
+            for (uint32_t i = 0; i < 16; ++i) {
+                s[n][i] = __builtin_amdgcn_exp2f(fmaf(s[n][i], a.scale, -at));
+                sum[i % 4u] += s[n][i];
+            }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    }
+
+    // o += values^T x weights.
+    template <uint32_t NB>
+    __device__ __forceinline__ void values(const uint8_t* vals, const f32x16 (&p)[NB]) {
+        const uint32_t lane = lane_id(), i = lane % 16u;
+        const uint32_t row = 4u * (lane / 32u) + i / 4u;                  // of 4 x 16-element pieces
+        const uint32_t c0 = 2u * ((lane / 16u) & 1u) + (i % 4u) / 2u;
+        const uint8_t* at = vals + row * (DP * 2u) + 8u * (i & 1u);
+        const uint32_t key = Geo<DP>::key_v(row);
+#pragma unroll
+        for (uint32_t n = 0; n < NB; ++n)
+#pragma unroll
+            for (uint32_t t = 0; t < 2; ++t) {
+                v8 w;
+#pragma unroll
+                for (uint32_t e = 0; e < 8; ++e) w[e] = (T)p[n][8u * t + e];
+#pragma unroll
+                for (uint32_t b = 0; b < NO; ++b) {
+                    const uint8_t* x = at + (n * 32u + t * 16u) * (DP * 2u) + ((4u * b + c0) ^ key) * 16u;
+                    union { s16x4 h[2]; v8 v; } u;
+                    u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)x);
+                    u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(x + 8u * DP * 2u));
+                    o[b] = mfma(u.v, w, o[b]);
+                }
+            }
+    }
+
+    // Whether a tile of 32 keys holds infinities or NaN in the values of keys
+    // [from, to), and those elements become 0.
+    __device__ __forceinline__ static bool not_finite(uint16_t x) { return (x & Vec<T>::kExp) == Vec<T>::kExp; }
+    template <bool CLEAR>
+    __device__ __forceinline__ static bool odd_values(uint8_t* vals, uint32_t from, uint32_t to) {
+        bool odd = false;
+        for (uint32_t i = lane_id(); i < kOwnTile * Geo<DP>::cpr; i += 64u) {
+            const uint32_t row = i / Geo<DP>::cpr;
+            if (row < from || row >= to) continue;
+            union { u32x4 v; uint16_t e[8]; } x;
+            x.v = *reinterpret_cast<const u32x4*>(vals + i * 16u);
+#pragma unroll
+            for (uint32_t e = 0; e < 8; ++e)
+                if (not_finite(x.e[e])) {
+                    odd = true;
+                    x.e[e] = 0;
+                }
+            if (CLEAR) *reinterpret_cast<u32x4*>(vals + i * 16u) = x.v;
+        }
+        return __any(odd);
+    }
+
+    // Keys that some queries of the wave see and others do not: an infinity or
+    // a NaN among their values must not meet the weight 0 of the latter.  Such
+    // elements are added here to the queries that see them, and are 0 for the
+    // matrix product.
+    __device__ __forceinline__ void ragged_values(uint8_t* vals, const f32x16 (&p)[1], int32_t limit, uint32_t from,
+                                                  uint32_t to) {
+        if (!odd_values<false>(vals, from, to)) return;
+        const uint32_t hh = lane_id() / 32u;
+        for (uint32_t key = from; key < to; ++key) {
+            const uint32_t at = 4u * (key / 8u) + key % 4u;
+            float x = 0.0f;
+#pragma unroll
+            for (uint32_t i = 0; i < 16; ++i)
+                if (i == at && (key >> 2 & 1u) == hh) x = p[0][i];
+            x = (float)(T)add_halves(x);
+            const uint8_t* row = vals + key * (DP * 2u) + 8u * hh;
+#pragma unroll
+            for (uint32_t f = 0; f < DP / 8u; ++f) {
+                const uint64_t bits = *reinterpret_cast<const uint64_t*>(row + (f ^ Geo<DP>::key_v(key)) * 16u);
+#pragma unroll
+                for (uint32_t e = 0; e < 4; ++e) {
+                    const uint16_t h = (uint16_t)(bits >> (16u * e));
+                    if (not_finite(h) && (int32_t)key < limit)
+                        o[f / 4u][4u * (f % 4u) + e] += x * (float)__builtin_bit_cast(T, h);
+                }
+            }
+        }
+        odd_values<true>(vals, from, to);
+    }
+
+    // Sum of the weights over both halves.
+    __device__ __forceinline__ float total() const { return add_halves(l); }
+};
+
+// Where keys base .. base + kSegment * count of a row lie.  Thread after
+// thread a key; what is not a page of the pool is recorded and left out.
+__device__ __forceinline__ int32_t page_of_key(const AttnArgs& a, uint32_t row, uint32_t key, uint32_t end) {
+    if (key >= end) return -1;
+    return *(const ATT_GLOBAL int32_t*)(gptr(a.table) + ((uint64_t)row * a.pitch + key / a.slots) * 4u);
+}
+
+template <uint32_t DP>
+__device__ __forceinline__ void place_key(const AttnArgs& a, uint32_t head, uint32_t key, uint32_t end, int32_t page,
+                                          Shared<DP>& sh, uint32_t at) {
+    const bool ok = key < end && (uint32_t)page < a.pages;
+    if (key < end && !ok) record_page_error(a.err);
+    const int64_t slot = key % a.slots;
+    sh.koff[at] = ok ? page * a.k.stride[3] + slot * a.k.stride[1] + (int64_t)head * a.k.stride[2] : -1;
+    sh.voff[at] = ok ? page * a.v.stride[3] + slot * a.v.stride[1] + (int64_t)head * a.v.stride[2] : -1;
+    const uint64_t mask = __ballot(ok);
+    if (at % 64u == 0) sh.there[at / 64u] = mask;
+}
+
+// Issue the copies of groups [first, first + N) x STEP of a tile: chunk i of
+// 64 * group + lane is row i / cpr; the row's offset says where it lies.
+// Rows that are not there stay as they are (VALUES: become 0, so that a weight
+// of 0 meets no NaN).
+template <uint32_t DP, uint32_t N, uint32_t STEP, bool VALUES>
+__device__ __forceinline__ void copy_rows(const AttnArgs& a, uint64_t base, const int64_t* off, uint32_t first,
+                                          uint8_t* dst, bool whole) {
+    const uint32_t lane = lane_id();
+    const uint32_t lds = uniform(lds_addr_of(dst));
+#pragma unroll
+    for (uint32_t n = 0; n < N; ++n) {
+        const uint32_t g = first + n * STEP, i = g * 64u + lane, row = i / Geo<DP>::cpr, p = i - row * Geo<DP>::cpr;
+        const uint32_t c = p ^ (VALUES ? Geo<DP>::key_v(row) : Geo<DP>::key_k(row));
+        const int64_t at = off[row];
+        const uint64_t src = base + (uint64_t)at + c * 16u;
+        if (whole) {
+            copy16(src, lds + g * 1024u);
+        } else if (c * 8u < a.dim) {
+            if (at >= 0) copy16(src, lds + g * 1024u);
+            else if (VALUES) *reinterpret_cast<u32x4*>(dst + i * 16u) = (u32x4)(0u);
+        }
+    }
+}
+
+// ---- partial results -------------------------------------------------------------
+
+// A block of 32 rows leaves its (m, l) by row and its sums as the lanes hold
+// them: piece f = 4 * b + g of lane l is elements 32 b + 8 g + 4 (l / 32) + 0..3
+// of row l % 32.
+template <uint32_t DP>
+__device__ __forceinline__ f32x4* part_at(const AttnArgs& a, uint64_t block) {
+    return a.part_o + block * (DP / 8u * 64u);
+}
+
+template <typename T>
+__device__ __forceinline__ void store_result(const AttnArgs& a, uint32_t head, uint32_t r, uint32_t d, f32x4 x) {
+    const uint32_t b = r / a.rows_own, in = r - b * a.rows_own, j = in / a.group, g = in - j * a.group;
+    gbyte* p = gptr(a.o.base) + (int64_t)b * a.o.stride[3] + (int64_t)j * a.o.stride[2] +
+               (int64_t)(head * a.group + g) * a.o.stride[1];
+    typename Vec<T>::v4 y;
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i) y[i] = (T)x[i];
+    *(ATT_GLOBAL uint64_t*)(p + d * 2u) = __builtin_bit_cast(uint64_t, y);
+}
+
+__device__ __forceinline__ void store_lse(const AttnArgs& a, uint32_t head, uint32_t r, float m, float l) {
+    const uint32_t b = r / a.rows_own, in = r - b * a.rows_own, j = in / a.group, g = in - j * a.group;
+    a.lse[((uint64_t)b * a.q_len + j) * ((uint64_t)a.kv * a.group) + head * a.group + g] =
+        l == 0.0f ? -INFINITY : m * 0.6931471805599453f + logf(l);
+}
+
+// ---- the prefix, shared -----------------------------------------------------------
+
+// Four waves of 32 rows each over the tiles of one part of the prefix.  Two
+// stages: while a tile is used the next is on its way; a barrier a tile.
+template <typename T, uint32_t DP>
+__device__ __forceinline__ void shared_part(const AttnArgs& a, Shared<DP>& sh, uint32_t head, uint32_t part,
+                                            uint32_t block) {
+    const uint32_t tid = threadIdx.x, wave = uniform(tid / 64u);
+    const uint32_t per = part_keys(a.prefix_len, a.parts_all, kTile);
+    const uint32_t k0 = part_begin(a.prefix_len, part, per), k1 = part_begin(a.prefix_len, part + 1u, per);
+    const uint32_t tiles = (k1 - k0 + kTile - 1u) / kTile;
+    const uint32_t r = block * kWgRows + wave * kRows + lane_id() % 32u;
+    const bool used = block * kWgRows + wave * kRows < a.rows_all;
+    constexpr uint32_t SEG = kSegment / kTile;                            // tiles of a segment
+    constexpr uint32_t NG = Geo<DP>::cpr / kWaves;                        // groups a wave copies of a tile's keys
+    Wave<T, DP> w;
+    w.load(a, head, r, r < a.rows_all);
+    int32_t page = page_of_key(a, a.prefix_row, k0 + tid, k1);
+    place_key(a, head, k0 + tid, k1, page, sh, tid);
+    if (a.dim < DP)                                                       // padded elements of the keys are 0
+        for (uint32_t i = tid * 16u; i < Geo<DP>::ring_bytes; i += kThreads * 16u)
+            *reinterpret_cast<u32x4*>(sh.ring + i) = (u32x4)(0u);
+    __syncthreads();
+    auto issue = [&](uint32_t t) {
+        uint8_t* dst = sh.ring + (t & 1u) * 2u * Geo<DP>::tile_bytes;
+        const uint32_t at = t % (2u * SEG);
+        const bool whole = uniform64(sh.there[at]) == ~0ull && a.dim == DP;
+        copy_rows<DP, NG, kWaves, false>(a, a.k.base, sh.koff + at * kTile, wave, dst, whole);
+        copy_rows<DP, NG, kWaves, true>(a, a.v.base, sh.voff + at * kTile, wave, dst + Geo<DP>::tile_bytes, whole);
+    };
+    if (tiles) issue(0);
+    for (uint32_t t = 0; t < tiles; ++t) {
+        wait_vmcnt<0>();
+        wait_lgkm0();
+        wg_barrier();
+        const uint32_t seg = t / SEG, next = k0 + (seg + 1u) * kSegment + tid;
+        if (t % SEG == SEG / 2)                                            // read from the next segment's first copy on
+            place_key(a, head, next, k1, page, sh, ((seg + 1u) & 1u) * kSegment + tid);
+        const uint64_t there = uniform64(sh.there[t % (2u * SEG)]);
+        if (t + 1u < tiles) issue(t + 1u);
+        if (t % SEG == 0) page = page_of_key(a, a.prefix_row, next, k1);
+        if (used) {
+            const uint8_t* keys = sh.ring + (t & 1u) * 2u * Geo<DP>::tile_bytes;
+            f32x16 s[2];
+            w.scores(keys, s);
+            if (there != ~0ull) w.mask(s, kTile, there);
+            w.weights(a, s);
+            w.values(keys + Geo<DP>::tile_bytes, s);
+        }
+    }
+    if (!used) return;
+    const uint32_t lane = lane_id();
+    const uint64_t at = ((uint64_t)head * a.parts_all + part) * a.blocks_all + block * kWaves + wave;
+    f32x4* out = part_at<DP>(a, at);
+#pragma unroll
+    for (uint32_t b = 0; b < DP / 32u; ++b)
+#pragma unroll
+        for (uint32_t g = 0; g < 4; ++g)
+            out[(4u * b + g) * 64u + lane] =
+                f32x4{w.o[b][4u * g], w.o[b][4u * g + 1u], w.o[b][4u * g + 2u], w.o[b][4u * g + 3u]};
+    const float l = w.total();
+    if (lane < 32u) a.part_ml[at * 32u + lane] = make_float2(w.m, l);
+}
+
+// ---- a wave's own tiles -------------------------------------------------------------
+
+// 32 rows (of one sequence, or of a prefix with few) over keys [k0, k1) of a
+// table row: the waves take tiles of 32 keys in turn, each in LDS of its own,
+// so that no barrier is needed: keys are fetched anew while the weights are
+// worked out, values while the next scores are.  At the end the waves' sums
+// are joined in LDS.
+struct OwnJob {
+    uint32_t head, row, k0, k1;      // keys [k0, k1) of a table row
+    uint32_t first, count;           // rows of the head
+    int64_t len;                     // tokens of the sequence; its query j sees len - q_len + 1 + j of them
+    bool all;                        // every query sees every key
+    uint64_t block;                  // of the partial results
+};
+
+template <typename T, uint32_t DP>
+__device__ __forceinline__ void own_part(const AttnArgs& a, Shared<DP>& sh, const OwnJob& job) {
+    const uint32_t tid = threadIdx.x, wave = uniform(tid / 64u), lane = lane_id(), n32 = lane % 32u;
+    const uint32_t r = job.first + n32;
+    const bool valid = n32 < job.count;
+    constexpr uint32_t NP = Geo<DP>::cpr / 2;                             // copies of a tile's keys
+    constexpr uint32_t SEG = 2 * kSegment;
+    Wave<T, DP> w;
+    w.load(a, job.head, r, valid);
+    // keys below `common` are seen by all of the rows, those below `limit` by this lane's
+    const int64_t first_sees = job.len - a.q_len + 1;
+    const uint32_t common = job.all ? job.k1 : first_sees < 0 ? 0u : (uint32_t)first_sees;
+    const int64_t sees = job.all ? (int64_t)job.k1 : first_sees + (r % a.rows_own) / a.group;
+    uint8_t* const keys = sh.ring + wave * 2u * Geo<DP>::own_bytes;
+    uint8_t* const vals = keys + Geo<DP>::own_bytes;
+    if (a.dim < DP)                                                       // padded elements of the keys are 0
+        for (uint32_t i = lane * 16u; i < 2u * Geo<DP>::own_bytes; i += 1024u)
+            *reinterpret_cast<u32x4*>(keys + i) = (u32x4)(0u);
+    for (uint32_t base = job.k0; base < job.k1; base += SEG) {
+        if (base != job.k0) __syncthreads();                              // the segment before is used up
+        for (uint32_t at = tid; at < SEG; at += kThreads)
+            place_key(a, job.head, base + at, job.k1, page_of_key(a, job.row, base + at, job.k1), sh, at);
+        __syncthreads();
+        const uint32_t left = job.k1 - base, n = left < SEG ? left : SEG, tiles = (n + kOwnTile - 1u) / kOwnTile;
+        auto mask_of = [&](uint32_t t) { return (uint32_t)(uniform64(sh.there[t / 2u]) >> (32u * (t & 1u))); };
+        auto issue_k = [&](uint32_t t) {
+            copy_rows<DP, NP, 1, false>(a, a.k.base, sh.koff + t * kOwnTile, 0, keys, mask_of(t) == ~0u && a.dim == DP);
+        };
+        auto issue_v = [&](uint32_t t) {
+            copy_rows<DP, NP, 1, true>(a, a.v.base, sh.voff + t * kOwnTile, 0, vals, mask_of(t) == ~0u && a.dim == DP);
+        };
+        if (wave < tiles) {
+            issue_k(wave);
+            issue_v(wave);
+        }
+        for (uint32_t t = wave; t < tiles; t += kWaves) {
+            const uint32_t bits = mask_of(t), next = t + kWaves, k = base + t * kOwnTile;
+            // a tile with rows that are not there may take fewer copies than NP
+            if (bits == ~0u) wait_vmcnt<NP>();
+            else wait_vmcnt<0>();
+            f32x16 s[1];
+            w.scores(keys, s);
+            wait_lgkm0();
+            bool counted = false;
+            if (next < tiles) {
+                issue_k(next);
+                counted = mask_of(next) == ~0u;
+            }
+            const int64_t lim = sees - k;
+            const int32_t limit = lim < 0 ? 0 : lim > (int64_t)kOwnTile ? (int32_t)kOwnTile : (int32_t)lim;
+            const bool ragged = k + kOwnTile > common;
+            if (ragged || bits != ~0u) w.mask(s, limit, bits);
+            w.weights(a, s);
+            if (counted) wait_vmcnt<NP>();
+            else wait_vmcnt<0>();
+            if (ragged && a.q_len > 1u)
+                w.ragged_values(vals, s, valid ? limit : 0, common > k ? common - k : 0u,
+                                job.k1 - k < kOwnTile ? job.k1 - k : kOwnTile);
+            w.values(vals, s);
+            wait_lgkm0();
+            if (next < tiles) issue_v(next);
+        }
+    }
+    // join the waves
+    constexpr uint32_t NF = DP / 8u;
+    __syncthreads();
+    float2* const ml = reinterpret_cast<float2*>(sh.koff);
+    f32x4* const sums = reinterpret_cast<f32x4*>(sh.ring);
+    const uint32_t tiles = (job.k1 - job.k0 + kOwnTile - 1u) / kOwnTile, busy = tiles < kWaves ? tiles : kWaves;
+    const float total = w.total();
+    if (lane < 32u) ml[wave * 32u + lane] = make_float2(w.m, total);
+    __syncthreads();
+    float m = -INFINITY, l = 0.0f;
+    for (uint32_t i = 0; i < busy; ++i) m = fmaxf(m, ml[i * 32u + n32].x);
+    const float at = m == -INFINITY ? 0.0f : m;
+    for (uint32_t i = 0; i < busy; ++i) l += ml[i * 32u + n32].y * __builtin_amdgcn_exp2f(ml[i * 32u + n32].x - at);
+    if (wave < busy) {
+        const float fade = __builtin_amdgcn_exp2f(w.m - at);
+#pragma unroll
+        for (uint32_t b = 0; b < DP / 32u; ++b)
+#pragma unroll
+            for (uint32_t g = 0; g < 4; ++g)
+                sums[(wave * NF + 4u * b + g) * 64u + lane] =
+                    f32x4{w.o[b][4u * g], w.o[b][4u * g + 1u], w.o[b][4u * g + 2u], w.o[b][4u * g + 3u]} * fade;
+    }
+    __syncthreads();
+    f32x4* const out = part_at<DP>(a, job.block);
+    for (uint32_t f = wave; f < NF; f += kWaves) {
+        f32x4 x = (f32x4)(0.0f);
+        for (uint32_t i = 0; i < busy; ++i) x += sums[(i * NF + f) * 64u + lane];
+        if (!valid) continue;
+        const uint32_t d = 8u * f + 4u * (lane / 32u);
+        if (!a.direct) out[f * 64u + lane] = x;
+        else if (d < a.dim) store_result<T>(a, job.head, r, d, l == 0.0f ? (f32x4)(0.0f) : x / l);
+    }
+    if (wave == 0 && valid && lane < 32u) {
+        if (!a.direct) a.part_ml[job.block * 32u + lane] = make_float2(m, l);
+        else if (a.lse) store_lse(a, job.head, r, m, l);
+    }
+}
+
+template <typename T, uint32_t DP>
+__global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_attn(const AttnArgs a) {
+    __shared__ __attribute__((aligned(1024))) Shared<DP> sh;
+    uint32_t id = blockIdx.x;
+    OwnJob job;
+    if (id < a.wg_all) {
+        // Workgroups go to the 8 XCDs in turn: those that read the same part of
+        // the prefix, one for each block of rows, meet in one XCD's L2.
+        const uint32_t rows = a.shared ? kWgRows : kRows, blocks = (a.rows_all + rows - 1u) / rows;
+        const uint32_t x = id % 8u, y = id / 8u, unit = x + 8u * (y / blocks), block = y % blocks;
+        if (unit >= a.units_all) return;
+        const uint32_t head = unit % a.kv, part = unit / a.kv;
+        if (a.shared) return shared_part<T, DP>(a, sh, head, part, block);
+        const uint32_t per = part_keys(a.prefix_len, a.parts_all, kOwnTile), left = a.rows_all - block * kRows;
+        job.head = head;
+        job.row = a.prefix_row;
+        job.k0 = part_begin(a.prefix_len, part, per);
+        job.k1 = part_begin(a.prefix_len, part + 1u, per);
+        job.first = block * kRows;
+        job.count = left < kRows ? left : kRows;
+        job.len = 0;
+        job.all = true;
+        job.block = ((uint64_t)head * a.parts_all + part) * a.blocks_all + block;
+    } else {
+        id -= a.wg_all;
+        job.head = id % a.kv;
+        id /= a.kv;
+        const uint32_t block = id % a.blocks_own;
+        id /= a.blocks_own;
+        const uint32_t part = id % a.parts_own, b = id / a.parts_own;
+        job.row = a.rows ? (uint32_t)a.rows[b] : b;
+        job.len = 0;
+        if (job.row < a.table_rows) {
+            const int64_t room = (int64_t)a.slots * a.row_pages, len = a.lens[job.row];
+            job.len = len < 0 ? 0 : len > room ? room : len;
+            if (job.len != len && threadIdx.x == 0) record_page_error(a.err);
+        } else if (threadIdx.x == 0) {
+            record_page_error(a.err);
+        }
+        const uint32_t per = part_keys((uint32_t)job.len, a.parts_own, kOwnTile), left = a.rows_own - block * kRows;
+        job.k0 = part_begin((uint32_t)job.len, part, per);
+        job.k1 = part_begin((uint32_t)job.len, part + 1u, per);
+        job.first = b * a.rows_own + block * kRows;
+        job.count = left < kRows ? left : kRows;
+        job.all = false;
+        job.block = a.own_first + (((uint64_t)b * a.kv + job.head) * a.blocks_own + block) * a.parts_own + part;
+    }
+    own_part<T, DP>(a, sh, job);
+}
+
+// The parts of 32 rows joined: blockIdx.x is the block of a head's rows, and
+// each wave takes one piece of 8 elements of them.
+template <typename T, uint32_t DP>
+__global__ __launch_bounds__(kThreads) void k_attn_join(const AttnArgs a) {
+    constexpr uint32_t U = 8;                                             // parts in flight
+    const uint32_t lane = lane_id(), n32 = lane % 32u, hh = lane / 32u;
+    const uint32_t head = blockIdx.x / a.blocks_all, block = blockIdx.x - head * a.blocks_all;
+    const uint32_t f = blockIdx.y * kWaves + threadIdx.x / 64u;
+    const uint32_t d = 8u * f + 4u * hh;
+    if (8u * f >= a.dim) return;
+    uint32_t r = block * kRows + n32;
+    const bool valid = r < a.rows_all;
+    if (!valid) r = a.rows_all - 1u;
+    const uint32_t b = r / a.rows_own, in = r - b * a.rows_own;
+    const uint64_t own = a.own_first + (((uint64_t)b * a.kv + head) * a.blocks_own + in / kRows) * a.parts_own;
+    const uint32_t parts = a.parts_all + a.parts_own;
+    f32x4 acc = (f32x4)(0.0f);
+    float m = -INFINITY, l = 0.0f;
+    for (uint32_t i0 = 0; i0 < parts; i0 += U) {
+        float2 ml[U];
+        f32x4 x[U];
+#pragma unroll
+        for (uint32_t u = 0; u < U; ++u) {
+            const uint32_t i = i0 + u;
+            ml[u] = make_float2(-INFINITY, 0.0f);
+            x[u] = (f32x4)(0.0f);
+            if (i >= parts) continue;
+            const bool all = i < a.parts_all;
+            const uint64_t at = all ? ((uint64_t)head * a.parts_all + i) * a.blocks_all + block : own + (i - a.parts_all);
+            const uint32_t slot = all ? n32 : in % kRows;
+            ml[u] = a.part_ml[at * 32u + slot];
+            x[u] = part_at<DP>(a, at)[f * 64u + hh * 32u + slot];
+        }
+        float next = m;
+#pragma unroll
+        for (uint32_t u = 0; u < U; ++u) next = fmaxf(next, ml[u].x);
+        if (next == -INFINITY) continue;
+        const float fade = __builtin_amdgcn_exp2f(m - next);
+        acc *= fade;
+        l *= fade;
+        m = next;
+#pragma unroll
+        for (uint32_t u = 0; u < U; ++u) {
+            if (ml[u].x == -INFINITY) continue;                           // a part that saw no key left no sums
+            const float w = __builtin_amdgcn_exp2f(ml[u].x - m);
+            l += w * ml[u].y;
+            acc += x[u] * w;
+        }
+    }
+    if (!valid) return;
+    if (d < a.dim) store_result<T>(a, head, r, d, l == 0.0f ? (f32x4)(0.0f) : acc / l);
+    if (f == 0 && hh == 0 && a.lse) store_lse(a, head, r, m, l);
+}
+
+// ---- host ---------------------------------------------------------------------------
 
 // Shapes of the queries against a pool.
 static bool shapes_fit(const View& q, const View& k) {
     return q.dim[0] == k.dim[0] && q.dim[0] % 8 == 0 && q.dim[0] <= 256 && q.dim[1] % k.dim[2] == 0 &&
            q.dim[1] <= 65535 && q.dim[2] <= 65535 && q.dim[3] <= 65535;
+}
+
+static uint32_t padded_dim(uint32_t dim) {
+    return dim <= 64 ? 64 : dim <= 96 ? 96 : dim <= 128 ? 128 : dim <= 192 ? 192 : 256;
+}
+
+static uint64_t ceil_div(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
+
+// How the work is cut: fills the fields of `a` that follow from the shapes
+// alone and returns the workspace's bytes, 0 if the rows or workgroups are too
+// many to count in 31 bits.
+static uint64_t plan(AttnArgs* a, uint64_t* groups_out) {
+    constexpr uint64_t cus = 256;
+    const uint64_t batch = (uint64_t)a->q.dim[3];
+    const uint32_t dp = padded_dim((uint32_t)a->q.dim[0]);
+    const uint64_t room = dp <= 128 ? 2 * cus : cus;                       // workgroups that run at once
+    a->dim = (uint32_t)a->q.dim[0];
+    a->q_len = (uint32_t)a->q.dim[2];
+    a->kv = (uint32_t)a->k.dim[2];
+    a->group = (uint32_t)a->q.dim[1] / a->kv;
+    const uint64_t rows_own = (uint64_t)a->q_len * a->group, rows_all = rows_own * batch;
+    if (rows_all > 0x7FFFFFFFull) return 0;
+    a->rows_own = (uint32_t)rows_own;
+    a->rows_all = (uint32_t)rows_all;
+    a->blocks_own = (uint32_t)ceil_div(rows_own, kRows);
+    a->blocks_all = (uint32_t)ceil_div(rows_all, kRows);
+    a->shared = rows_all > 2 * kRows;
+    const uint64_t blocks = ceil_div(rows_all, a->shared ? kWgRows : kRows);
+    a->parts_all = 0;
+    if (a->prefix_len) {
+        const uint64_t most = ceil_div(a->prefix_len, 128), want = cus / (a->kv * blocks);
+        a->parts_all = (uint32_t)(want < 1 ? 1 : want < most ? want : most);
+    }
+    a->units_all = a->kv * a->parts_all;
+    const uint64_t wg_all = ceil_div(a->units_all, 8) * 8 * blocks;
+    const uint64_t jobs = batch * a->kv * a->blocks_own;
+    const uint64_t most = ceil_div(a->hint ? a->hint : 1, 256), want = room / jobs;
+    a->parts_own = (uint32_t)(want < 1 ? 1 : want < most ? want : most);
+    a->direct = a->parts_all == 0 && a->parts_own == 1;
+    const uint64_t first = (uint64_t)a->units_all * a->blocks_all, own = jobs * a->parts_own;
+    const uint64_t groups = wg_all + own;
+    if (groups > 0x7FFFFFFFull || first > 0x7FFFFFFFull || (uint64_t)a->kv * a->blocks_all > 0x7FFFFFFFull) return 0;
+    a->wg_all = (uint32_t)wg_all;
+    a->own_first = (uint32_t)first;
+    *groups_out = groups;
+    const uint64_t parts = first + own;
+    a->part_ml = reinterpret_cast<float2*>(parts * dp * 32 * 4);           // behind the sums
+    return parts * (dp * 32 * 4 + 32 * 8) + 16;
+}
+
+template <typename T, uint32_t DP>
+static tmap_status launch(const AttnArgs& a, uint32_t groups, hipStream_t stream) {
+    hipLaunchKernelGGL((k_attn<T, DP>), dim3(groups), dim3(kThreads), 0, stream, a);
+    tmap_status st = check_launch("attn_shared_prefix");
+    if (st || a.direct) return st;
+    const dim3 grid(a.kv * a.blocks_all, (a.dim + 31u) / 32u);
+    hipLaunchKernelGGL((k_attn_join<T, DP>), grid, dim3(kThreads), 0, stream, a);
+    return check_launch("attn_shared_prefix");
+}
+
+template <typename T>
+static tmap_status launch_dim(const AttnArgs& a, uint32_t groups, hipStream_t stream) {
+    switch (padded_dim(a.dim)) {
+    case 64: return launch<T, 64>(a, groups, stream);
+    case 96: return launch<T, 96>(a, groups, stream);
+    case 128: return launch<T, 128>(a, groups, stream);
+    case 192: return launch<T, 192>(a, groups, stream);
+    default: return launch<T, 256>(a, groups, stream);
+    }
 }
 
 }  // namespace att
@@ -116,10 +767,14 @@ using namespace att;
 
 extern "C" uint64_t attn_workspace(const tmap_t* q, const tmap_t* k_pool, uint32_t prefix_len,
                                    uint32_t suffix_hint) {
-    View vq, vk;
+    AttnArgs a;
+    std::memset(&a, 0, sizeof(a));
     int32_t tq, tk;
-    if (view_of(q, 4, &vq, &tq) || view_of(k_pool, 4, &vk, &tk) || !shapes_fit(vq, vk)) return 0;
-    return workspace(vq, vk, prefix_len, suffix_hint);
+    if (view_of(q, 4, &a.q, &tq) || view_of(k_pool, 4, &a.k, &tk) || !shapes_fit(a.q, a.k)) return 0;
+    a.prefix_len = prefix_len;
+    a.hint = suffix_hint;
+    uint64_t groups;
+    return plan(&a, &groups);
 }
 
 extern "C" tmap_status attn_shared_prefix(const tmap_t* q, const tmap_t* k_pool, const tmap_t* v_pool,
@@ -144,7 +799,13 @@ extern "C" tmap_status attn_shared_prefix(const tmap_t* q, const tmap_t* k_pool,
     if (prefix_len && (prefix_row >= pt->rows || prefix_len > (uint64_t)pt->slots * pt->row_pages))
         return TMAP_ERR_UNSUPPORTED;
     if (reinterpret_cast<uintptr_t>(d_ws) % 16 != 0) return TMAP_ERR_ALIGN;
-    if (ws_bytes < workspace(a.q, a.k, prefix_len, suffix_hint)) return TMAP_ERR_UNSUPPORTED;
+    a.prefix_len = prefix_len;
+    a.hint = suffix_hint;
+    uint64_t groups = 0;
+    const uint64_t need = plan(&a, &groups);
+    if (need == 0 || ws_bytes < need) return TMAP_ERR_UNSUPPORTED;
+    a.part_o = static_cast<f32x4*>(d_ws);
+    a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(d_ws) + reinterpret_cast<uintptr_t>(a.part_ml));
     a.table = pt->d_table;
     a.lens = pt->d_lens;
     a.rows = d_rows;
@@ -154,13 +815,15 @@ extern "C" tmap_status attn_shared_prefix(const tmap_t* q, const tmap_t* k_pool,
     a.pages = pt->pages;
     a.slots = pt->slots;
     a.prefix_row = prefix_row;
-    a.prefix_len = prefix_len;
-    a.scale = scale;
+    // Scores are kept in powers of two.  A negative scale turns the queries
+    // around; 0 becomes a factor that no score of the types survives, so that
+    // masked scores stay at -inf.
+    a.scale = std::fabs(scale) * 1.4426950408889634f;
+    if (a.scale < 1e-37f) a.scale = 1e-37f;
+    a.flip = scale < 0 ? 0x80008000u : 0u;
     a.lse = d_lse;
     st = device_error_word(&a.err);
     if (st) return st;
-    const dim3 grid((uint32_t)a.q.dim[1], (uint32_t)a.q.dim[2], (uint32_t)a.q.dim[3]);
-    if (tq == TMAP_F16) hipLaunchKernelGGL(k_attn<_Float16>, grid, dim3(kThreads), 0, as_stream(stream), a);
-    else hipLaunchKernelGGL(k_attn<__bf16>, grid, dim3(kThreads), 0, as_stream(stream), a);
-    return check_launch("attn_shared_prefix");
+    if (tq == TMAP_F16) return launch_dim<_Float16>(a, (uint32_t)groups, as_stream(stream));
+    return launch_dim<__bf16>(a, (uint32_t)groups, as_stream(stream));
 }
