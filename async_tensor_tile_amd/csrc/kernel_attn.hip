@@ -21,6 +21,8 @@
 
 #include <cmath>
 #include <cstring>
+#include <type_traits>
+#include <utility>
 
 #include "cache_util.hpp"
 
@@ -39,6 +41,15 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+template <typename F, int... I>
+__device__ __forceinline__ void static_for_impl(F& f, std::integer_sequence<int, I...>) {
+    (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void static_for(F&& f) {
+    static_for_impl(f, std::make_integer_sequence<int, N>{});
+}
 
 template <typename T>
 struct Vec;
@@ -85,6 +96,24 @@ struct AttnArgs {
     float scale;                     // |scale| * log2(e), never 0
     uint32_t flip;                   // sign bits to turn in the queries (scale below 0)
 };
+
+// The arguments where the launch put them.  A long loop that reads them
+// through `fresh` loads them again where it uses them instead of keeping all
+// of them in scalar registers, which are too few.
+typedef __attribute__((address_space(4))) const AttnArgs cargs;
+__device__ __forceinline__ cargs& kernel_args() { return *(cargs*)__builtin_amdgcn_kernarg_segment_ptr(); }
+__device__ __forceinline__ cargs& fresh() {
+    cargs* p = &kernel_args();
+    asm volatile("" : "+s"(p));
+    return *p;
+}
+
+// A value at an address that is the same for the whole workgroup and that no
+// kernel writes meanwhile, through the scalar cache: past the queue of the
+// vector loads and copies in flight.
+__device__ __forceinline__ int32_t scalar_load(const int32_t* p, uint64_t i) {
+    return ((__attribute__((address_space(4))) const int32_t*)(uintptr_t)p)[i];
+}
 
 // LDS image of a tile: rows of DP elements (dim rounded up), the 16-byte
 // chunks of a row XORed by a key of the row.  64 banks of 4 bytes serve 16
@@ -145,11 +174,17 @@ __device__ __forceinline__ float add_halves(float x) {
     return h.low + h.high;
 }
 
+// What a key that is not there is read from: keys of 0, whose score is masked,
+// and values of 0, so that the weight 0 meets no NaN.  Also the elements of a
+// row past dim.
+static __device__ __attribute__((aligned(16))) const uint32_t g_zero_row[128] = {};
+__device__ __forceinline__ uint64_t zero_row() { return (uint64_t)(uintptr_t)g_zero_row; }
+
 template <uint32_t DP>
 struct Shared {
     uint8_t ring[Geo<DP>::ring_bytes];
-    int64_t koff[2 * kSegment];       // byte offset of each key's row in the pools, -1: not there
-    int64_t voff[2 * kSegment];
+    uint64_t kaddr[2 * kSegment];     // address of each key's row in the pools
+    uint64_t vaddr[2 * kSegment];
     uint64_t there[2 * kSegment / 64];
 };
 
@@ -172,7 +207,7 @@ struct Wave {
     }
 
     // The lane's query (row r of the head's rows; none past `rows`).
-    __device__ __forceinline__ void load(const AttnArgs& a, uint32_t head, uint32_t r, bool valid) {
+    __device__ __forceinline__ void load(cargs& a, uint32_t head, uint32_t r, bool valid) {
         const uint32_t lane = lane_id();
         const uint32_t b = r / a.rows_own, in = r - b * a.rows_own, j = in / a.group, g = in - j * a.group;
         const gbyte* p = gptr(a.q.base) + (int64_t)b * a.q.stride[3] + (int64_t)j * a.q.stride[2] +
@@ -187,48 +222,61 @@ struct Wave {
         clear();
     }
 
-    // Scores of NB blocks of 32 keys.
+    // Scores of NB blocks of 32 keys.  Keys are read two steps ahead of the
+    // product that takes them, no further: the registers are full.
     template <uint32_t NB>
     __device__ __forceinline__ void scores(const uint8_t* keys, f32x16 (&s)[NB]) const {
+        constexpr uint32_t AHEAD = 2;
         const uint32_t lane = lane_id(), row = lane % 32u, key = Geo<DP>::key_k(row);
+        const uint8_t* at = keys + row * (DP * 2u);
+        v8 x[AHEAD + 1][NB];
+        auto read = [&](uint32_t k) {
+            const uint32_t c = (2u * k + lane / 32u) ^ key;
+#pragma unroll
+            for (uint32_t n = 0; n < NB; ++n)
+                x[k % (AHEAD + 1)][n] = *reinterpret_cast<const v8*>(at + n * 32u * (DP * 2u) + c * 16u);
+        };
+#pragma unroll
+        for (uint32_t k = 0; k < AHEAD; ++k) read(k);
 #pragma unroll
         for (uint32_t n = 0; n < NB; ++n) s[n] = (f32x16)(0.0f);
 #pragma unroll
         for (uint32_t k = 0; k < NK; ++k) {
+            if (k + AHEAD < NK) read(k + AHEAD);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (uint32_t n = 0; n < NB; ++n) {
-                const uint32_t c = (2u * k + lane / 32u) ^ key;
-                const v8 x = *reinterpret_cast<const v8*>(keys + (n * 32u + row) * (DP * 2u) + c * 16u);
-                s[n] = mfma(x, q[k], s[n]);
-            }
+            for (uint32_t n = 0; n < NB; ++n) s[n] = mfma(x[k % (AHEAD + 1)][n], q[k], s[n]);
         }
     }
 
-    // Keys that this lane's query does not see, or that are not there, weigh
-    // nothing.  `limit` counts from the tile's first key.
+    // Keys that this lane's query does not see, or that are not there (a bit
+    // of `sees` each), weigh nothing.
     template <uint32_t NB>
-    __device__ __forceinline__ static void mask(f32x16 (&s)[NB], int32_t limit, uint64_t there) {
-        const uint32_t hh = lane_id() / 32u;
+    __device__ __forceinline__ static void mask(f32x16 (&s)[NB], uint64_t sees) {
 #pragma unroll
-        for (uint32_t n = 0; n < NB; ++n)
+        for (uint32_t n = 0; n < NB; ++n) {
+            const uint32_t bits = (uint32_t)(sees >> (32u * n)) >> (4u * (lane_id() / 32u));
 #pragma unroll
-            for (uint32_t i = 0; i < 16; ++i) {
-                const uint32_t key = n * 32u + 8u * (i / 4u) + 4u * hh + i % 4u;
-                if ((int32_t)key >= limit || !(there >> key & 1u)) s[n][i] = -INFINITY;
-            }
+            for (uint32_t i = 0; i < 16; ++i)
+                if (!(bits & (1u << (8u * (i / 4u) + i % 4u)))) s[n][i] = -INFINITY;
+        }
     }
 
-    // Weights of the scores, in place.  The sums are only rescaled when a
-    // score passes the largest of before by 2^kLazy; weights then stay below
-    // 2^kLazy, which both types hold.
+    // Largest score of the lane's query, in powers of two.
     template <uint32_t NB>
-    __device__ __forceinline__ void weights(const AttnArgs& a, f32x16 (&s)[NB]) {
+    __device__ __forceinline__ static float largest(float scale, const f32x16 (&s)[NB]) {
         float top = s[0][0];
 #pragma unroll
         for (uint32_t n = 0; n < NB; ++n)
 #pragma unroll
             for (uint32_t i = 0; i < 16; ++i) top = fmaxf(top, s[n][i]);
-        top = max_halves(top) * a.scale;
+        return max_halves(top) * scale;
+    }
+
+    // The sums are only rescaled when a score passes the largest of before by
+    // 2^kLazy; weights then stay below 2^kLazy, which both types hold.
+    // Returns what weights are taken relative to.
+    __device__ __forceinline__ float rescale(float top) {
         if (__any(top > m + kLazy)) {
             const float next = fmaxf(m, top), fade = next == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - next);
             m = next;
@@ -236,42 +284,119 @@ struct Wave {
 #pragma unroll
             for (uint32_t i = 0; i < NO; ++i) o[i] *= fade;
         }
-        const float at = m == -INFINITY ? 0.0f : m;
+        return m == -INFINITY ? 0.0f : m;
+    }
+
+    // Weights of the scores, in place.
+    template <uint32_t NB>
+    __device__ __forceinline__ void weights(float scale, f32x16 (&s)[NB]) {
+        const float at = rescale(largest(scale, s));
         float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (uint32_t n = 0; n < NB; ++n)
 #pragma unroll
             for (uint32_t i = 0; i < 16; ++i) {
-                s[n][i] = __builtin_amdgcn_exp2f(fmaf(s[n][i], a.scale, -at));
+                s[n][i] = __builtin_amdgcn_exp2f(fmaf(s[n][i], scale, -at));
                 sum[i % 4u] += s[n][i];
             }
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
     }
 
-    // o += values^T x weights.
-    template <uint32_t NB>
-    __device__ __forceinline__ void values(const uint8_t* vals, const f32x16 (&p)[NB]) {
+    // Values of 16 keys, transposed: NO pieces of 32 elements x 16 keys.
+    union Piece { s16x4 h[2]; v8 v; };
+    __device__ __forceinline__ static void read_values(const uint8_t* vals, uint32_t step, Piece (&x)[NO]) {
         const uint32_t lane = lane_id(), i = lane % 16u;
         const uint32_t row = 4u * (lane / 32u) + i / 4u;                  // of 4 x 16-element pieces
-        const uint32_t c0 = 2u * ((lane / 16u) & 1u) + (i % 4u) / 2u;
-        const uint8_t* at = vals + row * (DP * 2u) + 8u * (i & 1u);
-        const uint32_t key = Geo<DP>::key_v(row);
+        const uint32_t c0 = 2u * ((lane / 16u) & 1u) + (i % 4u) / 2u, key = Geo<DP>::key_v(row);
+        const uint8_t* at = vals + (step * 16u + row) * (DP * 2u) + 8u * (i & 1u);
 #pragma unroll
-        for (uint32_t n = 0; n < NB; ++n)
+        for (uint32_t b = 0; b < NO; ++b) {
+            const uint8_t* v = at + ((4u * b + c0) ^ key) * 16u;
+            x[b].h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)v);
+            x[b].h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(v + 8u * DP * 2u));
+        }
+    }
+
+    // o += values^T x weights; x[0] holds the first step's values.
+    template <uint32_t NB>
+    __device__ __forceinline__ void values(const uint8_t* vals, const f32x16 (&p)[NB], Piece (&x)[2][NO]) {
 #pragma unroll
-            for (uint32_t t = 0; t < 2; ++t) {
-                v8 w;
+        for (uint32_t t = 0; t < 2 * NB; ++t) {
+            if (t + 1u < 2 * NB) read_values(vals, t + 1u, x[(t + 1u) & 1u]);
+            v8 w;
 #pragma unroll
-                for (uint32_t e = 0; e < 8; ++e) w[e] = (T)p[n][8u * t + e];
+            for (uint32_t e = 0; e < 8; ++e) w[e] = (T)p[t / 2u][8u * (t & 1u) + e];
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (uint32_t b = 0; b < NO; ++b) {
-                    const uint8_t* x = at + (n * 32u + t * 16u) * (DP * 2u) + ((4u * b + c0) ^ key) * 16u;
-                    union { s16x4 h[2]; v8 v; } u;
-                    u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)x);
-                    u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(x + 8u * DP * 2u));
-                    o[b] = mfma(u.v, w, o[b]);
-                }
+            for (uint32_t b = 0; b < NO; ++b) o[b] = mfma(x[t & 1u][b].v, w, o[b]);
+        }
+    }
+
+    // Scores of the next tile of 64 keys, next = keys x q, while this tile's
+    // scores become weights, and then o += values^T x weights.  Written as one
+    // sequence of matrix instructions with the reads of the ones to come and
+    // the arithmetic of the weights spread evenly between them: the matrix
+    // cores and the other units work at the same time within a wave.
+    // Returns the largest of the next scores.
+    __device__ __forceinline__ float advance(float scale, const uint8_t* keys, const uint8_t* vals, float top,
+                                             f32x16 (&s)[2], f32x16 (&next)[2]) {
+        constexpr uint32_t NS = 2 * NK, NP = 4 * NO, AHEAD = 5;           // products of scores, of values
+        const uint32_t lane = lane_id(), row = lane % 32u, key = Geo<DP>::key_k(row);
+        const uint8_t* kat = keys + row * (DP * 2u);
+        const uint32_t i16 = lane % 16u, vrow = 4u * (lane / 32u) + i16 / 4u;
+        const uint32_t c0 = 2u * ((lane / 16u) & 1u) + (i16 % 4u) / 2u, vkey = Geo<DP>::key_v(vrow);
+        const uint8_t* vat = vals + vrow * (DP * 2u) + 8u * (i16 & 1u);
+        Piece x[AHEAD + 1];
+        auto read = [&](uint32_t i) {                                     // what product i takes from LDS
+            Piece& y = x[i % (AHEAD + 1u)];
+            if (i < NS) {
+                const uint32_t k = i / 2u, n = i % 2u;
+                y.v = *reinterpret_cast<const v8*>(kat + n * 32u * (DP * 2u) + ((2u * k + lane / 32u) ^ key) * 16u);
+            } else if (i < NS + NP) {
+                const uint32_t t = (i - NS) / NO, b = (i - NS) % NO;
+                const uint8_t* v = vat + t * 16u * (DP * 2u) + ((4u * b + c0) ^ vkey) * 16u;
+                y.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)v);
+                y.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(v + 8u * DP * 2u));
             }
+        };
+#pragma unroll
+        for (uint32_t i = 0; i < AHEAD; ++i) read(i);
+        const float at = rescale(top);
+        float sum[2] = {0.0f, 0.0f};
+        v8 w[4];
+        float best = 0.0f;
+        static_for<(int)(NS + NP)>([&](auto slot) {
+            constexpr uint32_t i = decltype(slot)::value;
+            read(i + AHEAD);
+            const v8 y = x[i % (AHEAD + 1u)].v;
+            if constexpr (i < NS) {
+                constexpr uint32_t k = i / 2u, n = i % 2u;
+                next[n] = mfma(y, q[k], k == 0 ? (f32x16)(0.0f) : next[n]);
+            } else {
+                constexpr uint32_t t = (i - NS) / NO, b = (i - NS) % NO;
+                o[b] = mfma(y, w[t], o[b]);
+            }
+            // weight e before product NS + NO * (e / 8) takes it
+            constexpr uint32_t M = NS + 3u * NO, e0 = (i * 32u + M - 1u) / M, e1 = ((i + 1u) * 32u + M - 1u) / M;
+            static_for<(int)(i < M ? e1 - e0 : 0u)>([&](auto which) {
+                constexpr uint32_t e = e0 + decltype(which)::value;
+                static_assert(e < 32u && (i < NS || e / 8u > (i - NS) / NO), "in time");
+                const float p = __builtin_amdgcn_exp2f(fmaf(s[e / 16u][e % 16u], scale, -at));
+                sum[e % 2u] += p;
+                asm volatile("" : "+v"(sum[e % 2u]));                     // here, not behind the last product
+                w[e / 8u][e % 8u] = (T)p;
+            });
+            // the next scores' largest, from the third product of values on
+            constexpr uint32_t per = (32u + NP - 3u) / (NP - 2u), j0 = i < NS + 2u ? 32u : (i - NS - 2u) * per;
+            static_for<(int)(j0 < 32u ? (32u - j0 < per ? 32u - j0 : per) : 0u)>([&](auto which) {
+                constexpr uint32_t j = j0 + decltype(which)::value;
+                if constexpr (j == 0) best = next[0][0];
+                else best = fmaxf(best, next[j / 16u][j % 16u]);
+            });
+            __builtin_amdgcn_sched_barrier(0);
+        });
+        l += sum[0] + sum[1];
+        return max_halves(best) * scale;
     }
 
     // Whether a tile of 32 keys holds infinities or NaN in the values of keys
@@ -300,7 +425,7 @@ struct Wave {
     // a NaN among their values must not meet the weight 0 of the latter.  Such
     // elements are added here to the queries that see them, and are 0 for the
     // matrix product.
-    __device__ __forceinline__ void ragged_values(uint8_t* vals, const f32x16 (&p)[1], int32_t limit, uint32_t from,
+    __device__ __forceinline__ void ragged_values(uint8_t* vals, const f32x16 (&p)[1], uint32_t limit, uint32_t from,
                                                   uint32_t to) {
         if (!odd_values<false>(vals, from, to)) return;
         const uint32_t hh = lane_id() / 32u;
@@ -318,7 +443,7 @@ struct Wave {
 #pragma unroll
                 for (uint32_t e = 0; e < 4; ++e) {
                     const uint16_t h = (uint16_t)(bits >> (16u * e));
-                    if (not_finite(h) && (int32_t)key < limit)
+                    if (not_finite(h) && key < limit)
                         o[f / 4u][4u * (f % 4u) + e] += x * (float)__builtin_bit_cast(T, h);
                 }
             }
@@ -332,46 +457,54 @@ struct Wave {
 
 // Where keys base .. base + kSegment * count of a row lie.  Thread after
 // thread a key; what is not a page of the pool is recorded and left out.
-__device__ __forceinline__ int32_t page_of_key(const AttnArgs& a, uint32_t row, uint32_t key, uint32_t end) {
+__device__ __forceinline__ int32_t page_of_key(cargs& a, uint32_t row, uint32_t key, uint32_t end) {
     if (key >= end) return -1;
     return *(const ATT_GLOBAL int32_t*)(gptr(a.table) + ((uint64_t)row * a.pitch + key / a.slots) * 4u);
 }
 
 template <uint32_t DP>
-__device__ __forceinline__ void place_key(const AttnArgs& a, uint32_t head, uint32_t key, uint32_t end, int32_t page,
+__device__ __forceinline__ void place_key(cargs& a, uint32_t head, uint32_t key, uint32_t end, int32_t page,
                                           Shared<DP>& sh, uint32_t at) {
     const bool ok = key < end && (uint32_t)page < a.pages;
     if (key < end && !ok) record_page_error(a.err);
     const int64_t slot = key % a.slots;
-    sh.koff[at] = ok ? page * a.k.stride[3] + slot * a.k.stride[1] + (int64_t)head * a.k.stride[2] : -1;
-    sh.voff[at] = ok ? page * a.v.stride[3] + slot * a.v.stride[1] + (int64_t)head * a.v.stride[2] : -1;
+    sh.kaddr[at] = ok ? a.k.base + (uint64_t)(page * a.k.stride[3] + slot * a.k.stride[1] + head * a.k.stride[2]) : zero_row();
+    sh.vaddr[at] = ok ? a.v.base + (uint64_t)(page * a.v.stride[3] + slot * a.v.stride[1] + head * a.v.stride[2]) : zero_row();
     const uint64_t mask = __ballot(ok);
     if (at % 64u == 0) sh.there[at / 64u] = mask;
 }
 
-// Issue the copies of groups [first, first + N) x STEP of a tile: chunk i of
-// 64 * group + lane is row i / cpr; the row's offset says where it lies.
-// Rows that are not there stay as they are (VALUES: become 0, so that a weight
-// of 0 meets no NaN).
-template <uint32_t DP, uint32_t N, uint32_t STEP, bool VALUES>
-__device__ __forceinline__ void copy_rows(const AttnArgs& a, uint64_t base, const int64_t* off, uint32_t first,
-                                          uint8_t* dst, bool whole) {
-    const uint32_t lane = lane_id();
-    const uint32_t lds = uniform(lds_addr_of(dst));
-#pragma unroll
-    for (uint32_t n = 0; n < N; ++n) {
-        const uint32_t g = first + n * STEP, i = g * 64u + lane, row = i / Geo<DP>::cpr, p = i - row * Geo<DP>::cpr;
-        const uint32_t c = p ^ (VALUES ? Geo<DP>::key_v(row) : Geo<DP>::key_k(row));
-        const int64_t at = off[row];
-        const uint64_t src = base + (uint64_t)at + c * 16u;
-        if (whole) {
-            copy16(src, lds + g * 1024u);
-        } else if (c * 8u < a.dim) {
-            if (at >= 0) copy16(src, lds + g * 1024u);
-            else if (VALUES) *reinterpret_cast<u32x4*>(dst + i * 16u) = (u32x4)(0u);
-        }
+// Copy n of N of a wave's share of a tile: groups first, first + STEP, ... of
+// 64 chunks each.  Chunk i = 64 * group + lane is row i / cpr; the row's
+// address says where it lies.
+template <uint32_t DP, uint32_t STEP, bool VALUES>
+struct RowCopy {
+    uint32_t first, dim;
+    __device__ __forceinline__ uint32_t chunk(uint32_t n, uint32_t& row) const {
+        const uint32_t i = (first + n * STEP) * 64u + lane_id();
+        row = i / Geo<DP>::cpr;
+        return (i - row * Geo<DP>::cpr) ^ (VALUES ? Geo<DP>::key_v(row) : Geo<DP>::key_k(row));
     }
-}
+    __device__ __forceinline__ uint64_t source(uint32_t n, const uint64_t* addr) const {
+        uint32_t row;
+        const uint32_t c = chunk(n, row);
+        const uint64_t at = addr[row] + c * 16u;
+        const uint64_t in = (uint64_t)((int64_t)(int32_t)(c * 8u - dim) >> 32);   // all ones below dim, without a branch
+        return (at & in) | (zero_row() & ~in);
+    }
+    __device__ __forceinline__ void issue(uint32_t n, uint64_t src, uint32_t lds) const {
+        copy16(src, lds + (first + n * STEP) * 1024u);
+    }
+    template <uint32_t N>
+    __device__ __forceinline__ void all(const uint64_t* addr, const uint8_t* dst) const {
+        const uint32_t lds = uniform(lds_addr_of(dst));
+        uint64_t src[N];
+#pragma unroll
+        for (uint32_t n = 0; n < N; ++n) src[n] = source(n, addr);
+#pragma unroll
+        for (uint32_t n = 0; n < N; ++n) issue(n, src[n], lds);
+    }
+};
 
 // ---- partial results -------------------------------------------------------------
 
@@ -379,12 +512,12 @@ __device__ __forceinline__ void copy_rows(const AttnArgs& a, uint64_t base, cons
 // them: piece f = 4 * b + g of lane l is elements 32 b + 8 g + 4 (l / 32) + 0..3
 // of row l % 32.
 template <uint32_t DP>
-__device__ __forceinline__ f32x4* part_at(const AttnArgs& a, uint64_t block) {
+__device__ __forceinline__ f32x4* part_at(cargs& a, uint64_t block) {
     return a.part_o + block * (DP / 8u * 64u);
 }
 
 template <typename T>
-__device__ __forceinline__ void store_result(const AttnArgs& a, uint32_t head, uint32_t r, uint32_t d, f32x4 x) {
+__device__ __forceinline__ void store_result(cargs& a, uint32_t head, uint32_t r, uint32_t d, f32x4 x) {
     const uint32_t b = r / a.rows_own, in = r - b * a.rows_own, j = in / a.group, g = in - j * a.group;
     gbyte* p = gptr(a.o.base) + (int64_t)b * a.o.stride[3] + (int64_t)j * a.o.stride[2] +
                (int64_t)(head * a.group + g) * a.o.stride[1];
@@ -394,7 +527,7 @@ __device__ __forceinline__ void store_result(const AttnArgs& a, uint32_t head, u
     *(ATT_GLOBAL uint64_t*)(p + d * 2u) = __builtin_bit_cast(uint64_t, y);
 }
 
-__device__ __forceinline__ void store_lse(const AttnArgs& a, uint32_t head, uint32_t r, float m, float l) {
+__device__ __forceinline__ void store_lse(cargs& a, uint32_t head, uint32_t r, float m, float l) {
     const uint32_t b = r / a.rows_own, in = r - b * a.rows_own, j = in / a.group, g = in - j * a.group;
     a.lse[((uint64_t)b * a.q_len + j) * ((uint64_t)a.kv * a.group) + head * a.group + g] =
         l == 0.0f ? -INFINITY : m * 0.6931471805599453f + logf(l);
@@ -405,55 +538,86 @@ __device__ __forceinline__ void store_lse(const AttnArgs& a, uint32_t head, uint
 // Four waves of 32 rows each over the tiles of one part of the prefix.  Two
 // stages: while a tile is used the next is on its way; a barrier a tile.
 template <typename T, uint32_t DP>
-__device__ __forceinline__ void shared_part(const AttnArgs& a, Shared<DP>& sh, uint32_t head, uint32_t part,
+__device__ __forceinline__ void shared_part(cargs& a, Shared<DP>& sh, uint32_t head, uint32_t part,
                                             uint32_t block) {
     const uint32_t tid = threadIdx.x, wave = uniform(tid / 64u);
     const uint32_t per = part_keys(a.prefix_len, a.parts_all, kTile);
     const uint32_t k0 = part_begin(a.prefix_len, part, per), k1 = part_begin(a.prefix_len, part + 1u, per);
     const uint32_t tiles = (k1 - k0 + kTile - 1u) / kTile;
     const uint32_t r = block * kWgRows + wave * kRows + lane_id() % 32u;
-    const bool used = block * kWgRows + wave * kRows < a.rows_all;
     constexpr uint32_t SEG = kSegment / kTile;                            // tiles of a segment
     constexpr uint32_t NG = Geo<DP>::cpr / kWaves;                        // groups a wave copies of a tile's keys
     Wave<T, DP> w;
     w.load(a, head, r, r < a.rows_all);
     int32_t page = page_of_key(a, a.prefix_row, k0 + tid, k1);
     place_key(a, head, k0 + tid, k1, page, sh, tid);
-    if (a.dim < DP)                                                       // padded elements of the keys are 0
-        for (uint32_t i = tid * 16u; i < Geo<DP>::ring_bytes; i += kThreads * 16u)
-            *reinterpret_cast<u32x4*>(sh.ring + i) = (u32x4)(0u);
     __syncthreads();
-    auto issue = [&](uint32_t t) {
-        uint8_t* dst = sh.ring + (t & 1u) * 2u * Geo<DP>::tile_bytes;
-        const uint32_t at = t % (2u * SEG);
-        const bool whole = uniform64(sh.there[at]) == ~0ull && a.dim == DP;
-        copy_rows<DP, NG, kWaves, false>(a, a.k.base, sh.koff + at * kTile, wave, dst, whole);
-        copy_rows<DP, NG, kWaves, true>(a, a.v.base, sh.voff + at * kTile, wave, dst + Geo<DP>::tile_bytes, whole);
-    };
-    if (tiles) issue(0);
-    for (uint32_t t = 0; t < tiles; ++t) {
+    // Stages of keys first, of values behind them.
+    auto keys = [&](uint32_t t) { return sh.ring + (t & 1u) * Geo<DP>::tile_bytes; };
+    auto vals = [&](uint32_t t) { return sh.ring + (2u + (t & 1u)) * Geo<DP>::tile_bytes; };
+    auto there = [&](uint32_t t) { return uniform64(sh.there[t % (2u * SEG)]); };
+    const RowCopy<DP, kWaves, false> kcopy{wave, a.dim};
+    const RowCopy<DP, kWaves, true> vcopy{wave, a.dim};
+    auto kaddr = [&](uint32_t t) { return sh.kaddr + t % (2u * SEG) * kTile; };
+    auto vaddr = [&](uint32_t t) { return sh.vaddr + t % (2u * SEG) * kTile; };
+    // What is on its way has arrived, for every wave, and every wave is done
+    // with the stages that are filled next.
+    auto meet = [&] {
         wait_vmcnt<0>();
         wait_lgkm0();
         wg_barrier();
-        const uint32_t seg = t / SEG, next = k0 + (seg + 1u) * kSegment + tid;
-        if (t % SEG == SEG / 2)                                            // read from the next segment's first copy on
-            place_key(a, head, next, k1, page, sh, ((seg + 1u) & 1u) * kSegment + tid);
-        const uint64_t there = uniform64(sh.there[t % (2u * SEG)]);
-        if (t + 1u < tiles) issue(t + 1u);
-        if (t % SEG == 0) page = page_of_key(a, a.prefix_row, next, k1);
-        if (used) {
-            const uint8_t* keys = sh.ring + (t & 1u) * 2u * Geo<DP>::tile_bytes;
-            f32x16 s[2];
-            w.scores(keys, s);
-            if (there != ~0ull) w.mask(s, kTile, there);
-            w.weights(a, s);
-            w.values(keys + Geo<DP>::tile_bytes, s);
-        }
+    };
+    auto begin = [&](uint32_t t) {
+        meet();
+        const uint32_t next = k0 + (t / SEG + 1u) * kSegment + tid;
+        if (t % SEG == 1)                                                  // used from the next segment's first keys on
+            place_key(fresh(), head, next, k1, page, sh, ((t / SEG + 1u) & 1u) * kSegment + tid);
+        if (t % SEG == 0) page = page_of_key(fresh(), fresh().prefix_row, next, k1);
+    };
+    if (tiles) {
+        kcopy.template all<NG>(kaddr(0), keys(0));
+        kcopy.template all<NG>(kaddr(1), keys(1));
+        vcopy.template all<NG>(vaddr(0), vals(0));
     }
-    if (!used) return;
+    meet();
+    if (block * kWgRows + wave * kRows >= a.rows_all) {                    // no rows for this wave: it only copies
+        for (uint32_t t = 0; t < tiles; ++t) {
+            begin(t);
+            kcopy.template all<NG>(kaddr(t + 2u), keys(t));
+            vcopy.template all<NG>(vaddr(t + 1u), vals(t + 1u));
+        }
+        wait_vmcnt<0>();
+        return;
+    }
+    const float scale = a.scale;
+    f32x16 s[2][2];
+    w.scores(keys(0), s[0]);
+    float top = 0.0f;
+    auto finish = [&](uint32_t t, f32x16 (&x)[2], bool known) {            // tile t's scores are there
+        const uint64_t sees = there(t);
+        if (sees != ~0ull) w.mask(x, sees);
+        if (sees != ~0ull || !known) top = w.largest(scale, x);
+    };
+    finish(0, s[0], false);
+    // Behind the last tile, keys that are not there are copied and multiplied:
+    // two tiles' work at most, and every tile is like the others.
+    auto step = [&](uint32_t t, f32x16 (&x)[2], f32x16 (&y)[2]) {
+        begin(t);
+        kcopy.template all<NG>(kaddr(t + 2u), keys(t));
+        vcopy.template all<NG>(vaddr(t + 1u), vals(t + 1u));
+        top = w.advance(scale, keys(t + 1u), vals(t), top, x, y);
+        finish(t + 1u, y, true);
+    };
+    for (uint32_t t = 0; t < tiles; ++t) {
+        step(t, s[0], s[1]);
+        if (++t == tiles) break;
+        step(t, s[1], s[0]);
+    }
+    wait_vmcnt<0>();                                                       // nothing may land in LDS of a later workgroup
+    cargs& e = fresh();
     const uint32_t lane = lane_id();
-    const uint64_t at = ((uint64_t)head * a.parts_all + part) * a.blocks_all + block * kWaves + wave;
-    f32x4* out = part_at<DP>(a, at);
+    const uint64_t at = ((uint64_t)head * e.parts_all + part) * e.blocks_all + block * kWaves + wave;
+    f32x4* out = part_at<DP>(e, at);
 #pragma unroll
     for (uint32_t b = 0; b < DP / 32u; ++b)
 #pragma unroll
@@ -461,7 +625,7 @@ __device__ __forceinline__ void shared_part(const AttnArgs& a, Shared<DP>& sh, u
             out[(4u * b + g) * 64u + lane] =
                 f32x4{w.o[b][4u * g], w.o[b][4u * g + 1u], w.o[b][4u * g + 2u], w.o[b][4u * g + 3u]};
     const float l = w.total();
-    if (lane < 32u) a.part_ml[at * 32u + lane] = make_float2(w.m, l);
+    if (lane < 32u) e.part_ml[at * 32u + lane] = make_float2(w.m, l);
 }
 
 // ---- a wave's own tiles -------------------------------------------------------------
@@ -480,12 +644,20 @@ struct OwnJob {
 };
 
 template <typename T, uint32_t DP>
-__device__ __forceinline__ void own_part(const AttnArgs& a, Shared<DP>& sh, const OwnJob& job) {
+__device__ __forceinline__ void own_part(cargs& a, Shared<DP>& sh, const OwnJob& job) {
     const uint32_t tid = threadIdx.x, wave = uniform(tid / 64u), lane = lane_id(), n32 = lane % 32u;
     const uint32_t r = job.first + n32;
     const bool valid = n32 < job.count;
     constexpr uint32_t NP = Geo<DP>::cpr / 2;                             // copies of a tile's keys
     constexpr uint32_t SEG = 2 * kSegment;
+    int32_t page[SEG / kThreads];                                         // of the next segment's keys
+    auto pages = [&](uint32_t base) {
+        cargs& e = fresh();
+#pragma unroll
+        for (uint32_t i = 0; i < SEG / kThreads; ++i)
+            page[i] = page_of_key(e, job.row, base + i * kThreads + tid, job.k1);
+    };
+    pages(job.k0);                                                        // on its way while the queries are
     Wave<T, DP> w;
     w.load(a, job.head, r, valid);
     // keys below `common` are seen by all of the rows, those below `limit` by this lane's
@@ -494,58 +666,54 @@ __device__ __forceinline__ void own_part(const AttnArgs& a, Shared<DP>& sh, cons
     const int64_t sees = job.all ? (int64_t)job.k1 : first_sees + (r % a.rows_own) / a.group;
     uint8_t* const keys = sh.ring + wave * 2u * Geo<DP>::own_bytes;
     uint8_t* const vals = keys + Geo<DP>::own_bytes;
-    if (a.dim < DP)                                                       // padded elements of the keys are 0
-        for (uint32_t i = lane * 16u; i < 2u * Geo<DP>::own_bytes; i += 1024u)
-            *reinterpret_cast<u32x4*>(keys + i) = (u32x4)(0u);
+    const float scale = a.scale;
+    const uint32_t q_len = a.q_len;
+    const RowCopy<DP, 1, false> kcopy{0, a.dim};
+    const RowCopy<DP, 1, true> vcopy{0, a.dim};
     for (uint32_t base = job.k0; base < job.k1; base += SEG) {
         if (base != job.k0) __syncthreads();                              // the segment before is used up
-        for (uint32_t at = tid; at < SEG; at += kThreads)
-            place_key(a, job.head, base + at, job.k1, page_of_key(a, job.row, base + at, job.k1), sh, at);
+#pragma unroll
+        for (uint32_t i = 0; i < SEG / kThreads; ++i)
+            place_key(a, job.head, base + i * kThreads + tid, job.k1, page[i], sh, i * kThreads + tid);
         __syncthreads();
+        pages(base + SEG);
         const uint32_t left = job.k1 - base, n = left < SEG ? left : SEG, tiles = (n + kOwnTile - 1u) / kOwnTile;
         auto mask_of = [&](uint32_t t) { return (uint32_t)(uniform64(sh.there[t / 2u]) >> (32u * (t & 1u))); };
-        auto issue_k = [&](uint32_t t) {
-            copy_rows<DP, NP, 1, false>(a, a.k.base, sh.koff + t * kOwnTile, 0, keys, mask_of(t) == ~0u && a.dim == DP);
-        };
-        auto issue_v = [&](uint32_t t) {
-            copy_rows<DP, NP, 1, true>(a, a.v.base, sh.voff + t * kOwnTile, 0, vals, mask_of(t) == ~0u && a.dim == DP);
-        };
+        auto issue_k = [&](uint32_t t) { kcopy.template all<NP>(sh.kaddr + t * kOwnTile, keys); };
+        auto issue_v = [&](uint32_t t) { vcopy.template all<NP>(sh.vaddr + t * kOwnTile, vals); };
         if (wave < tiles) {
             issue_k(wave);
             issue_v(wave);
         }
         for (uint32_t t = wave; t < tiles; t += kWaves) {
             const uint32_t bits = mask_of(t), next = t + kWaves, k = base + t * kOwnTile;
-            // a tile with rows that are not there may take fewer copies than NP
-            if (bits == ~0u) wait_vmcnt<NP>();
-            else wait_vmcnt<0>();
+            wait_vmcnt<NP>();
             f32x16 s[1];
             w.scores(keys, s);
             wait_lgkm0();
-            bool counted = false;
-            if (next < tiles) {
-                issue_k(next);
-                counted = mask_of(next) == ~0u;
-            }
+            if (next < tiles) issue_k(next);
             const int64_t lim = sees - k;
-            const int32_t limit = lim < 0 ? 0 : lim > (int64_t)kOwnTile ? (int32_t)kOwnTile : (int32_t)lim;
+            const uint32_t limit = lim < 0 ? 0u : lim > (int64_t)kOwnTile ? kOwnTile : (uint32_t)lim;
             const bool ragged = k + kOwnTile > common;
-            if (ragged || bits != ~0u) w.mask(s, limit, bits);
-            w.weights(a, s);
-            if (counted) wait_vmcnt<NP>();
+            if (ragged || bits != ~0u) w.mask(s, bits & ((1ull << limit) - 1ull));
+            w.weights(scale, s);
+            if (next < tiles) wait_vmcnt<NP>();
             else wait_vmcnt<0>();
-            if (ragged && a.q_len > 1u)
-                w.ragged_values(vals, s, valid ? limit : 0, common > k ? common - k : 0u,
+            if (ragged && q_len > 1u)
+                w.ragged_values(vals, s, valid ? limit : 0u, common > k ? common - k : 0u,
                                 job.k1 - k < kOwnTile ? job.k1 - k : kOwnTile);
-            w.values(vals, s);
+            typename Wave<T, DP>::Piece x[2][DP / 32];
+            w.read_values(vals, 0, x[0]);
+            w.values(vals, s, x);
             wait_lgkm0();
             if (next < tiles) issue_v(next);
         }
     }
     // join the waves
+    cargs& e = fresh();
     constexpr uint32_t NF = DP / 8u;
     __syncthreads();
-    float2* const ml = reinterpret_cast<float2*>(sh.koff);
+    float2* const ml = reinterpret_cast<float2*>(sh.kaddr);
     f32x4* const sums = reinterpret_cast<f32x4*>(sh.ring);
     const uint32_t tiles = (job.k1 - job.k0 + kOwnTile - 1u) / kOwnTile, busy = tiles < kWaves ? tiles : kWaves;
     const float total = w.total();
@@ -565,31 +733,35 @@ __device__ __forceinline__ void own_part(const AttnArgs& a, Shared<DP>& sh, cons
                     f32x4{w.o[b][4u * g], w.o[b][4u * g + 1u], w.o[b][4u * g + 2u], w.o[b][4u * g + 3u]} * fade;
     }
     __syncthreads();
-    f32x4* const out = part_at<DP>(a, job.block);
+    f32x4* const out = part_at<DP>(e, job.block);
     for (uint32_t f = wave; f < NF; f += kWaves) {
         f32x4 x = (f32x4)(0.0f);
         for (uint32_t i = 0; i < busy; ++i) x += sums[(i * NF + f) * 64u + lane];
         if (!valid) continue;
         const uint32_t d = 8u * f + 4u * (lane / 32u);
-        if (!a.direct) out[f * 64u + lane] = x;
-        else if (d < a.dim) store_result<T>(a, job.head, r, d, l == 0.0f ? (f32x4)(0.0f) : x / l);
+        if (!e.direct) out[f * 64u + lane] = x;
+        else if (d < e.dim) store_result<T>(e, job.head, r, d, l == 0.0f ? (f32x4)(0.0f) : x / l);
     }
     if (wave == 0 && valid && lane < 32u) {
-        if (!a.direct) a.part_ml[job.block * 32u + lane] = make_float2(m, l);
-        else if (a.lse) store_lse(a, job.head, r, m, l);
+        if (!e.direct) e.part_ml[job.block * 32u + lane] = make_float2(m, l);
+        else if (e.lse) store_lse(e, job.head, r, m, l);
     }
 }
 
 template <typename T, uint32_t DP>
-__global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_attn(const AttnArgs a) {
+__global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_attn(const AttnArgs) {
+    cargs& a = kernel_args();
     __shared__ __attribute__((aligned(1024))) Shared<DP> sh;
     uint32_t id = blockIdx.x;
     OwnJob job;
     if (id < a.wg_all) {
         // Workgroups go to the 8 XCDs in turn: those that read the same part of
-        // the prefix, one for each block of rows, meet in one XCD's L2.
+        // the prefix, one for each block of rows, meet in one XCD's L2, and so do
+        // the heads of a part: where they lie side by side in a token's row, one
+        // head alone would keep only two of the L2's 16 channels busy.
         const uint32_t rows = a.shared ? kWgRows : kRows, blocks = (a.rows_all + rows - 1u) / rows;
-        const uint32_t x = id % 8u, y = id / 8u, unit = x + 8u * (y / blocks), block = y % blocks;
+        const uint32_t x = id % 8u, y = id / 8u, each = (a.units_all + 7u) / 8u, unit = x * each + y / blocks;
+        const uint32_t block = y % blocks;
         if (unit >= a.units_all) return;
         const uint32_t head = unit % a.kv, part = unit / a.kv;
         if (a.shared) return shared_part<T, DP>(a, sh, head, part, block);
@@ -610,10 +782,10 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_attn(const Attn
         const uint32_t block = id % a.blocks_own;
         id /= a.blocks_own;
         const uint32_t part = id % a.parts_own, b = id / a.parts_own;
-        job.row = a.rows ? (uint32_t)a.rows[b] : b;
+        job.row = a.rows ? (uint32_t)scalar_load(a.rows, b) : b;
         job.len = 0;
         if (job.row < a.table_rows) {
-            const int64_t room = (int64_t)a.slots * a.row_pages, len = a.lens[job.row];
+            const int64_t room = (int64_t)a.slots * a.row_pages, len = scalar_load(a.lens, job.row);
             job.len = len < 0 ? 0 : len > room ? room : len;
             if (job.len != len && threadIdx.x == 0) record_page_error(a.err);
         } else if (threadIdx.x == 0) {
@@ -633,7 +805,8 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_attn(const Attn
 // The parts of 32 rows joined: blockIdx.x is the block of a head's rows, and
 // each wave takes one piece of 8 elements of them.
 template <typename T, uint32_t DP>
-__global__ __launch_bounds__(kThreads) void k_attn_join(const AttnArgs a) {
+__global__ __launch_bounds__(kThreads) void k_attn_join(const AttnArgs) {
+    cargs& a = kernel_args();
     constexpr uint32_t U = 8;                                             // parts in flight
     const uint32_t lane = lane_id(), n32 = lane % 32u, hh = lane / 32u;
     const uint32_t head = blockIdx.x / a.blocks_all, block = blockIdx.x - head * a.blocks_all;
