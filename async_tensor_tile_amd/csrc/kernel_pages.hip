@@ -55,7 +55,9 @@ __device__ __forceinline__ uint32_t div_by(uint32_t n, uint32_t d, uint32_t magi
 }
 
 // One part (16 KiB) of one page, by 256 threads: the loads of a thread's four
-// chunks are in flight together.
+// chunks are in flight together.  STREAM: the pages are many more than the
+// caches hold, so neither side is kept there.
+template <bool STREAM>
 __device__ __forceinline__ void copy_part(const Pools& p, uint32_t pool, int64_t from, int64_t to, uint32_t part) {
     const gbyte* src = gptr(p.base[pool]) + from * p.page;
     gbyte* dst = gptr(p.base[pool]) + to * p.page;
@@ -71,13 +73,17 @@ __device__ __forceinline__ void copy_part(const Pools& p, uint32_t pool, int64_t
             const uint32_t r2 = div_by(row, p.n1, p.magic_n1);
             off[i] = (int64_t)r2 * p.s2 + (int64_t)(row - r2 * p.n1) * p.s1 + (int64_t)k * 16;
             left[i] = p.row_bytes - k * 16u;
-            if (left[i] >= 16u) v[i] = *(const ATT_GLOBAL u32x4*)(src + off[i]);
+            if (left[i] >= 16u)
+                v[i] = STREAM ? __builtin_nontemporal_load((const ATT_GLOBAL u32x4*)(src + off[i]))
+                              : *(const ATT_GLOBAL u32x4*)(src + off[i]);
         }
     }
 #pragma unroll
     for (uint32_t i = 0; i < 4; ++i) {
-        if (left[i] >= 16u) *(ATT_GLOBAL u32x4*)(dst + off[i]) = v[i];
-        else for (uint32_t b = 0; b < left[i]; ++b) dst[off[i] + b] = src[off[i] + b];   // a row's last bytes
+        if (left[i] >= 16u) {
+            if (STREAM) __builtin_nontemporal_store(v[i], (ATT_GLOBAL u32x4*)(dst + off[i]));
+            else *(ATT_GLOBAL u32x4*)(dst + off[i]) = v[i];
+        } else for (uint32_t b = 0; b < left[i]; ++b) dst[off[i] + b] = src[off[i] + b];   // a row's last bytes
     }
 }
 
@@ -90,7 +96,7 @@ __global__ __launch_bounds__(kCopyThreads) void k_page_copy(const Pools p, const
         if (threadIdx.x == 0) record_page_error(err);
         return;
     }
-    copy_part(p, blockIdx.y, from, to, part);
+    copy_part<false>(p, blockIdx.y, from, to, part);
 }
 
 // ---- ranks ---------------------------------------------------------------------
@@ -119,53 +125,61 @@ __device__ __forceinline__ uint32_t scan_block(uint32_t v, uint32_t* total) {
     return before + x - v;
 }
 
-// Busy bits (count above 0) of the 64 pages from base + 64 * thread on; pages
-// past the last are busy.  Reads are coalesced (lane after lane 16 bytes), the
-// bits change hands in LDS.
-__device__ __forceinline__ uint64_t busy_word(const int32_t* refs, uint32_t base, uint32_t pages) {
+// Use counts of one sweep: thread t holds four pages of each 4096, so that
+// reads are coalesced.  Pages past the last count as busy.
+struct Counts {
     typedef int32_t i32x4 __attribute__((ext_vector_type(4), aligned(4)));
-    __shared__ uint8_t nibble[kSweep / 4];
     i32x4 v[16];
+    __device__ __forceinline__ void load(const int32_t* refs, uint32_t base, uint32_t pages) {
 #pragma unroll
-    for (uint32_t u = 0; u < 16; ++u) {
-        const uint32_t p = base + (u * kScanThreads + threadIdx.x) * 4u;
-        v[u] = (i32x4)(1);
-        if (p + 4 <= pages) {
-            v[u] = *(const ATT_GLOBAL i32x4*)(gptr(refs) + (uint64_t)p * 4u);
-        } else {
-            for (uint32_t k = 0; k < 4; ++k)
-                if (p + k < pages) v[u][k] = refs[p + k];
+        for (uint32_t u = 0; u < 16; ++u) {
+            const uint32_t p = base + (u * kScanThreads + threadIdx.x) * 4u;
+            v[u] = (i32x4)(1);
+            if (base + u * kScanThreads * 4u >= pages) continue;         // the whole workgroup is past the end
+            if (p + 4 <= pages) {
+                v[u] = *(const ATT_GLOBAL i32x4*)(gptr(refs) + (uint64_t)p * 4u);
+            } else {
+                for (uint32_t k = 0; k < 4; ++k)
+                    if (p + k < pages) v[u][k] = refs[p + k];
+            }
         }
     }
-    __syncthreads();                     // the previous sweep's readers are done
+    // Busy bits (count above 0) of the 64 pages from base + 64 * thread on: the
+    // bits change hands in LDS.
+    __device__ __forceinline__ uint64_t busy(uint32_t base, uint32_t pages) const {
+        __shared__ uint8_t nibble[kSweep / 4];
+        __syncthreads();                 // the previous sweep's readers are done
 #pragma unroll
-    for (uint32_t u = 0; u < 16; ++u) {
-        nibble[u * kScanThreads + threadIdx.x] =
-            (uint8_t)((v[u][0] > 0) | (v[u][1] > 0) << 1 | (v[u][2] > 0) << 2 | (v[u][3] > 0) << 3);
-    }
-    __syncthreads();
-    uint64_t word = 0;
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(nibble) + threadIdx.x * 4u;
+        for (uint32_t u = 0; u < 16; ++u) {
+            if (base + u * kScanThreads * 4u >= pages) break;
+            nibble[u * kScanThreads + threadIdx.x] =
+                (uint8_t)((v[u][0] > 0) | (v[u][1] > 0) << 1 | (v[u][2] > 0) << 2 | (v[u][3] > 0) << 3);
+        }
+        __syncthreads();
+        if (base + threadIdx.x * 64u >= pages) return ~0ull;
+        uint64_t word = 0;
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(nibble) + threadIdx.x * 4u;
 #pragma unroll
-    for (uint32_t i = 0; i < 4; ++i) {
-        uint32_t x = w[i];                               // four nibbles, one in each byte
-        x = (x | x >> 4) & 0x00FF00FFu;
-        x = (x | x >> 8) & 0xFFFFu;
-        word |= (uint64_t)x << (16 * i);
+        for (uint32_t i = 0; i < 4; ++i) {
+            uint32_t x = w[i];                           // four nibbles, one in each byte
+            x = (x | x >> 4) & 0x00FF00FFu;
+            x = (x | x >> 8) & 0xFFFFu;
+            word |= (uint64_t)x << (16 * i);
+        }
+        return word;
     }
-    return word;
-}
+};
 
 // ---- extend and fork -------------------------------------------------------------
 
-// Workspace of extend and fork: the running need before each entry, each
-// entry's need, the length its row started from, and the free pages.
+// Workspace of extend and fork: for a fork the page each entry gets and the
+// length its row starts from, and the free pages that do not fit into LDS.
 struct AllocWs {
-    int32_t* start;      // [n]
-    int32_t* need;       // [n], -1: not served whatever is free
+    int32_t* page;       // [n]: -1 none needed, -2 not served
     int32_t* held;       // [n]
     int32_t* fresh;      // [pages]
 };
+constexpr uint32_t kFreshLds = 4096;
 
 // Entry i's need of pages, and the length of the row it starts from.  -1 for
 // an entry that cannot be served.
@@ -202,69 +216,97 @@ __device__ __forceinline__ int32_t entry_need(const Table& t, const int32_t* a, 
 }
 
 // One workgroup hands out the lowest free pages.  Extend finishes here; fork
-// leaves the rows and the data to k_fork_rows.
+// leaves the rows and the data to k_fork_rows.  A chain of latencies (entries,
+// their lengths, the counts, the stores), so the counts are on their way
+// before the entries are looked at and nothing passes through memory between
+// the steps: 16384 pages and 128 entries take HAND_OUT_US.
 template <bool FORK>
 __global__ __launch_bounds__(kScanThreads) void k_hand_out(const Table t, const int32_t* a, const int32_t* b,
                                                            uint32_t n, int32_t* ok, AllocWs ws, uint32_t* err) {
+    __shared__ int32_t fresh[kFreshLds];
+    __shared__ uint64_t words[kScanThreads];
+    __shared__ uint32_t ranks[kScanThreads];
+    __shared__ uint32_t starts[kScanThreads + 1];
+    __shared__ int32_t row_of[kScanThreads], first_of[kScanThreads];
     const uint32_t tid = threadIdx.x;
-    uint64_t want = 0;                                    // pages asked for by the entries so far
+    Counts counts;
+    counts.load(t.refs, 0, t.pages);
+    // pages asked for by all entries; with one round of entries, each thread's stays in its registers
+    int32_t held = 0, need = 0;
+    uint32_t before = 0;
+    uint64_t want = 0;
     for (uint32_t i0 = 0; i0 < n; i0 += kScanThreads) {
         const uint32_t i = i0 + tid;
-        int32_t held = 0, need = 0;
+        need = 0;
         if (i < n) need = entry_need<FORK>(t, a, b, i, &held, err);
         uint32_t all;
-        const uint32_t before = scan_block(need > 0 ? (uint32_t)need : 0u, &all);   // a need is below 2^21
-        if (i < n) {
-            const uint64_t s = want + before;
-            ws.start[i] = (int32_t)(s < 0x7FFFFFFFull ? s : 0x7FFFFFFFull);
-            ws.need[i] = need;
-            ws.held[i] = held;
-        }
+        before = scan_block(need > 0 ? (uint32_t)need : 0u, &all);       // a need is below 2^21
         want += all;
     }
-    uint32_t found = 0;
+    uint64_t found = 0;
     for (uint32_t base = 0; base < t.pages && found < want; base += kSweep) {
-        uint64_t open = ~busy_word(t.refs, base, t.pages);
+        if (base) counts.load(t.refs, base, t.pages);
+        const uint64_t open = ~counts.busy(base, t.pages);
         uint32_t all;
-        uint32_t rank = found + scan_block((uint32_t)__popcll(open), &all);
-        while (open && rank < want) {
-            const int k = __ffsll((unsigned long long)open) - 1;
-            open &= open - 1;
-            ws.fresh[rank++] = (int32_t)(base + tid * 64u + (uint32_t)k);
+        ranks[tid] = (uint32_t)found + scan_block((uint32_t)__popcll(open), &all);
+        words[tid] = open;
+        __syncthreads();
+        for (uint32_t p = tid; p < kSweep; p += kScanThreads) {           // a thread for a page, as far as pages are wanted
+            const uint32_t w = p / 64u, first = ranks[w];
+            if (first >= want) break;
+            const uint64_t bit = 1ull << (p % 64u);
+            if (!(words[w] & bit)) continue;
+            const uint32_t rank = first + (uint32_t)__popcll(words[w] & (bit - 1ull));
+            if (rank >= want) break;
+            if (rank < kFreshLds) fresh[rank] = (int32_t)(base + p);
+            else ws.fresh[rank] = (int32_t)(base + p);
         }
         found += all;
     }
-    __syncthreads();                                      // the lists are written
-    // An entry that needs no page is still served only while those before it are.
-    for (uint32_t i = tid; i < n; i += kScanThreads) {
-        const int32_t need = ws.need[i];
-        const uint64_t start = (uint32_t)ws.start[i];
-        const bool served = need >= 0 && start + (uint32_t)need <= found;
-        ok[i] = served;
-        if (FORK) {
-            const int32_t page = served && need ? ws.fresh[start] : -1;
-            if (page >= 0) t.refs[page] = 1;
-            ws.need[i] = served ? page : -2;              // for k_fork_rows: the new page, -1 none, -2 not served
-        } else if (served) {
-            const uint32_t row = (uint32_t)a[i];
-            t.lens[row] = ws.held[i] + b[i];
+    __syncthreads();                                      // the list is written, and every count was read
+    auto page_at = [&](uint64_t rank) { return rank < kFreshLds ? fresh[rank] : ws.fresh[rank]; };
+    uint64_t from = 0;                                    // pages of the entries of earlier rounds
+    for (uint32_t i0 = 0; i0 < n; i0 += kScanThreads) {
+        const uint32_t i = i0 + tid;
+        uint32_t all = (uint32_t)want;
+        if (n > kScanThreads) {
+            need = 0;
+            if (i < n) need = entry_need<FORK>(t, a, b, i, &held, err);
+            before = scan_block(need > 0 ? (uint32_t)need : 0u, &all);
         }
-    }
-    if (!FORK) {
-        // the new pages: a wave for an entry, a lane for a page
-        const uint32_t lane = lane_id();
-        for (uint32_t i = tid / 64u; i < n; i += kScanThreads / 64u) {
-            const int32_t need = ws.need[i];
-            const uint64_t start = (uint32_t)ws.start[i];
-            if (need <= 0 || start + (uint32_t)need > found) continue;
-            const uint32_t first = ((uint32_t)ws.held[i] + t.slots - 1) / t.slots;
-            int32_t* row = t.table + (uint64_t)(uint32_t)a[i] * t.pitch + first;
-            for (uint32_t k = lane; k < (uint32_t)need; k += 64u) {
-                const int32_t page = ws.fresh[start + k];
-                row[k] = page;
+        // An entry that needs no page is still served only while those before it are.
+        const uint64_t start = from + before;
+        const bool served = i < n && need >= 0 && start + (uint32_t)need <= found;
+        if (i < n) ok[i] = served;
+        if (FORK) {
+            if (i < n) {
+                const int32_t page = served && need ? page_at(start) : -1;
+                if (page >= 0) t.refs[page] = 1;
+                ws.page[i] = served ? page : -2;
+                ws.held[i] = held;
+            }
+        } else {
+            // the new pages: a thread for a page, which looks for its entry
+            starts[tid] = before;
+            row_of[tid] = served ? a[i] : -1;
+            first_of[tid] = (int32_t)(((uint32_t)held + t.slots - 1u) / t.slots);
+            if (tid == 0) starts[kScanThreads] = all;
+            if (served) t.lens[(uint32_t)a[i]] = held + b[i];
+            __syncthreads();
+            for (uint32_t k = tid; k < all && from + k < found; k += kScanThreads) {
+                uint32_t e = 0;                           // the last entry that starts at k or before
+#pragma unroll
+                for (uint32_t step = kScanThreads / 2; step; step /= 2)
+                    if (starts[e + step] <= k) e += step;
+                const int32_t row = row_of[e];
+                if (row < 0) continue;
+                const int32_t page = page_at(from + k);
+                t.table[(uint64_t)(uint32_t)row * t.pitch + (uint32_t)first_of[e] + (k - starts[e])] = page;
                 t.refs[page] = 1;
             }
+            __syncthreads();
         }
+        from += all;
     }
 }
 
@@ -275,7 +317,7 @@ __global__ __launch_bounds__(kCopyThreads) void k_fork_rows(const Table t, const
                                                             const int32_t* dst, AllocWs ws, uint32_t pieces,
                                                             uint32_t* err) {
     const uint32_t i = blockIdx.x;
-    const int32_t fresh = ws.need[i];
+    const int32_t fresh = ws.page[i];
     if (fresh == -2) return;
     const int32_t held = ws.held[i];
     const uint32_t full = (uint32_t)held / t.slots;
@@ -305,7 +347,7 @@ __global__ __launch_bounds__(kCopyThreads) void k_fork_rows(const Table t, const
         if (threadIdx.x == 0 && at == 0) record_page_error(err);
         return;
     }
-    copy_part(p, pool, last, fresh, part);
+    copy_part<false>(p, pool, last, fresh, part);
 }
 
 // ---- free ------------------------------------------------------------------------
@@ -341,11 +383,20 @@ struct CompactWs {
     uint32_t* count;      // U, how many move, busy pages below U
 };
 
+// Sweeps of 65536 pages: ranks first, then each thread lists the pages that
+// it finds to be holes or movers.  With one sweep
+// the words stay in LDS between the two.
 __global__ __launch_bounds__(kScanThreads) void k_compact_plan(const Table t, CompactWs ws, int32_t* used) {
+    __shared__ uint64_t words[kScanThreads];
+    __shared__ uint32_t ranks[kScanThreads];
+    __shared__ uint32_t below;                            // busy pages below U
     const uint32_t tid = threadIdx.x;
+    const bool one = t.pages <= kSweep;
+    Counts counts;
     uint32_t total = 0;
     for (uint32_t base = 0; base < t.pages; base += kSweep) {
-        uint64_t busy = busy_word(t.refs, base, t.pages);
+        counts.load(t.refs, base, t.pages);
+        uint64_t busy = counts.busy(base, t.pages);
         const uint32_t p = base + tid * 64u;
         // pages past the last are not in use here
         if (p + 64u > t.pages) busy &= p < t.pages ? (~0ull >> (p + 64u - t.pages)) : 0ull;
@@ -355,28 +406,25 @@ __global__ __launch_bounds__(kScanThreads) void k_compact_plan(const Table t, Co
             ws.busy[p / 64u] = busy;
             ws.before[p / 64u] = rank;
         }
+        words[tid] = busy;
+        ranks[tid] = rank;
         total += all;
     }
-    __syncthreads();                                      // busy and before are written (by their own threads)
-    __shared__ uint32_t below;                            // busy pages below U
-    if (tid == 0) below = total;
-    __syncthreads();
+    __syncthreads();                                      // the words are written
     const uint32_t U = total;
-    if (tid == 0 && U < t.pages)
-        below = ws.before[U / 64u] + (uint32_t)__popcll(ws.busy[U / 64u] & ((1ull << (U % 64u)) - 1ull));
+    auto word_of = [&](uint32_t w) { return one ? words[w] : ws.busy[w]; };
+    auto rank_of = [&](uint32_t w) { return one ? ranks[w] : ws.before[w]; };
+    if (tid == 0)
+        below = U < t.pages ? rank_of(U / 64u) + (uint32_t)__popcll(word_of(U / 64u) & ((1ull << (U % 64u)) - 1ull)) : U;
     __syncthreads();
     const uint32_t kept = below;
-    for (uint32_t w = tid; w < (t.pages + 63u) / 64u; w += kScanThreads) {
-        const uint64_t busy = ws.busy[w];
-        const uint32_t p = w * 64u, rank = ws.before[w];
-        // free pages of this word below U
-        const uint64_t low = p + 64u <= U ? ~0ull : p < U ? (1ull << (U - p)) - 1ull : 0ull;
-        uint32_t r = p - rank;
-        for (uint64_t x = ~busy & low; x; x &= x - 1)
-            ws.hole[r++] = (int32_t)(p + (uint32_t)__ffsll((unsigned long long)x) - 1u);
-        r = rank + (uint32_t)__popcll(busy & low) - kept;  // busy pages at or above U before the word's first
-        for (uint64_t x = busy & ~low; x; x &= x - 1)
-            ws.mover[r++] = (int32_t)(p + (uint32_t)__ffsll((unsigned long long)x) - 1u);
+    for (uint32_t p = tid; p < t.pages; p += kScanThreads) {
+        const uint64_t word = word_of(p / 64u), bit = 1ull << (p % 64u);
+        const bool busy = word & bit;
+        if (busy == (p < U)) continue;                    // it stays as it is
+        const uint32_t rank = rank_of(p / 64u) + (uint32_t)__popcll(word & (bit - 1ull));
+        if (busy) ws.mover[rank - kept] = (int32_t)p;
+        else ws.hole[p - rank] = (int32_t)p;
     }
     if (tid == 0) {
         ws.count[0] = U;
@@ -425,12 +473,19 @@ __global__ __launch_bounds__(kCopyThreads) void k_compact_move(const Table t, in
         }
         return;
     }
-    const uint64_t work = (uint64_t)moves * p.npool * p.parts;
-    for (uint64_t i = blockIdx.x - table_blocks; i < work; i += gridDim.x - table_blocks) {
-        const uint32_t part = (uint32_t)(i % p.parts);
-        const uint64_t r = i / p.parts;
-        const uint32_t m = (uint32_t)(r % moves), pool = (uint32_t)(r / moves);
-        copy_part(p, pool, ws.mover[m], ws.hole[m], part);
+    // work item (mover, pool, part), the parts of a page side by side
+    const uint32_t each = p.npool * p.parts, step = gridDim.x - table_blocks;
+    const uint32_t step_m = step / each, step_r = step - step_m * each;
+    uint32_t m = (blockIdx.x - table_blocks) / each, r = (blockIdx.x - table_blocks) - m * each;
+    while (m < moves) {
+        const uint32_t pool = r / p.parts;
+        copy_part<true>(p, pool, ws.mover[m], ws.hole[m], r - pool * p.parts);
+        m += step_m;
+        r += step_r;
+        if (r >= each) {
+            r -= each;
+            ++m;
+        }
     }
 }
 
@@ -495,12 +550,12 @@ static tmap_status pools_of(const tmap_t* maps, uint32_t npool, const page_table
 
 static uint64_t align16(uint64_t x) { return (x + 15) & ~15ull; }
 
-static uint64_t alloc_bytes(uint32_t pages, uint32_t n) { return 3 * align16(4ull * n) + align16(4ull * pages); }
+static uint64_t alloc_bytes(uint32_t pages, uint32_t n) { return 2 * align16(4ull * n) + align16(4ull * pages); }
 
 static AllocWs alloc_ws(void* ws, uint32_t n) {
     uint8_t* p = static_cast<uint8_t*>(ws);
     const uint64_t list = align16(4ull * n);
-    return {(int32_t*)p, (int32_t*)(p + list), (int32_t*)(p + 2 * list), (int32_t*)(p + 3 * list)};
+    return {(int32_t*)p, (int32_t*)(p + list), (int32_t*)(p + 2 * list)};
 }
 
 static uint64_t compact_bytes(uint32_t pages) {
