@@ -8,9 +8,12 @@
 // drops the whole turns and only then goes to fp32, so that the fraction of a
 // turn is right to fp32 precision at any int32 position.
 //
-// Bound: HBM.  A head's element is read once and written once; the cosine and
-// sine of a (token, pair) are computed once per workgroup, into LDS, and used
-// for every head of the token.
+// Bound: HBM, or the launch for a few tokens.  A head's element is read once
+// and written once; the cosine and sine of a (token, pair) are computed once
+// per workgroup, into LDS, and used for every head of the token.  8192 tokens of
+// 32 x 128 bf16 take 24 us (5.5 TB/s), the step that writes 8191 tokens' keys
+// and values to their pages 41 us (4.9 TB/s); 64 tokens' step 8.4 us, of which
+// the kernel is 6.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -22,6 +25,7 @@ namespace att {
 
 constexpr uint32_t kMaxPairs = 128;
 constexpr uint32_t kRopeThreads = 256;
+constexpr uint32_t kTokMax = 2;         // tokens of a workgroup
 
 struct RopePlan {
     double turns[kMaxPairs];   // turns per position of each pair
@@ -83,12 +87,13 @@ __device__ __forceinline__ void load_chunk(Chunk<T>& c, const gbyte* p, uint32_t
     }
 }
 
-template <typename T>
+template <bool STREAM, typename T>
 __device__ __forceinline__ void store_chunk(const Chunk<T>& c, gbyte* p, uint32_t n) {
     if (n == Chunk<T>::N) {
         u32x4 v;
         __builtin_memcpy(&v, &c, 16);
-        *(ATT_GLOBAL u32x4*)p = v;
+        if (STREAM) __builtin_nontemporal_store(v, (ATT_GLOBAL u32x4*)p);
+        else *(ATT_GLOBAL u32x4*)p = v;
     } else {
 #pragma unroll
         for (uint32_t i = 0; i < Chunk<T>::N; ++i)
@@ -96,10 +101,11 @@ __device__ __forceinline__ void store_chunk(const Chunk<T>& c, gbyte* p, uint32_
     }
 }
 
-template <typename T, int MODE>
+// STREAM: the call writes more than the L2s hold, so its output is not kept
+// there.
+template <typename T, int MODE, bool STREAM>
 __global__ __launch_bounds__(kRopeThreads) void k_rope(const RopeArgs a) {
     constexpr uint32_t N = Chunk<T>::N;
-    constexpr uint32_t kTokMax = 8;
     __shared__ float2 turn[kTokMax][kMaxPairs];   // magnitude * (cos, sin)
     __shared__ int2 where[kTokMax];               // page (-1: none) and slot
     const uint32_t tid = threadIdx.x;
@@ -223,8 +229,8 @@ __global__ __launch_bounds__(kRopeThreads) void k_rope(const RopeArgs a) {
                     ((ATT_GLOBAL T*)p)[e0] = x[i].e[0];
                     if (two) ((ATT_GLOBAL T*)p)[e1] = y[i].e[0];
                 } else {
-                    store_chunk(x[i], p + e0 * sizeof(T), n0);
-                    if (two) store_chunk(y[i], p + e1 * sizeof(T), N);
+                    store_chunk<STREAM>(x[i], p + e0 * sizeof(T), n0);
+                    if (two) store_chunk<STREAM>(y[i], p + e1 * sizeof(T), N);
                 }
             }
         }
@@ -246,17 +252,29 @@ static void launch_mode(RopeArgs& a, hipStream_t stream) {
         mode = ELEMENTS;
         a.units = rot / 2 + rest;
     }
-    // Tokens of a workgroup: as many as give each thread a cosine to compute,
-    // but one each while there are too few to fill the GPU.
+    // Tokens of a workgroup: two, which share its start, once each thread has
+    // work for them (8192 tokens of 32 x 128 bf16: 25.7 us with one, 24.2 with
+    // two, 25.9 with eight), but one each while there are too few to fill the GPU.
     const uint32_t most = a.units > rot / 2 ? a.units : rot / 2;
-    a.tok_block = kRopeThreads / (most ? most : 1u);
-    if (a.tok_block > 8u) a.tok_block = 8u;
-    if (a.tok_block < 1u || a.tokens < 1024u) a.tok_block = 1u;
+    a.tok_block = most > kRopeThreads / 2 || a.tokens < 1024u ? 1u : kTokMax;
     a.head_lanes = kRopeThreads / (a.units * a.tok_block);
+    // Beyond the L2s (8 x 4 MiB) the output is streamed: 8192 tokens as above
+    // 31 -> 26 us, the write of 8191 tokens to their pages 48 -> 43 us.
+    uint64_t heads = 0;
+    for (uint32_t i = 0; i < a.nseg; ++i) heads += a.seg[i].heads;
+    const bool stream_out = heads * a.tokens * a.dim * sizeof(T) > (32ull << 20);
     const dim3 grid((a.tokens + a.tok_block - 1) / a.tok_block), block(kRopeThreads);
-    if (mode == PAIRED) hipLaunchKernelGGL((k_rope<T, PAIRED>), grid, block, 0, stream, a);
-    else if (mode == SPLIT) hipLaunchKernelGGL((k_rope<T, SPLIT>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((k_rope<T, ELEMENTS>), grid, block, 0, stream, a);
+#define ATT_ROPE(MODE)                                                                           \
+    if (stream_out) hipLaunchKernelGGL((k_rope<T, MODE, true>), grid, block, 0, stream, a);      \
+    else hipLaunchKernelGGL((k_rope<T, MODE, false>), grid, block, 0, stream, a)
+    if (mode == PAIRED) {
+        ATT_ROPE(PAIRED);
+    } else if (mode == SPLIT) {
+        ATT_ROPE(SPLIT);
+    } else {
+        ATT_ROPE(ELEMENTS);
+    }
+#undef ATT_ROPE
 }
 
 static tmap_status launch_rope(RopeArgs& a, int32_t dtype, void* stream, const char* name) {
