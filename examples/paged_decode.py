@@ -141,7 +141,7 @@ def generate(steps=24, answers=8, prompt=300, every=8, slots=16, seed=0):
 
     top = last.topk(answers)
     token, score = top.indices.clone(), top.values.log_softmax(0)         # the answers' first tokens
-    history = token[:, None]
+    history = token[:, None].clone()
     rows = ints(range(1, answers + 1))
     step = Runner(model, cache, rows, 1, prompt, steps)                  # reads `rows` on the device
 
