@@ -480,10 +480,14 @@ __device__ __forceinline__ void place_key(cargs& a, uint32_t head, uint32_t key,
 template <uint32_t DP, uint32_t STEP, bool VALUES>
 struct RowCopy {
     uint32_t first, dim;
+    // Rows from one of the wave's groups to the next; where that is a whole
+    // number of periods of the rows' key, a lane's chunk is the same in all.
+    static constexpr uint32_t rows = STEP * 64u / Geo<DP>::cpr;
+    static constexpr bool same = STEP * 64u % Geo<DP>::cpr == 0 && rows % (VALUES ? 4u : 16u) == 0;
     __device__ __forceinline__ uint32_t chunk(uint32_t n, uint32_t& row) const {
-        const uint32_t i = (first + n * STEP) * 64u + lane_id();
-        row = i / Geo<DP>::cpr;
-        return (i - row * Geo<DP>::cpr) ^ (VALUES ? Geo<DP>::key_v(row) : Geo<DP>::key_k(row));
+        const uint32_t i = (first + (same ? 0u : n * STEP)) * 64u + lane_id(), r = i / Geo<DP>::cpr;
+        row = r + (same ? n * rows : 0u);
+        return (i - r * Geo<DP>::cpr) ^ (VALUES ? Geo<DP>::key_v(r) : Geo<DP>::key_k(r));
     }
     __device__ __forceinline__ uint64_t source(uint32_t n, const uint64_t* addr) const {
         uint32_t row;
@@ -807,7 +811,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_attn(const Attn
 template <typename T, uint32_t DP>
 __global__ __launch_bounds__(kThreads) void k_attn_join(const AttnArgs) {
     cargs& a = kernel_args();
-    constexpr uint32_t U = 8;                                             // parts in flight
+    constexpr uint32_t U = 16;                                            // parts in flight
     const uint32_t lane = lane_id(), n32 = lane % 32u, hh = lane / 32u;
     const uint32_t head = blockIdx.x / a.blocks_all, block = blockIdx.x - head * a.blocks_all;
     const uint32_t f = blockIdx.y * kWaves + threadIdx.x / 64u;
