@@ -17,6 +17,18 @@
 // already lie as the second product's B operand (values transposed x weights)
 // if that product takes its keys in the order 0-3, 8-11 | 4-7, 12-15, which
 // the transposing LDS read of the values delivers for free.
+//
+// What bounds it.  128 sequences of 32 heads over 8 key / value heads, dim
+// 128, behind 32768 shared tokens, up to 1024 own: 128 us.  The products are
+// 70 Gflop (50 us at the 1.4 Pflop/s of a large library product), the keys and
+// values 404 MB (78 us at a large copy's 5.2 TB/s; read alone, the own tokens
+// take 60 us, 4.5 TB/s).  A tile of the prefix takes a wave 2660 cycles, of
+// which its 32 products are 1050 and its weights' arithmetic is hidden behind
+// them; the rest is the tile's meeting point, its copies and their latency,
+// with one such wave on a SIMD.  Two waves each bring the tile to 1600 cycles
+// but leave no place for the own tokens' loads beside them, and come out
+// slower together.  A few short sequences take 12 us: two launches, three
+// dependent reads before the first product, the join.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -893,17 +905,30 @@ static uint64_t plan(AttnArgs* a, uint64_t* groups_out) {
     a->rows_all = (uint32_t)rows_all;
     a->blocks_own = (uint32_t)ceil_div(rows_own, kRows);
     a->blocks_all = (uint32_t)ceil_div(rows_all, kRows);
-    a->shared = rows_all > 2 * kRows;
+    // Four waves share the prefix's tiles where the product is large; otherwise
+    // each has its own, which is read again for every 32 rows but needs no
+    // meeting (8 key / value heads, own tiles first: 64 rows behind 16384 tokens
+    // 24.4 and 25.3 us, 128 rows 31.1 and 28.2; 256 rows behind 4096 23.1 and
+    // 26.2, 512 rows 37.4 and 32.1).
+    a->shared = rows_all > 2 * kRows && a->kv * rows_all * a->prefix_len > 10000000;
     const uint64_t blocks = ceil_div(rows_all, a->shared ? kWgRows : kRows);
+    // One workgroup on the prefix for each compute unit, so that the sequences'
+    // own tokens are read beside it: two each are 17 % slower at 128 sequences
+    // behind 32768 tokens, half as many 75 %.  Parts of 256 keys and above: each
+    // is joined once more (64 rows behind 4096 tokens: parts of 128 keys 19.7 us,
+    // 256 17.1, 512 18.8).
     a->parts_all = 0;
     if (a->prefix_len) {
-        const uint64_t most = ceil_div(a->prefix_len, 128), want = cus / (a->kv * blocks);
+        const uint64_t most = ceil_div(a->prefix_len, 256), want = cus / (a->kv * blocks);
         a->parts_all = (uint32_t)(want < 1 ? 1 : want < most ? want : most);
     }
     a->units_all = a->kv * a->parts_all;
     const uint64_t wg_all = ceil_div(a->units_all, 8) * 8 * blocks;
     const uint64_t jobs = batch * a->kv * a->blocks_own;
-    const uint64_t most = ceil_div(a->hint ? a->hint : 1, 256), want = room / jobs;
+    // Without a prefix one part needs no second launch: 512 tokens of 64 elements
+    // 9.8 us in one part and 11.3 in two, 1024 tokens 12.9 and 11.6 in four.
+    const bool one = a->prefix_len == 0 && a->hint <= 512;
+    const uint64_t most = one ? 1 : ceil_div(a->hint ? a->hint : 1, 256), want = room / jobs;
     a->parts_own = (uint32_t)(want < 1 ? 1 : want < most ? want : most);
     a->direct = a->parts_all == 0 && a->parts_own == 1;
     const uint64_t first = (uint64_t)a->units_all * a->blocks_all, own = jobs * a->parts_own;

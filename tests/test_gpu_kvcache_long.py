@@ -65,6 +65,10 @@ LONG = [  # as ATTN in test_gpu_kvcache.py
     # own tokens past one placement, in one part (hint 0) or several
     ("bf16", 2, 1, 4, 2, 128, 48, 70, [1300, 700], True, 0),
     ("f16", 3, 3, 2, 1, 256, 16, 0, [1100, 2, 513], False, 0),
+    # products large enough for shared tiles: kv * rows * prefix above 10^7
+    ("bf16", 40, 2, 64, 64, 64, 16, 2100, [(5 * i) % 60 for i in range(40)], False, 0),
+    ("f16", 50, 1, 96, 48, 96, 7, 2301, [(7 * i) % 33 for i in range(50)], True, 8),
+    ("bf16", 70, 1, 16, 16, 200, 48, 9001, [i % 3 for i in range(70)], False, 0),
     # few rows behind a long prefix: each wave has tiles of its own
     ("bf16", 3, 1, 8, 2, 80, 5, 3001, [3, 0, 40], False, 0),
 ]
@@ -81,11 +85,11 @@ def test_attention_long(case, hint):
     base.attn_check(got, lse, q, kp, vp, table, lens, rows, slots, prefix, scale, dtype)
 
 
-@pytest.mark.parametrize("rows_of_queries", [70, 3])
-def test_bad_pages_in_a_long_prefix(rows_of_queries):
+@pytest.mark.parametrize("rows_of_queries, kv", [(70, 2), (3, 2), (70, 160)])
+def test_bad_pages_in_a_long_prefix(rows_of_queries, kv):
     """Entries of the prefix that are not pages: their keys are not there, for
     every query, and the others' weights do not change."""
-    c = ("bf16", rows_of_queries, 1, 2, 2, 64, 16, 1000, [3] * rows_of_queries, False, 0)
+    c = ("bf16", rows_of_queries, 1, kv, kv, 64, 16, 1000, [3] * rows_of_queries, False, 0)
     q, kp, vp, table, lens, rows = base.attn_setup(c, base.gen(9))
     bad = table.copy()
     bad[1, [0, 17, 40]] = [-1, kp.shape[0], 2 ** 31 - 1]
@@ -102,14 +106,14 @@ def test_bad_pages_in_a_long_prefix(rows_of_queries):
     base.attn_check(got, lse, q, kp, vp, short, lens, rows, 16, 1000 - 48, 0.125, "bf16")
 
 
-@pytest.mark.parametrize("batch", [80, 2])
-def test_values_that_are_not_finite_stay_in_their_column(batch):
+@pytest.mark.parametrize("batch, kv", [(80, 1), (2, 1), (80, 500)])
+def test_values_that_are_not_finite_stay_in_their_column(batch, kv):
     """An infinity among the prefix's values that every query sees: infinite in
     its element, the others as they are."""
-    c = ("f16", batch, 1, 2, 1, 64, 16, 300, [5] * batch, False, 0)
+    c = ("f16", batch, 1, kv if kv > 1 else 2, kv, 64, 16, 300, [5] * batch, False, 0)
     q, kp, vp, table, lens, rows = base.attn_setup(c, base.gen(10))
     clean, lse = base.attn_run(q, kp, vp, table, lens, rows, 16, 300, 0.125, "f16")
-    vp[int(table[1][7]), 3, 0, 11] = math.inf
+    vp[int(table[1][7]), 3, :, 11] = math.inf
     got, lse2 = base.attn_run(q, kp, vp, table, lens, rows, 16, 300, 0.125, "f16")
     assert np.isposinf(got[..., 11]).all()
     got[..., 11] = clean[..., 11]
