@@ -40,14 +40,26 @@ static Table table_of(const page_table_t* pt) {
 
 // The pools of one geometry: a page is n2 x n1 rows of row_bytes (dimensions
 // that lie packed are merged, so a page without gaps is one row).
-struct Pools {
-    uint64_t base[kMaxPools];
+// Kernels take a few of them where that is enough: a launch costs the host
+// 0.7 us more for each KiB of arguments.
+template <uint32_t N>
+struct PoolsOf {
     int64_t page;                 // bytes from one page to the next
     int64_t s1, s2;
     uint32_t npool, n1, n2;
     uint32_t row_bytes, row_chunks, chunks, parts;
     uint32_t magic_row, magic_n1; // multiply-high divisors, 0 for 1
+    uint64_t base[N];
 };
+constexpr uint32_t kFewPools = 16;
+typedef PoolsOf<kMaxPools> Pools;
+typedef PoolsOf<kFewPools> FewPools;
+
+static FewPools few(const Pools& p) {
+    FewPools f;
+    std::memcpy(&f, &p, sizeof(f));       // the same fields, fewer bases
+    return f;
+}
 
 // ---- copying -------------------------------------------------------------------
 
@@ -60,8 +72,8 @@ __device__ __forceinline__ uint32_t div_by(uint32_t n, uint32_t d, uint32_t magi
 // One part (16 KiB) of one page, by 256 threads: the loads of a thread's four
 // chunks are in flight together.  STREAM: the pages are many more than the
 // caches hold, so neither side is kept there.
-template <bool STREAM>
-__device__ __forceinline__ void copy_part(const Pools& p, uint32_t pool, int64_t from, int64_t to, uint32_t part) {
+template <bool STREAM, uint32_t N>
+__device__ __forceinline__ void copy_part(const PoolsOf<N>& p, uint32_t pool, int64_t from, int64_t to, uint32_t part) {
     const gbyte* src = gptr(p.base[pool]) + from * p.page;
     gbyte* dst = gptr(p.base[pool]) + to * p.page;
     u32x4 v[4];
@@ -90,7 +102,8 @@ __device__ __forceinline__ void copy_part(const Pools& p, uint32_t pool, int64_t
     }
 }
 
-__global__ __launch_bounds__(kCopyThreads) void k_page_copy(const Pools p, const int32_t* src, const int32_t* dst,
+template <uint32_t N>
+__global__ __launch_bounds__(kCopyThreads) void k_page_copy(const PoolsOf<N> p, const int32_t* src, const int32_t* dst,
                                                             uint32_t pages, uint32_t* err) {
     const uint32_t i = blockIdx.x / p.parts, part = blockIdx.x - i * p.parts;
     const int32_t from = src[i], to = dst[i];
@@ -316,7 +329,8 @@ __global__ __launch_bounds__(kScanThreads) void k_hand_out(const Table t, const 
 // Rows and data of a fork, after k_hand_out.  blockIdx.x: the entry; y: pieces
 // of 1024 table entries first, then parts of the unfinished page, pool after
 // pool.
-__global__ __launch_bounds__(kCopyThreads) void k_fork_rows(const Table t, const Pools p, const int32_t* src,
+template <uint32_t N>
+__global__ __launch_bounds__(kCopyThreads) void k_fork_rows(const Table t, const PoolsOf<N> p, const int32_t* src,
                                                             const int32_t* dst, AllocWs ws, uint32_t pieces,
                                                             uint32_t* err) {
     const uint32_t i = blockIdx.x;
@@ -447,8 +461,9 @@ __device__ __forceinline__ int32_t new_place(const CompactWs& ws, uint32_t page,
 
 // The first table_blocks workgroups rewrite the table and the counts, the
 // others move the pages.
+template <uint32_t N>
 __global__ __launch_bounds__(kCopyThreads) void k_compact_move(const Table t, int32_t* table_out, uint64_t pitch_out,
-                                                               int32_t* refs_out, const Pools p, CompactWs ws,
+                                                               int32_t* refs_out, const PoolsOf<N> p, CompactWs ws,
                                                                uint32_t table_blocks, uint32_t* err) {
     const uint32_t U = ws.count[0], moves = ws.count[1];
     if (blockIdx.x < table_blocks) {
@@ -612,8 +627,10 @@ extern "C" tmap_status page_copy(const tmap_t* pools, uint32_t npool, const int3
     uint32_t* err = nullptr;
     st = device_error_word(&err);
     if (st) return st;
-    hipLaunchKernelGGL(k_page_copy, dim3(n * p.parts, npool), dim3(kCopyThreads), 0, as_stream(stream), p, d_src,
-                       d_dst, pages, err);
+    const dim3 grid(n * p.parts, npool), block(kCopyThreads);
+    const hipStream_t s = as_stream(stream);
+    if (npool <= kFewPools) hipLaunchKernelGGL(k_page_copy, grid, block, 0, s, few(p), d_src, d_dst, pages, err);
+    else hipLaunchKernelGGL(k_page_copy, grid, block, 0, s, p, d_src, d_dst, pages, err);
     return check_launch("page_copy");
 }
 
@@ -659,8 +676,11 @@ extern "C" tmap_status page_fork(const page_table_t* pt, const tmap_t* pools, ui
                        d_dst, n, d_ok, ws, err);
     st = check_launch("page_fork");
     if (st) return st;
-    hipLaunchKernelGGL(k_fork_rows, dim3(n, (uint32_t)gy), dim3(kCopyThreads), 0, as_stream(stream), table_of(pt), p,
-                       d_src, d_dst, ws, pieces, err);
+    const dim3 grid(n, (uint32_t)gy), block(kCopyThreads);
+    const hipStream_t s = as_stream(stream);
+    if (npool <= kFewPools)
+        hipLaunchKernelGGL(k_fork_rows, grid, block, 0, s, table_of(pt), few(p), d_src, d_dst, ws, pieces, err);
+    else hipLaunchKernelGGL(k_fork_rows, grid, block, 0, s, table_of(pt), p, d_src, d_dst, ws, pieces, err);
     return check_launch("page_fork");
 }
 
@@ -713,7 +733,13 @@ extern "C" tmap_status page_compact(const page_table_t* from, const page_table_t
     const uint32_t table_blocks = (uint32_t)(tb < 4ull * cus ? tb : 4ull * cus);
     const uint64_t most = ((uint64_t)from->pages / 2) * npool * p.parts;
     const uint32_t movers = (uint32_t)(most < 8ull * cus ? most : 8ull * cus);
-    hipLaunchKernelGGL(k_compact_move, dim3(table_blocks + movers), dim3(kCopyThreads), 0, as_stream(stream),
-                       table_of(from), to->d_table, to->pitch, to->d_refs, p, ws, table_blocks, err);
+    const dim3 grid(table_blocks + movers), block(kCopyThreads);
+    const hipStream_t s = as_stream(stream);
+    if (npool <= kFewPools)
+        hipLaunchKernelGGL(k_compact_move, grid, block, 0, s, table_of(from), to->d_table, to->pitch, to->d_refs,
+                           few(p), ws, table_blocks, err);
+    else
+        hipLaunchKernelGGL(k_compact_move, grid, block, 0, s, table_of(from), to->d_table, to->pitch, to->d_refs, p,
+                           ws, table_blocks, err);
     return check_launch("page_compact");
 }

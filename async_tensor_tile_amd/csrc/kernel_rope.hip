@@ -46,8 +46,15 @@ struct RopeSeg {
     uint32_t rotate;
 };
 
+// The plan's frequencies as a kernel takes them.  A launch costs the host about
+// 0.7 us more for each KiB of arguments, so a small call passes only as many as
+// it needs.
+template <uint32_t P>
+struct RopeTurns {
+    double turns[P];
+};
+
 struct RopeArgs {
-    RopePlan plan;
     RopeSeg seg[3];
     const int32_t* pos;
     const int32_t* rows;            // pools: row and token index of each token
@@ -55,7 +62,9 @@ struct RopeArgs {
     const int32_t* table;
     uint64_t pitch;
     uint32_t* err;
-    uint32_t nseg, tokens, dim, inverse;
+    float magnitude, sine;          // of the cosine and the sine (whose sign turns for the inverse)
+    uint32_t rot;
+    uint32_t nseg, tokens, dim;
     uint32_t table_rows, row_pages, pages, slots;
     uint32_t units, tok_block, head_lanes;
     uint32_t in_place;
@@ -103,23 +112,23 @@ __device__ __forceinline__ void store_chunk(const Chunk<T>& c, gbyte* p, uint32_
 
 // STREAM: the call writes more than the L2s hold, so its output is not kept
 // there.
-template <typename T, int MODE, bool STREAM>
-__global__ __launch_bounds__(kRopeThreads) void k_rope(const RopeArgs a) {
+template <typename T, int MODE, bool STREAM, uint32_t P>
+__global__ __launch_bounds__(kRopeThreads) void k_rope(const RopeTurns<P> plan, const RopeArgs a) {
     constexpr uint32_t N = Chunk<T>::N;
-    __shared__ float2 turn[kTokMax][kMaxPairs];   // magnitude * (cos, sin)
+    __shared__ float2 turn[kTokMax][P];           // magnitude * (cos, sin)
     __shared__ int2 where[kTokMax];               // page (-1: none) and slot
     const uint32_t tid = threadIdx.x;
     const uint32_t t0 = blockIdx.x * a.tok_block;
-    const uint32_t pairs = a.plan.rot / 2;
+    const uint32_t pairs = a.rot / 2;
     for (uint32_t i = tid; i < a.tok_block * pairs; i += kRopeThreads) {
         const uint32_t k = i / pairs, j = i - k * pairs;
         if (t0 + k < a.tokens) {
-            const double p = (double)a.pos[t0 + k], f = a.plan.turns[j];
+            const double p = (double)a.pos[t0 + k], f = plan.turns[j];
             const double whole = p * f;
             const double part = (whole - rint(whole)) + fma(p, f, -whole);
             float s, c;
             sincospif(2.0f * (float)part, &s, &c);
-            turn[k][j] = make_float2(a.plan.magnitude * c, (a.inverse ? -a.plan.magnitude : a.plan.magnitude) * s);
+            turn[k][j] = make_float2(a.magnitude * c, a.sine * s);
         }
     }
     if (a.table && tid < a.tok_block && t0 + tid < a.tokens) {
@@ -148,12 +157,12 @@ __global__ __launch_bounds__(kRopeThreads) void k_rope(const RopeArgs a) {
     if (MODE == PAIRED) {
         e0 = u * N;
         pair0 = e0 / 2;
-        turned = e0 < a.plan.rot;
+        turned = e0 < a.rot;
         two = false;
     } else {
         const uint32_t half = pairs / per;                // units that hold a pair
         two = u < half;
-        e0 = two ? u * per : a.plan.rot + (u - half) * per;
+        e0 = two ? u * per : a.rot + (u - half) * per;
         e1 = e0 + pairs;
         pair0 = e0;
         turned = two;
@@ -237,12 +246,28 @@ __global__ __launch_bounds__(kRopeThreads) void k_rope(const RopeArgs a) {
     }
 }
 
+template <typename T, int MODE, bool STREAM, uint32_t P>
+static void launch_pairs(const RopePlan& plan, const RopeArgs& a, hipStream_t stream) {
+    RopeTurns<P> turns;
+    std::memcpy(&turns, plan.turns, sizeof(turns));
+    const dim3 grid((a.tokens + a.tok_block - 1) / a.tok_block);
+    hipLaunchKernelGGL((k_rope<T, MODE, STREAM, P>), grid, dim3(kRopeThreads), 0, stream, turns, a);
+}
+
+template <typename T, int MODE>
+static void launch_size(const RopePlan& plan, const RopeArgs& a, bool stream_out, hipStream_t stream) {
+    if (stream_out) launch_pairs<T, MODE, true, kMaxPairs>(plan, a, stream);
+    else if (a.rot <= 64) launch_pairs<T, MODE, false, 32>(plan, a, stream);
+    else if (a.rot <= 128) launch_pairs<T, MODE, false, 64>(plan, a, stream);
+    else launch_pairs<T, MODE, false, kMaxPairs>(plan, a, stream);
+}
+
 template <typename T>
-static void launch_mode(RopeArgs& a, hipStream_t stream) {
+static void launch_mode(const RopePlan& plan, RopeArgs& a, hipStream_t stream) {
     constexpr uint32_t N = 16 / sizeof(T);
-    const uint32_t rot = a.plan.rot, rest = a.dim - rot;
+    const uint32_t rot = a.rot, rest = a.dim - rot;
     int mode;
-    if (a.plan.layout == ROPE_INTERLEAVED) {
+    if (plan.layout == ROPE_INTERLEAVED) {
         mode = PAIRED;
         a.units = (a.dim + N - 1) / N;
     } else if (rot / 2 % N == 0) {
@@ -263,25 +288,20 @@ static void launch_mode(RopeArgs& a, hipStream_t stream) {
     uint64_t heads = 0;
     for (uint32_t i = 0; i < a.nseg; ++i) heads += a.seg[i].heads;
     const bool stream_out = heads * a.tokens * a.dim * sizeof(T) > (32ull << 20);
-    const dim3 grid((a.tokens + a.tok_block - 1) / a.tok_block), block(kRopeThreads);
-#define ATT_ROPE(MODE)                                                                           \
-    if (stream_out) hipLaunchKernelGGL((k_rope<T, MODE, true>), grid, block, 0, stream, a);      \
-    else hipLaunchKernelGGL((k_rope<T, MODE, false>), grid, block, 0, stream, a)
-    if (mode == PAIRED) {
-        ATT_ROPE(PAIRED);
-    } else if (mode == SPLIT) {
-        ATT_ROPE(SPLIT);
-    } else {
-        ATT_ROPE(ELEMENTS);
-    }
-#undef ATT_ROPE
+    if (mode == PAIRED) launch_size<T, PAIRED>(plan, a, stream_out, stream);
+    else if (mode == SPLIT) launch_size<T, SPLIT>(plan, a, stream_out, stream);
+    else launch_size<T, ELEMENTS>(plan, a, stream_out, stream);
 }
 
-static tmap_status launch_rope(RopeArgs& a, int32_t dtype, void* stream, const char* name) {
+static tmap_status launch_rope(const RopePlan& plan, RopeArgs& a, bool inverse, int32_t dtype, void* stream,
+                               const char* name) {
+    a.rot = plan.rot;
+    a.magnitude = plan.magnitude;
+    a.sine = inverse ? -plan.magnitude : plan.magnitude;
     switch (dtype) {
-    case TMAP_F16: launch_mode<_Float16>(a, as_stream(stream)); break;
-    case TMAP_BF16: launch_mode<__bf16>(a, as_stream(stream)); break;
-    default: launch_mode<float>(a, as_stream(stream)); break;
+    case TMAP_F16: launch_mode<_Float16>(plan, a, as_stream(stream)); break;
+    case TMAP_BF16: launch_mode<__bf16>(plan, a, as_stream(stream)); break;
+    default: launch_mode<float>(plan, a, as_stream(stream)); break;
     }
     return check_launch(name);
 }
@@ -357,8 +377,8 @@ extern "C" tmap_status rope_apply(const rope_t* r, const tmap_t* x, const tmap_t
     if (st == TMAP_OK) st = view_of(y, 3, &vy, &ty);
     if (st) return st;
     if (!rope_type(tx)) return TMAP_ERR_DTYPE;
-    a.plan = load_plan(r);
-    if (ty != tx || !same_dims(vx, vy) || a.plan.rot < 2 || !heads_fit(vx, a.plan.rot)) return TMAP_ERR_UNSUPPORTED;
+    const RopePlan plan = load_plan(r);
+    if (ty != tx || !same_dims(vx, vy) || plan.rot < 2 || !heads_fit(vx, plan.rot)) return TMAP_ERR_UNSUPPORTED;
     a.in_place = vx.base == vy.base;
     if (a.in_place && (vx.stride[1] != vy.stride[1] || vx.stride[2] != vy.stride[2])) return TMAP_ERR_UNSUPPORTED;
     a.seg[0] = tensor_seg(vx, vy);
@@ -366,8 +386,7 @@ extern "C" tmap_status rope_apply(const rope_t* r, const tmap_t* x, const tmap_t
     a.pos = d_pos;
     a.tokens = (uint32_t)vx.dim[2];
     a.dim = (uint32_t)vx.dim[0];
-    a.inverse = inverse != 0;
-    return launch_rope(a, tx, stream, "rope_apply");
+    return launch_rope(plan, a, inverse != 0, tx, stream, "rope_apply");
 }
 
 extern "C" tmap_status rope_append(const rope_t* r, const tmap_t* q, const tmap_t* q_out, const tmap_t* k,
@@ -387,10 +406,12 @@ extern "C" tmap_status rope_append(const rope_t* r, const tmap_t* q, const tmap_
     if (st == TMAP_OK) st = check_table(pt);
     if (st) return st;
     if (!rope_type(tk)) return TMAP_ERR_DTYPE;
-    if (r) a.plan = load_plan(r);
-    if (r && a.plan.rot < 2) return TMAP_ERR_UNSUPPORTED;
+    RopePlan plan;
+    std::memset(&plan, 0, sizeof(plan));
+    if (r) plan = load_plan(r);
+    if (r && plan.rot < 2) return TMAP_ERR_UNSUPPORTED;
     if (tv != tk || tpk != tk || tpv != tk || !same_dims(vk, vv) || !same_dims(pk, pv) ||
-        !heads_fit(vk, a.plan.rot) || pk.dim[0] != vk.dim[0] || pk.dim[2] != vk.dim[1] ||
+        !heads_fit(vk, plan.rot) || pk.dim[0] != vk.dim[0] || pk.dim[2] != vk.dim[1] ||
         pk.dim[1] != pt->slots || pk.dim[3] != pt->pages)
         return TMAP_ERR_UNSUPPORTED;
     if (q) {
@@ -399,7 +420,7 @@ extern "C" tmap_status rope_append(const rope_t* r, const tmap_t* q, const tmap_
         st = view_of(q, 3, &vq, &tq);
         if (st == TMAP_OK) st = view_of(q_out, 3, &vo, &to);
         if (st) return st;
-        if (tq != tk || to != tk || !same_dims(vq, vo) || !heads_fit(vq, a.plan.rot) || vq.dim[0] != vk.dim[0] ||
+        if (tq != tk || to != tk || !same_dims(vq, vo) || !heads_fit(vq, plan.rot) || vq.dim[0] != vk.dim[0] ||
             vq.dim[2] != vk.dim[2])
             return TMAP_ERR_UNSUPPORTED;
         if (vq.base == vo.base && (vq.stride[1] != vo.stride[1] || vq.stride[2] != vo.stride[2]))
@@ -421,5 +442,5 @@ extern "C" tmap_status rope_append(const rope_t* r, const tmap_t* q, const tmap_
     a.dim = (uint32_t)vk.dim[0];
     st = device_error_word(&a.err);
     if (st) return st;
-    return launch_rope(a, tk, stream, "rope_append");
+    return launch_rope(plan, a, false, tk, stream, "rope_append");
 }
