@@ -287,11 +287,14 @@ struct Wave {
 
     // The sums are only rescaled when a score passes the largest of before by
     // 2^kLazy; weights then stay below 2^kLazy, which both types hold.
-    // Returns what weights are taken relative to.
+    // Returns what weights are taken relative to.  Each query goes by its own
+    // scores, so its result does not depend on the others of the wave.  A top
+    // that is NaN (no score is a number) makes the sums NaN, as it has to.
     __device__ __forceinline__ float rescale(float top) {
-        if (__any(top > m + kLazy)) {
-            const float next = fmaxf(m, top), fade = next == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - next);
-            m = next;
+        const bool pass = !(top <= m + kLazy);
+        if (__any(pass)) {
+            const float fade = pass ? __builtin_amdgcn_exp2f(m - top) : 1.0f;
+            m = pass ? top : m;
             l *= fade;
 #pragma unroll
             for (uint32_t i = 0; i < NO; ++i) o[i] *= fade;
@@ -855,15 +858,14 @@ __global__ __launch_bounds__(kThreads) void k_attn_join(const AttnArgs) {
         float next = m;
 #pragma unroll
         for (uint32_t u = 0; u < U; ++u) next = fmaxf(next, ml[u].x);
-        if (next == -INFINITY) continue;
-        const float fade = __builtin_amdgcn_exp2f(m - next);
+        const float at = next == -INFINITY ? 0.0f : next, fade = __builtin_amdgcn_exp2f(m - at);
         acc *= fade;
         l *= fade;
         m = next;
 #pragma unroll
         for (uint32_t u = 0; u < U; ++u) {
-            if (ml[u].x == -INFINITY) continue;                           // a part that saw no key left no sums
-            const float w = __builtin_amdgcn_exp2f(ml[u].x - m);
+            if (ml[u].y == 0.0f) continue;                                // a part that saw no key left no sums
+            const float w = __builtin_amdgcn_exp2f(ml[u].x - at);
             l += w * ml[u].y;
             acc += x[u] * w;
         }

@@ -118,3 +118,22 @@ def test_values_that_are_not_finite_stay_in_their_column(batch, kv):
     assert np.isposinf(got[..., 11]).all()
     got[..., 11] = clean[..., 11]
     assert np.array_equal(got, clean) and np.array_equal(lse, lse2)
+
+
+@pytest.mark.parametrize("batch, kv, prefix", [(80, 500, 300), (3, 2, 300), (3, 2, 2000), (3, 2, 0)])
+@pytest.mark.parametrize("where", ["query", "key"])
+def test_scores_that_are_not_numbers(batch, kv, prefix, where):
+    """A NaN in a query makes all of its scores NaN, one in a key that it sees
+    one of them: its result and sum are NaN in either case, the other queries'
+    are as they were."""
+    c = ("bf16", batch, 1, kv, kv, 64, 16, prefix, [20] * batch, False, 0)
+    q, kp, vp, table, lens, rows = base.attn_setup(c, base.gen(11))
+    clean, lse = base.attn_run(q, kp, vp, table, lens, rows, 16, prefix, 0.125, "bf16")
+    if where == "query":
+        q[1, 0, 1, 5] = math.nan
+    else:
+        kp[int(table[rows[1]][1]), 2, 1, 5] = math.nan
+    got, lse2 = base.attn_run(q, kp, vp, table, lens, rows, 16, prefix, 0.125, "bf16")
+    assert np.isnan(got[1, 0, 1]).all() and np.isnan(lse2[1, 0, 1])
+    got[1, 0, 1], lse2[1, 0, 1] = clean[1, 0, 1], lse[1, 0, 1]
+    assert np.array_equal(got, clean) and np.array_equal(lse2, lse)
