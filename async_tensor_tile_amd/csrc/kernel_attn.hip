@@ -19,16 +19,18 @@
 // the transposing LDS read of the values delivers for free.
 //
 // What bounds it.  128 sequences of 32 heads over 8 key / value heads, dim
-// 128, behind 32768 shared tokens, up to 1024 own: 128 us.  The products are
-// 70 Gflop (50 us at the 1.4 Pflop/s of a large library product), the keys and
-// values 404 MB (78 us at a large copy's 5.2 TB/s; read alone, the own tokens
-// take 60 us, 4.5 TB/s).  A tile of the prefix takes a wave 2660 cycles, of
-// which its 32 products are 1050 and its weights' arithmetic is hidden behind
-// them; the rest is the tile's meeting point, its copies and their latency,
-// with one such wave on a SIMD.  Two waves each bring the tile to 1600 cycles
-// but leave no place for the own tokens' loads beside them, and come out
-// slower together.  A few short sequences take 12 us: two launches, three
-// dependent reads before the first product, the join.
+// 128, behind 32768 shared tokens, up to 1024 own: 122 to 128 us.  The products
+// are 70 Gflop (50 us at the 1.4 Pflop/s of a large library product), the keys
+// and values 404 MB (78 us at a large copy's 5.2 TB/s; read alone, the own
+// tokens take 60 us, 4.5 TB/s).  A tile of the prefix takes a wave 2660 cycles
+// at 2.1 GHz, of which its 32 products are 1050 (34 % of the matrix cores' time
+// over the launch); the weights' arithmetic costs 380 beside them, the copies
+// 550, where the keys lie 170, and the rest is the tile's meeting point and the
+// waits between its parts, with one such wave on a SIMD.  Two waves each bring
+// the tile to 1600 cycles, at 1.9 GHz, but leave no place for the own tokens'
+// loads beside them, and come out slower together.  A few short sequences take
+// 11.5 us: two launches, three dependent reads before the first product, the
+// join.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
