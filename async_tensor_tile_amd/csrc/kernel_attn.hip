@@ -472,8 +472,11 @@ struct Wave {
     __device__ __forceinline__ float total() const { return add_halves(l); }
 };
 
-// Where keys base .. base + kSegment * count of a row lie.  Thread after
-// thread a key; what is not a page of the pool is recorded and left out.
+// Where the keys of a row lie, thread after thread a key: first its page, then
+// its addresses; what is not a page of the pool is recorded and left out.
+// The division by the page's slots is the compiler's: by a multiplication with
+// a reciprocal from the host, 128 sequences behind 32768 keys took 136.6 us
+// against 135.4.
 __device__ __forceinline__ int32_t page_of_key(cargs& a, uint32_t row, uint32_t key, uint32_t end) {
     if (key >= end) return -1;
     return *(const ATT_GLOBAL int32_t*)(gptr(a.table) + ((uint64_t)row * a.pitch + key / a.slots) * 4u);
