@@ -1027,8 +1027,11 @@ __device__ __forceinline__ void txbar_init(TxBar* b, int32_t count) {
 }
 
 // Applies (d_arrivals, d_bytes); returns the state right after this
-// operation (phase already flipped if it completed the phase).
+// operation (phase already flipped if it completed the phase).  The phase of an
+// operation that does not complete it is read before the operation: until
+// then the phase waits for it, while right afterwards the others may complete it.
 __device__ __forceinline__ TxState txbar_op(TxBar* b, int32_t d_arrivals, int32_t d_bytes) {
+    const uint32_t phase = __hip_atomic_load(&b->phase, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
     const int64_t delta = ((int64_t)d_arrivals << 32) + (int64_t)d_bytes;
     const int64_t old = __hip_atomic_fetch_add(&b->state, delta, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_WORKGROUP);
     const int64_t now = old + delta;
@@ -1043,7 +1046,7 @@ __device__ __forceinline__ TxState txbar_op(TxBar* b, int32_t d_arrivals, int32_
     } else {
         s.pending = (int32_t)(uint32_t)(uint64_t)now;
         s.arrivals_left = (int32_t)((now - (int64_t)s.pending) >> 32);
-        s.phase = __hip_atomic_load(&b->phase, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+        s.phase = phase;
     }
     return s;
 }
