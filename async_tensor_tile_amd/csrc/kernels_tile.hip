@@ -169,7 +169,9 @@ __global__ __launch_bounds__(kBatchThreads) void k_tile_store(tmap_t map, const 
 // Byte-counted barrier self-test: one barrier (arrival count 1) completes
 // after `ntile` copies signal their own byte counts.  Trace records are
 // (who, arrivals_left, pending, phase); who = -1 init, -2 arrive.expect_tx,
-// t >= 0 the complete-tx of tile t.
+// t >= 0 the complete-tx of tile t.  The slot of a completion follows from the
+// bytes that its own barrier operation left pending, so the records stand in
+// the order of the operations, however the waves go on after them.
 __global__ __launch_bounds__(kBatchThreads) void k_txbar_selftest(tmap_t map, const int32_t* __restrict__ coords,
                                                                  uint32_t ntile, int32_t* __restrict__ trace,
                                                                  uint8_t* __restrict__ out, uint32_t img_stride,
@@ -177,15 +179,14 @@ __global__ __launch_bounds__(kBatchThreads) void k_txbar_selftest(tmap_t map, co
                                                                  uint32_t max_polls) {
     extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
     TxBar* bar = reinterpret_cast<TxBar*>(smem + bar_off);
-    uint32_t* counter = reinterpret_cast<uint32_t*>(smem + bar_off + sizeof(TxBar));
     const TmapImpl m = tmap_tiled_uniform(map);
     const uint32_t tid = threadIdx.x, wave = tid >> 6, nwaves = blockDim.x >> 6;
+    const uint32_t total = tile_box_bytes(map) * ntile + extra_bytes;
     if (tid == 0) {
         txbar_init(bar, 1);
         trace[0] = -1; trace[1] = bar->expected; trace[2] = 0; trace[3] = 0;
-        const TxState s = txbar_arrive_expect_tx(bar, (int32_t)(tile_box_bytes(map) * ntile + extra_bytes));
+        const TxState s = txbar_arrive_expect_tx(bar, (int32_t)total);
         trace[4] = -2; trace[5] = s.arrivals_left; trace[6] = s.pending; trace[7] = (int32_t)s.phase;
-        *counter = 0;
     }
     __syncthreads();
     for (uint32_t t = wave; t < ntile; t += nwaves) {
@@ -198,7 +199,8 @@ __global__ __launch_bounds__(kBatchThreads) void k_txbar_selftest(tmap_t map, co
         wait_lgkm0();
         if (lane_id() == 0) {
             const TxState s = txbar_complete_tx(bar, (int32_t)bytes);
-            const uint32_t slot = 2u + atomicAdd(counter, 1u);
+            const uint32_t slot = 1u + (total - (uint32_t)s.pending) / m.box_bytes;
+            if (slot >= 2u + ntile) continue;           // a count that went wrong: the final wait reports it
             trace[slot * 4 + 0] = (int32_t)t;
             trace[slot * 4 + 1] = s.arrivals_left;
             trace[slot * 4 + 2] = s.pending;

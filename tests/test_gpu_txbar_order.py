@@ -50,3 +50,8 @@ def test_completions_report_their_own_state(traces):
         got = sorted((tuple(int(x) for x in r[1:]) for r in rec[2:]), key=lambda s: -s[1])
         assert got == sorted(states(), key=lambda s: -s[1])
         assert sorted(rec[2:, 0].tolist()) == list(range(NTILE))
+
+
+def test_records_stand_in_the_order_of_the_operations(traces):
+    for rec in traces:
+        assert [tuple(int(x) for x in r[1:]) for r in rec[2:]] == states()
