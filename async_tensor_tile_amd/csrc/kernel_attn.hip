@@ -107,8 +107,9 @@ struct AttnArgs {
     uint32_t shared;                 // prefix tiles shared by a workgroup's four waves
     uint32_t own_first;              // partial results of the prefix
     uint32_t direct;                 // one part in all: it writes the result
-    float scale;                     // |scale| * log2(e), never 0
+    float scale;                     // |scale| * log2(e), 1 if that is 0
     uint32_t flip;                   // sign bits to turn in the queries (scale below 0)
+    uint32_t zero;                   // the scale is 0
 };
 
 // The arguments where the launch put them.  A long loop that reads them
@@ -220,6 +221,15 @@ struct Wave {
         l = 0.0f;
     }
 
+    // Eight elements times 0: infinities and NaN become NaN.
+    __device__ __forceinline__ static u32x4 times_zero(u32x4 x) {
+        union { u32x4 v; uint16_t e[8]; } y;
+        y.v = x;
+#pragma unroll
+        for (uint32_t i = 0; i < 8; ++i) y.e[i] = not_finite(y.e[i]) ? 0x7FFFu : 0u;
+        return y.v;
+    }
+
     // The lane's query (row r of the head's rows; none past `rows`).
     __device__ __forceinline__ void load(cargs& a, uint32_t head, uint32_t r, bool valid) {
         const uint32_t lane = lane_id();
@@ -231,6 +241,7 @@ struct Wave {
             const uint32_t d = k * 16u + (lane / 32u) * 8u;
             u32x4 x = (u32x4)(0u);
             if (valid && d < a.dim) x = *(const ATT_GLOBAL u32x4*)(p + d * 2u) ^ a.flip;
+            if (a.zero) x = times_zero(x);
             q[k] = __builtin_bit_cast(v8, x);
         }
         clear();
@@ -1025,10 +1036,10 @@ extern "C" tmap_status attn_shared_prefix(const tmap_t* q, const tmap_t* k_pool,
     a.slots = pt->slots;
     a.prefix_row = prefix_row;
     // Scores are kept in powers of two.  A negative scale turns the queries
-    // around; 0 becomes a factor that no score of the types survives, so that
+    // around and a scale of 0 makes them 0, so that the factor is above 0 and
     // masked scores stay at -inf.
-    a.scale = std::fabs(scale) * 1.4426950408889634f;
-    if (a.scale < 1e-37f) a.scale = 1e-37f;
+    a.zero = scale == 0;
+    a.scale = a.zero ? 1.0f : std::fabs(scale) * 1.4426950408889634f;
     a.flip = scale < 0 ? 0x80008000u : 0u;
     a.lse = d_lse;
     st = device_error_word(&a.err);
