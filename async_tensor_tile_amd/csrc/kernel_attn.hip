@@ -50,6 +50,7 @@ constexpr uint32_t kTile = 64;                    // keys of a shared tile
 constexpr uint32_t kOwnTile = 32;                 // keys of a wave's own tile
 constexpr uint32_t kSegment = 256;                // keys whose addresses are worked out together
 constexpr float kLazy = 8.0f;                     // powers of two by which a weight may pass 1
+constexpr float kLog2e = 1.4426950408889634f;
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -1014,7 +1015,7 @@ extern "C" tmap_status attn_shared_prefix(const tmap_t* q, const tmap_t* k_pool,
     if (!pt->d_lens) return TMAP_ERR_NULL;
     if (tq != TMAP_F16 && tq != TMAP_BF16) return TMAP_ERR_DTYPE;
     if (tk != tq || tv != tq || to != tq || !same_dims(a.q, a.o) || !same_dims(a.k, a.v) || !shapes_fit(a.q, a.k) ||
-        (uint64_t)a.k.dim[1] != pt->slots || (uint64_t)a.k.dim[3] != pt->pages || !std::isfinite(scale))
+        (uint64_t)a.k.dim[1] != pt->slots || (uint64_t)a.k.dim[3] != pt->pages || !std::isfinite(scale * kLog2e))
         return TMAP_ERR_UNSUPPORTED;
     if (prefix_len && (prefix_row >= pt->rows || prefix_len > (uint64_t)pt->slots * pt->row_pages))
         return TMAP_ERR_UNSUPPORTED;
@@ -1039,7 +1040,7 @@ extern "C" tmap_status attn_shared_prefix(const tmap_t* q, const tmap_t* k_pool,
     // around and a scale of 0 makes them 0, so that the factor is above 0 and
     // masked scores stay at -inf.
     a.zero = scale == 0;
-    a.scale = a.zero ? 1.0f : std::fabs(scale) * 1.4426950408889634f;
+    a.scale = a.zero ? 1.0f : std::fabs(scale) * kLog2e;
     a.flip = scale < 0 ? 0x80008000u : 0u;
     a.lse = d_lse;
     st = device_error_word(&a.err);
