@@ -340,7 +340,7 @@ extern "C" tmap_status rope_encode(rope_t* out, uint32_t rot_dim, int32_t layout
     if (rot_dim < 2 || rot_dim > 2 * kMaxPairs || rot_dim % 2 != 0) return TMAP_ERR_UNSUPPORTED;
     if (layout != ROPE_HALF && layout != ROPE_INTERLEAVED) return TMAP_ERR_UNSUPPORTED;
     if (scaling < ROPE_SCALE_NONE || scaling > ROPE_SCALE_RAMP) return TMAP_ERR_UNSUPPORTED;
-    if (!(base > 0) || !std::isfinite(base) || !std::isfinite(magnitude)) return TMAP_ERR_UNSUPPORTED;
+    if (!(base > 0) || !std::isfinite(base) || !std::isfinite((float)magnitude)) return TMAP_ERR_UNSUPPORTED;
     if (scaling != ROPE_SCALE_NONE && (!(factor > 0) || !std::isfinite(factor))) return TMAP_ERR_UNSUPPORTED;
     if (scaling == ROPE_SCALE_RAMP &&
         (original_len == 0 || !(fast > slow) || !std::isfinite(fast) || !std::isfinite(slow)))
@@ -351,6 +351,7 @@ extern "C" tmap_status rope_encode(rope_t* out, uint32_t rot_dim, int32_t layout
     p.layout = layout;
     p.magnitude = (float)magnitude;
     if (scaling == ROPE_SCALE_BASE && rot_dim > 2) base *= std::pow(factor, (double)rot_dim / (rot_dim - 2));
+    if (!std::isfinite(base)) return TMAP_ERR_UNSUPPORTED;
     const double two_pi = 6.283185307179586476925286766559;
     for (uint32_t j = 0; j < rot_dim / 2; ++j) {
         double theta = std::pow(base, -2.0 * j / rot_dim);
@@ -361,6 +362,7 @@ extern "C" tmap_status rope_encode(rope_t* out, uint32_t rot_dim, int32_t layout
             theta *= w + (1 - w) / factor;
         }
         p.turns[j] = theta / two_pi;
+        if (!std::isfinite(p.turns[j] * 2147483648.0)) return TMAP_ERR_UNSUPPORTED;   // the farthest position
     }
     std::memcpy(out, &p, sizeof(p));
     return TMAP_OK;

@@ -68,9 +68,10 @@ enum { ROPE_SCALE_NONE = 0, ROPE_SCALE_LINEAR = 1, ROPE_SCALE_BASE = 2, ROPE_SCA
  *   RAMP    theta_j * (w + (1 - w) / factor), w = (n_j - slow) / (fast - slow)
  *           clamped to [0, 1], n_j = original_len * theta_j / 2 pi the turns
  *           of pair j over the trained context.
- * Everything is kept in 64 bits.  Errors: NULL; UNSUPPORTED (enum, rot_dim,
- * base or factor not above 0, magnitude not finite, for RAMP original_len 0
- * or fast <= slow). */
+ * Angles are kept in 64 bits, the magnitude in 32.  Errors: NULL; UNSUPPORTED
+ * (enum, rot_dim, base or factor not above 0, magnitude not finite in fp32, a
+ * base or an angle that is not finite in 64 bits, for RAMP original_len 0 or
+ * fast <= slow). */
 tmap_status rope_encode(rope_t* out, uint32_t rot_dim, int32_t layout, double base, int32_t scaling, double factor,
                         uint32_t original_len, double slow, double fast, double magnitude);
 

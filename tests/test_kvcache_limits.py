@@ -14,3 +14,19 @@ def test_scale_beyond_powers_of_two(scale):
     ws = att.attn_workspace(q, p, 100, 64)
     refused(lambda: att.attn_shared_prefix(q, p, p, table(), 0, 100, 0, 64, scale, q, 0, BASE, 0, ws),
             "ERR_UNSUPPORTED")
+
+
+@pytest.mark.parametrize("args", [dict(rot_dim=64, magnitude=1e39),                       # infinite in fp32
+                                  dict(rot_dim=64, scaling="base", base=1e300, factor=1e9),  # so is the scaled base
+                                  dict(rot_dim=64, scaling="base", base=1e-300, factor=1e-30),
+                                  dict(rot_dim=64, scaling="linear", factor=1e-308),
+                                  dict(rot_dim=64, scaling="ramp", factor=1e-308, original_len=64),
+                                  dict(rot_dim=256, base=1e-307)])
+def test_rope_plans_that_cannot_be_held(args):
+    refused(lambda: att.rope_encode(**args), "ERR_UNSUPPORTED")
+
+
+@pytest.mark.parametrize("args", [dict(rot_dim=64, magnitude=3e38), dict(rot_dim=64, base=1e300),
+                                  dict(rot_dim=64, base=1e-290), dict(rot_dim=2, scaling="base", factor=1e300)])
+def test_rope_plans_at_the_limits(args):
+    att.rope_encode(**args)
