@@ -50,6 +50,10 @@ inline tmap_status check_table(const page_table_t* pt) {
     return TMAP_OK;
 }
 
+// Workgroups along x that one launch holds: HIP counts a grid's threads of one
+// dimension in 32 bits.  Calls with more work launch again for the rest.
+constexpr uint32_t max_groups(uint32_t threads) { return 0xFFFFFFFFu / threads; }
+
 __device__ __forceinline__ void record_page_error(uint32_t* word) {
     __hip_atomic_fetch_or(word, DEVERR_PAGE, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }

@@ -246,12 +246,29 @@ __global__ __launch_bounds__(kRopeThreads) void k_rope(const RopeTurns<P> plan, 
     }
 }
 
+// The arguments of the tokens behind the first n.
+static void skip_tokens(RopeArgs& a, uint32_t n) {
+    for (uint32_t i = 0; i < a.nseg; ++i) {
+        a.seg[i].src += (uint64_t)n * (uint64_t)a.seg[i].src_tok;
+        if (!a.seg[i].dst_page) a.seg[i].dst += (uint64_t)n * (uint64_t)a.seg[i].dst_tok;
+    }
+    if (a.pos) a.pos += n;
+    if (a.rows) a.rows += n, a.at += n;
+}
+
 template <typename T, int MODE, bool STREAM, uint32_t P>
 static void launch_pairs(const RopePlan& plan, const RopeArgs& a, hipStream_t stream) {
     RopeTurns<P> turns;
     std::memcpy(&turns, plan.turns, sizeof(turns));
-    const dim3 grid((a.tokens + a.tok_block - 1) / a.tok_block);
-    hipLaunchKernelGGL((k_rope<T, MODE, STREAM, P>), grid, dim3(kRopeThreads), 0, stream, turns, a);
+    constexpr uint32_t most = max_groups(kRopeThreads);
+    RopeArgs part = a;
+    for (uint32_t left = a.tokens; left; left -= part.tokens) {
+        const uint32_t groups = (left - 1) / a.tok_block + 1;
+        part.tokens = groups <= most ? left : most * a.tok_block;
+        const dim3 grid((part.tokens - 1) / a.tok_block + 1);
+        hipLaunchKernelGGL((k_rope<T, MODE, STREAM, P>), grid, dim3(kRopeThreads), 0, stream, turns, part);
+        skip_tokens(part, part.tokens);
+    }
 }
 
 template <typename T, int MODE>

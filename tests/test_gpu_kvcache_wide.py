@@ -1,0 +1,64 @@
+"""The paged cache's calls with more work than one launch holds (2^32 - 1 threads
+along a dimension), against the same calls piece by piece."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import async_tensor_tile_amd as att  # noqa: E402
+
+import test_gpu_kvcache as base  # noqa: E402
+from gpu_util import require_native, stream  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+def setup_module(module):
+    require_native()
+
+
+# ---- rotary positions: two tokens of 256 threads --------------------------------------
+
+TOKENS = (1 << 25) + 1029
+
+
+def pieces():
+    """Cuts that do not meet those between launches."""
+    at = [0, 1 << 23, (1 << 24) + 7, (1 << 25) - 1000, TOKENS]
+    return list(zip(at, at[1:]))
+
+
+@pytest.mark.parametrize("layout, rot", [("half", 6), ("interleaved", 8)])
+def test_rope_of_many_tokens(layout, rot):
+    x = torch.randn((TOKENS, 1, 8), device="cuda").to(torch.bfloat16)
+    pos = torch.randint(0, 1 << 20, (TOKENS,), dtype=torch.int32, device="cuda")
+    y, want = torch.empty_like(x), torch.empty_like(x)
+    plan = att.rope_encode(rot, layout)
+    att.rope_apply(plan, base.tensor_map(x, "bf16"), base.tensor_map(y, "bf16"), pos, False, stream())
+    for a, b in pieces():
+        att.rope_apply(plan, base.tensor_map(x[a:b], "bf16"), base.tensor_map(want[a:b], "bf16"), pos[a:b], False,
+                       stream())
+    assert torch.equal(y, want)
+
+
+def test_append_of_many_tokens():
+    slots = 4096
+    pages = -(-TOKENS // slots)
+    q, k, v = (torch.randn((TOKENS, 1, 8), device="cuda").to(torch.float16) for _ in "qkv")
+    pools = [torch.zeros((pages, slots, 1, 8), dtype=torch.float16, device="cuda") for _ in range(4)]
+    out, want = torch.empty_like(q), torch.empty_like(q)
+    table = torch.randperm(pages, device="cuda").to(torch.int32)[None].contiguous()
+    pt = att.page_table(table, None, None, pages, slots)
+    rows = torch.zeros(TOKENS, dtype=torch.int32, device="cuda")
+    at = torch.arange(TOKENS, dtype=torch.int32, device="cuda")
+    plan = att.rope_encode(8)
+
+    def append(a, b, o, kp, vp):
+        att.rope_append(plan, *(base.tensor_map(t[a:b], "f16") for t in (q, o, k, v)), base.pool_map(kp, "f16"),
+                        base.pool_map(vp, "f16"), pt, rows[a:b], at[a:b], at[a:b], stream())
+
+    append(0, TOKENS, out, pools[0], pools[1])
+    for a, b in pieces():
+        append(a, b, want, pools[2], pools[3])
+    att.tile_device_status(stream())
+    assert torch.equal(out, want) and torch.equal(pools[0], pools[2]) and torch.equal(pools[1], pools[3])
+    assert torch.equal(pools[1][table[0].long()].view(-1, 8)[:TOKENS], v[:, 0])
