@@ -335,17 +335,17 @@ template <uint32_t N>
 __global__ __launch_bounds__(kCopyThreads) void k_fork_rows(const Table t, const PoolsOf<N> p, const int32_t* src,
                                                             const int32_t* dst, AllocWs ws, uint32_t pieces,
                                                             uint32_t* err) {
-    const uint32_t i = blockIdx.x;
+    const uint32_t i = blockIdx.x, y = blockIdx.y;
     const int32_t fresh = ws.page[i];
     if (fresh == -2) return;
     const int32_t held = ws.held[i];
     const uint32_t full = (uint32_t)held / t.slots;
     const int32_t* from = t.table + (uint64_t)(uint32_t)src[i] * t.pitch;
-    if (blockIdx.y < pieces) {
+    if (y < pieces) {
         int32_t* to = t.table + (uint64_t)(uint32_t)dst[i] * t.pitch;
-        if (blockIdx.y == 0 && threadIdx.x == 0) t.lens[(uint32_t)dst[i]] = held;
+        if (y == 0 && threadIdx.x == 0) t.lens[(uint32_t)dst[i]] = held;
         for (uint32_t k = 0; k < 4; ++k) {
-            const uint32_t c = blockIdx.y * 4u * kCopyThreads + k * kCopyThreads + threadIdx.x;
+            const uint32_t c = y * 4u * kCopyThreads + k * kCopyThreads + threadIdx.x;
             if (c >= t.row_pages) break;
             int32_t page = -1;
             if (c < full) {
@@ -360,7 +360,7 @@ __global__ __launch_bounds__(kCopyThreads) void k_fork_rows(const Table t, const
         return;
     }
     if (fresh < 0) return;
-    const uint32_t at = blockIdx.y - pieces, pool = at / p.parts, part = at - pool * p.parts;
+    const uint32_t at = y - pieces, pool = at / p.parts, part = at - pool * p.parts;
     const int32_t last = from[full];
     if ((uint32_t)last >= t.pages) {
         if (threadIdx.x == 0 && at == 0) record_page_error(err);
@@ -690,14 +690,19 @@ extern "C" tmap_status page_copy(const tmap_t* pools, uint32_t npool, const int3
     if (st) return st;
     if (n == 0) return TMAP_OK;
     if (!d_src || !d_dst) return TMAP_ERR_NULL;
-    if ((uint64_t)n * p.parts > 0x7FFFFFFFull) return TMAP_ERR_UNSUPPORTED;
     uint32_t* err = nullptr;
     st = device_error_word(&err);
     if (st) return st;
-    const dim3 grid(n * p.parts, npool), block(kCopyThreads);
+    const dim3 block(kCopyThreads);
     const hipStream_t s = as_stream(stream);
-    if (npool <= kFewPools) hipLaunchKernelGGL(k_page_copy, grid, block, 0, s, few(p), d_src, d_dst, pages, err);
-    else hipLaunchKernelGGL(k_page_copy, grid, block, 0, s, p, d_src, d_dst, pages, err);
+    const uint32_t most = max_groups(kCopyThreads) / p.parts;              // entries of a launch
+    for (uint32_t i = 0, m = 0; i < n; i += m) {
+        m = n - i < most ? n - i : most;
+        const dim3 grid(m * p.parts, npool);
+        if (npool <= kFewPools)
+            hipLaunchKernelGGL(k_page_copy, grid, block, 0, s, few(p), d_src + i, d_dst + i, pages, err);
+        else hipLaunchKernelGGL(k_page_copy, grid, block, 0, s, p, d_src + i, d_dst + i, pages, err);
+    }
     return check_launch("page_copy");
 }
 
@@ -733,21 +738,28 @@ extern "C" tmap_status page_fork(const page_table_t* pt, const tmap_t* pools, ui
     st = check_ws(d_ws, ws_bytes, alloc_bytes(pt->pages, n));
     if (st) return st;
     const uint32_t pieces = (pt->row_pages + 4 * kCopyThreads - 1) / (4 * kCopyThreads);
-    const uint64_t gy = (uint64_t)pieces + (uint64_t)npool * p.parts;
-    if (gy > 65535 || n > 0x7FFFFFFFu) return TMAP_ERR_UNSUPPORTED;
+    const uint32_t all_y = pieces + npool * p.parts;
+    if (all_y > 65535 || n > 0x7FFFFFFFu) return TMAP_ERR_UNSUPPORTED;
     uint32_t* err = nullptr;
     st = device_error_word(&err);
     if (st) return st;
-    const AllocWs ws = alloc_ws(d_ws, n);
-    hipLaunchKernelGGL(k_hand_out<true>, dim3(1), dim3(kScanThreads), 0, as_stream(stream), table_of(pt), d_src,
-                       d_dst, n, d_ok, ws, err);
+    AllocWs ws = alloc_ws(d_ws, n);
+    const hipStream_t s = as_stream(stream);
+    hipLaunchKernelGGL(k_hand_out<true>, dim3(1), dim3(kScanThreads), 0, s, table_of(pt), d_src, d_dst, n, d_ok, ws,
+                       err);
     st = check_launch("page_fork");
     if (st) return st;
-    const dim3 grid(n, (uint32_t)gy), block(kCopyThreads);
-    const hipStream_t s = as_stream(stream);
-    if (npool <= kFewPools)
-        hipLaunchKernelGGL(k_fork_rows, grid, block, 0, s, table_of(pt), few(p), d_src, d_dst, ws, pieces, err);
-    else hipLaunchKernelGGL(k_fork_rows, grid, block, 0, s, table_of(pt), p, d_src, d_dst, ws, pieces, err);
+    constexpr uint32_t most = max_groups(kCopyThreads);
+    const dim3 block(kCopyThreads);
+    for (uint32_t i = 0, m = 0; i < n; i += m, ws.page += m, ws.held += m) {
+        m = n - i < most ? n - i : most;
+        const dim3 grid(m, all_y);
+        if (npool <= kFewPools)
+            hipLaunchKernelGGL(k_fork_rows, grid, block, 0, s, table_of(pt), few(p), d_src + i, d_dst + i, ws, pieces,
+                               err);
+        else
+            hipLaunchKernelGGL(k_fork_rows, grid, block, 0, s, table_of(pt), p, d_src + i, d_dst + i, ws, pieces, err);
+    }
     return check_launch("page_fork");
 }
 
@@ -758,12 +770,15 @@ extern "C" tmap_status page_free(const page_table_t* pt, const int32_t* d_rows, 
     if (n == 0) return TMAP_OK;
     if (!d_rows) return TMAP_ERR_NULL;
     const uint32_t pieces = (pt->row_pages + 4 * kCopyThreads - 1) / (4 * kCopyThreads);
-    if (pieces > 65535 || n > 0x7FFFFFFFu) return TMAP_ERR_UNSUPPORTED;
     uint32_t* err = nullptr;
     st = device_error_word(&err);
     if (st) return st;
-    hipLaunchKernelGGL(k_page_free, dim3(n, pieces), dim3(kCopyThreads), 0, as_stream(stream), table_of(pt), d_rows,
-                       err);
+    constexpr uint32_t most = max_groups(kCopyThreads);
+    for (uint32_t i = 0, m = 0; i < n; i += m) {
+        m = n - i < most ? n - i : most;
+        hipLaunchKernelGGL(k_page_free, dim3(m, pieces), dim3(kCopyThreads), 0, as_stream(stream), table_of(pt),
+                           d_rows + i, err);
+    }
     return check_launch("page_free");
 }
 

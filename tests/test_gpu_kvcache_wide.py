@@ -62,3 +62,40 @@ def test_append_of_many_tokens():
     att.tile_device_status(stream())
     assert torch.equal(out, want) and torch.equal(pools[0], pools[2]) and torch.equal(pools[1], pools[3])
     assert torch.equal(pools[1][table[0].long()].view(-1, 8)[:TOKENS], v[:, 0])
+
+
+# ---- pages: an entry of 256 threads -----------------------------------------------------
+
+ENTRIES = (1 << 24) + 100
+
+
+def test_page_copy_of_many_entries():
+    """Nearly all skipped; those on either side of the cut are copied."""
+    pools = torch.randint(-999, 999, (64, 4, 1, 8), device="cuda").to(torch.int16)
+    src = torch.full((ENTRIES,), -1, dtype=torch.int32, device="cuda")
+    dst = src.clone()
+    want = pools.clone()
+    for k, i in enumerate([0, 5, (1 << 24) - 3, (1 << 24) - 2, (1 << 24) - 1, 1 << 24, ENTRIES - 1]):
+        src[i], dst[i] = k, 32 + k
+        want[32 + k] = pools[k]
+    att.page_copy(base.pool_map(pools, "u16"), src, dst, ENTRIES, stream())
+    assert torch.equal(pools, want)
+
+
+def test_fork_and_free_of_many_rows():
+    """A finished page shared by 2^24 and more rows, and given back by all."""
+    rows = ENTRIES + 1
+    table = torch.full((rows, 1), -1, dtype=torch.int32, device="cuda")
+    lens = torch.zeros(rows, dtype=torch.int32, device="cuda")
+    refs = base.ints([0, 0, 1])
+    table[0, 0], lens[0] = 2, 4
+    pt = att.page_table(table, lens, refs, 3, 4)
+    dst = torch.arange(rows - 1, 0, -1, dtype=torch.int32, device="cuda")
+    src = torch.zeros_like(dst)
+    flag = torch.empty_like(dst)
+    ws = torch.empty(att.page_workspace(pt, ENTRIES), dtype=torch.uint8, device="cuda")
+    att.page_fork(pt, None, src, dst, ENTRIES, flag, ws, stream())
+    assert (flag == 1).all() and (table == 2).all() and (lens == 4).all() and refs.tolist() == [0, 0, rows]
+    att.page_free(pt, dst, ENTRIES, stream())
+    assert (table[1:] == -1).all() and (lens[1:] == 0).all() and refs.tolist() == [0, 0, 1]
+    att.tile_device_status(stream())
