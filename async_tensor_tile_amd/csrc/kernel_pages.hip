@@ -328,14 +328,14 @@ __global__ __launch_bounds__(kScanThreads) void k_hand_out(const Table t, const 
     }
 }
 
-// Rows and data of a fork, after k_hand_out.  blockIdx.x: the entry; y: pieces
-// of 1024 table entries first, then parts of the unfinished page, pool after
-// pool.
+// Rows and data of a fork, after k_hand_out.  blockIdx.x: the entry; y (from
+// first_y on): pieces of 1024 table entries first, then parts of the
+// unfinished page, pool after pool.
 template <uint32_t N>
 __global__ __launch_bounds__(kCopyThreads) void k_fork_rows(const Table t, const PoolsOf<N> p, const int32_t* src,
                                                             const int32_t* dst, AllocWs ws, uint32_t pieces,
-                                                            uint32_t* err) {
-    const uint32_t i = blockIdx.x, y = blockIdx.y;
+                                                            uint32_t first_y, uint32_t* err) {
+    const uint32_t i = blockIdx.x, y = first_y + blockIdx.y;
     const int32_t fresh = ws.page[i];
     if (fresh == -2) return;
     const int32_t held = ws.held[i];
@@ -739,7 +739,7 @@ extern "C" tmap_status page_fork(const page_table_t* pt, const tmap_t* pools, ui
     if (st) return st;
     const uint32_t pieces = (pt->row_pages + 4 * kCopyThreads - 1) / (4 * kCopyThreads);
     const uint32_t all_y = pieces + npool * p.parts;
-    if (all_y > 65535 || n > 0x7FFFFFFFu) return TMAP_ERR_UNSUPPORTED;
+    if (n > 0x7FFFFFFFu) return TMAP_ERR_UNSUPPORTED;
     uint32_t* err = nullptr;
     st = device_error_word(&err);
     if (st) return st;
@@ -749,16 +749,19 @@ extern "C" tmap_status page_fork(const page_table_t* pt, const tmap_t* pools, ui
                        err);
     st = check_launch("page_fork");
     if (st) return st;
-    constexpr uint32_t most = max_groups(kCopyThreads);
+    constexpr uint32_t most = max_groups(kCopyThreads), most_y = 65535;
     const dim3 block(kCopyThreads);
     for (uint32_t i = 0, m = 0; i < n; i += m, ws.page += m, ws.held += m) {
         m = n - i < most ? n - i : most;
-        const dim3 grid(m, all_y);
-        if (npool <= kFewPools)
-            hipLaunchKernelGGL(k_fork_rows, grid, block, 0, s, table_of(pt), few(p), d_src + i, d_dst + i, ws, pieces,
-                               err);
-        else
-            hipLaunchKernelGGL(k_fork_rows, grid, block, 0, s, table_of(pt), p, d_src + i, d_dst + i, ws, pieces, err);
+        for (uint32_t y = 0; y < all_y; y += most_y) {
+            const dim3 grid(m, all_y - y < most_y ? all_y - y : most_y);
+            if (npool <= kFewPools)
+                hipLaunchKernelGGL(k_fork_rows, grid, block, 0, s, table_of(pt), few(p), d_src + i, d_dst + i, ws,
+                                   pieces, y, err);
+            else
+                hipLaunchKernelGGL(k_fork_rows, grid, block, 0, s, table_of(pt), p, d_src + i, d_dst + i, ws, pieces,
+                                   y, err);
+        }
     }
     return check_launch("page_fork");
 }

@@ -99,3 +99,19 @@ def test_fork_and_free_of_many_rows():
     att.page_free(pt, dst, ENTRIES, stream())
     assert (table[1:] == -1).all() and (lens[1:] == 0).all() and refs.tolist() == [0, 0, 1]
     att.tile_device_status(stream())
+
+
+def test_fork_of_many_large_pages():
+    """256 pools with pages of 4 MiB: more parts of a page than a grid is high."""
+    slots, npool = 512, 256
+    pools = torch.empty((npool, 2, slots, 8, 1024), dtype=torch.uint8, device="cuda")
+    pools[:, 1].random_(0, 255)
+    pools[:, 0] = 0
+    maps = att.tmap_array([base.pool_map(p, "u8") for p in pools])
+    table, lens, refs = base.ints([[1], [-1]]), base.ints([5, 0]), base.ints([0, 1])
+    pt = att.page_table(table, lens, refs, 2, slots)
+    ws = torch.empty(att.page_workspace(pt, 1), dtype=torch.uint8, device="cuda")
+    flag = base.ints([9])
+    att.page_fork(pt, maps, base.ints([0]), base.ints([1]), 1, flag, ws, stream())
+    assert flag.tolist() == [1] and table.tolist() == [[1], [0]] and refs.tolist() == [1, 1]
+    assert torch.equal(pools[:, 0], pools[:, 1])
