@@ -713,6 +713,7 @@ extern "C" tmap_status page_extend(const page_table_t* pt, const int32_t* d_rows
     if (!pt->d_lens || !pt->d_refs) return TMAP_ERR_NULL;
     if (n == 0) return TMAP_OK;
     if (!d_rows || !d_add || !d_ok) return TMAP_ERR_NULL;
+    if (n > 0x7FFFFFFFu) return TMAP_ERR_UNSUPPORTED;      // the kernel counts them in steps of its threads
     st = check_ws(d_ws, ws_bytes, alloc_bytes(pt->pages, n));
     if (st) return st;
     uint32_t* err = nullptr;

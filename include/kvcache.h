@@ -120,8 +120,8 @@ tmap_status page_copy(const tmap_t* pools, uint32_t npool, const int32_t* d_src,
  * from the first that does not fit on, entries are left as they were
  * (d_ok[i] = 0).  So is an entry whose row cannot hold the tokens (it needs
  * no pages).  Rows are distinct.  Errors: NULL, UNSUPPORTED (table, workspace
- * too small), ALIGN (workspace not 16-byte aligned), HIP.  n == 0 is a
- * no-op. */
+ * too small, n above 2^31 - 1), ALIGN (workspace not 16-byte aligned), HIP.
+ * n == 0 is a no-op. */
 tmap_status page_extend(const page_table_t* pt, const int32_t* d_rows, const int32_t* d_add, uint32_t n,
                         int32_t* d_ok, void* d_ws, uint64_t ws_bytes, void* stream);
 

@@ -30,3 +30,9 @@ def test_rope_plans_that_cannot_be_held(args):
                                   dict(rot_dim=64, base=1e-290), dict(rot_dim=2, scaling="base", factor=1e300)])
 def test_rope_plans_at_the_limits(args):
     att.rope_encode(**args)
+
+
+@pytest.mark.parametrize("n", [1 << 31, (1 << 32) - 1])
+def test_entries_that_32_bits_cannot_step_through(n):
+    refused(lambda: att.page_extend(table(), BASE, BASE, n, BASE, BASE, ws_bytes=1 << 40), "ERR_UNSUPPORTED")
+    refused(lambda: att.page_fork(table(), pool(), BASE, BASE, n, BASE, BASE, ws_bytes=1 << 40), "ERR_UNSUPPORTED")
