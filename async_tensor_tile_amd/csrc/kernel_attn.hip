@@ -907,8 +907,8 @@ static uint32_t padded_dim(uint32_t dim) {
 static uint64_t ceil_div(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
 
 // How the work is cut: fills the fields of `a` that follow from the shapes
-// alone and returns the workspace's bytes, 0 if the rows or workgroups are too
-// many to count in 31 bits.
+// alone and returns the workspace's bytes, 0 if there are more rows than 31
+// bits count or more workgroups than a launch holds.
 static uint64_t plan(AttnArgs* a, uint64_t* groups_out) {
     constexpr uint64_t cus = 256;
     const uint64_t batch = (uint64_t)a->q.dim[3];
@@ -952,7 +952,8 @@ static uint64_t plan(AttnArgs* a, uint64_t* groups_out) {
     a->direct = a->parts_all == 0 && a->parts_own == 1;
     const uint64_t first = (uint64_t)a->units_all * a->blocks_all, own = jobs * a->parts_own;
     const uint64_t groups = wg_all + own;
-    if (groups > 0x7FFFFFFFull || first > 0x7FFFFFFFull || (uint64_t)a->kv * a->blocks_all > 0x7FFFFFFFull) return 0;
+    constexpr uint64_t most_groups = max_groups(kThreads);                 // of the products' launch, of the join's
+    if (groups > most_groups || first > 0x7FFFFFFFull || (uint64_t)a->kv * a->blocks_all > most_groups) return 0;
     a->wg_all = (uint32_t)wg_all;
     a->own_first = (uint32_t)first;
     *groups_out = groups;

@@ -175,9 +175,11 @@ uint64_t attn_workspace(const tmap_t* q, const tmap_t* k_pool, uint32_t prefix_l
  * element type for the product with the values.  dim is a multiple of 8, at
  * most 256.  Errors: NULL, DTYPE, RANK, ALIGN (workspace), UNSUPPORTED
  * (shapes, heads not a multiple of the pool's, prefix_row, prefix_len beyond
- * the row, scale * log2(e) not finite in fp32, workspace too small, more rows
- * or parts than 31 bits count), HIP.  An empty batch is not expressible (a
- * map's dimensions are at least 1). */
+ * the row, scale * log2(e) not finite in fp32, workspace too small, heads,
+ * q_len or batch above 65535, more than 2^31 - 1 queries for a key / value
+ * head, more than 2^24 - 1 workgroups: about one for each sequence, key / value
+ * head and 32 of its queries), HIP.  An empty batch is not expressible (a map's
+ * dimensions are at least 1). */
 tmap_status attn_shared_prefix(const tmap_t* q, const tmap_t* k_pool, const tmap_t* v_pool, const page_table_t* pt,
                                uint32_t prefix_row, uint32_t prefix_len, const int32_t* d_rows, uint32_t suffix_hint,
                                float scale, const tmap_t* o, float* d_lse, void* d_ws, uint64_t ws_bytes,

@@ -36,3 +36,17 @@ def test_rope_plans_at_the_limits(args):
 def test_entries_that_32_bits_cannot_step_through(n):
     refused(lambda: att.page_extend(table(), BASE, BASE, n, BASE, BASE, ws_bytes=1 << 40), "ERR_UNSUPPORTED")
     refused(lambda: att.page_fork(table(), pool(), BASE, BASE, n, BASE, BASE, ws_bytes=1 << 40), "ERR_UNSUPPORTED")
+
+
+def test_attention_beyond_one_launch():
+    """2^24 - 1 workgroups of 256 threads: one for each sequence and head here."""
+    p = pool(n=512)
+    assert att.attn_workspace(queries(n=512, batch=32767), p, 0, 0) > 0
+    for prefix in (0, 100):
+        q = queries(n=512, batch=32768)
+        assert att.attn_workspace(q, p, prefix, 0) == 0
+        refused(lambda: att.attn_shared_prefix(q, p, p, table(rows=40000), 0, prefix, 0, 0, 0.1, q, 0, BASE, 0, 1 << 40),
+                "ERR_UNSUPPORTED")
+    # many queries of one sequence
+    q = queries(n=64, q_len=65535, batch=128)
+    assert att.attn_workspace(q, pool(n=4), 0, 0) == 0
