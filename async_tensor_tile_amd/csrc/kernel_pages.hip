@@ -601,6 +601,11 @@ static tmap_status pools_of(const tmap_t* maps, uint32_t npool, const page_table
     }
     if (v.dim[3] > 0x7FFFFFFF) return TMAP_ERR_UNSUPPORTED;
     if (pt && ((uint64_t)v.dim[1] != pt->slots || (uint64_t)v.dim[3] != pt->pages)) return TMAP_ERR_UNSUPPORTED;
+    // 256 MiB of one page; a map's dimensions may count more bytes than 64 bits
+    constexpr uint64_t most = 1ull << 28;
+    if ((unsigned __int128)v.dim[0] * v.stride[0] * v.dim[1] > most ||
+        (unsigned __int128)v.dim[0] * v.stride[0] * v.dim[1] * v.dim[2] > most)
+        return TMAP_ERR_UNSUPPORTED;
     uint64_t row = (uint64_t)v.dim[0] * (uint64_t)v.stride[0], n1 = (uint64_t)v.dim[1], n2 = (uint64_t)v.dim[2];
     int64_t s1 = v.stride[1], s2 = v.stride[2];
     if (s2 < s1 || n1 == 1) {                             // the closer dimension first
@@ -617,7 +622,7 @@ static tmap_status pools_of(const tmap_t* maps, uint32_t npool, const page_table
         }
     }
     const uint64_t row_chunks = (row + 15) / 16, chunks = row_chunks * n1 * n2;
-    if (chunks > (1ull << 24)) return TMAP_ERR_UNSUPPORTED;   // 256 MiB of one page
+    if (chunks > most / 16) return TMAP_ERR_UNSUPPORTED;      // rows are copied in whole chunks
     out->page = v.stride[3];
     out->s1 = s1;
     out->s2 = s2;

@@ -110,7 +110,8 @@ uint64_t page_workspace(const page_table_t* pt, uint32_t n);
  * 256, all of one geometry: type, dims, strides; e.g. every layer's keys and
  * values).  An entry with a negative page number is skipped.  A page that is
  * both written and read, or written twice, races.  Errors: NULL, RANK,
- * UNSUPPORTED (pools), HIP.  n == 0 is a no-op. */
+ * UNSUPPORTED (pools, or a page of more than 256 MiB, its rows counted in whole
+ * 16 bytes), HIP.  n == 0 is a no-op. */
 tmap_status page_copy(const tmap_t* pools, uint32_t npool, const int32_t* d_src, const int32_t* d_dst, uint32_t n,
                       void* stream);
 

@@ -50,3 +50,20 @@ def test_attention_beyond_one_launch():
     # many queries of one sequence
     q = queries(n=64, q_len=65535, batch=128)
     assert att.attn_workspace(q, pool(n=4), 0, 0) == 0
+
+
+def u8_pool(dims, strides):
+    return att.tmap_encode("u8", 4, BASE, dims, strides, (16, 1, 1, 1))
+
+
+def test_pages_above_256_mib():
+    """n == 0 checks the pools alone.  Bytes of a page that wrap 64 bits count too."""
+    k = 1 << 14
+    att.page_copy(u8_pool((k, k, 1, 2), (k, k * k, k * k)), BASE, BASE, 0)
+    big = [u8_pool((k, k + 1, 1, 2), (k, k * (k + 1), k * (k + 1))),
+           u8_pool((k, 1, k + 1, 2), (k, k, k * (k + 1))),
+           u8_pool((1, k, k // 4 + 1, 2), (16, 16 * k, 16 * k * k)),                  # rows of one byte, 16 each
+           u8_pool((1 << 32, 1 << 32, 1, 2), (1 << 32, 1 << 39, 1 << 39)),            # 2^64 bytes in a packed row
+           u8_pool((1 << 20, 1 << 32, 1 << 32, 2), (1 << 24, 1 << 39, 1 << 39))]      # 2^84, rows apart
+    for p in big:
+        refused(lambda: att.page_copy(p, BASE, BASE, 0), "ERR_UNSUPPORTED")
