@@ -323,10 +323,32 @@ def gemm_bf16_ex(A: tmap_t, B: tmap_t, d_C, M: int, N: int, K: int, ldc: int, st
 
 
 # ---- a paged key / value cache (include/kvcache.h) ----------------------------
+#
+# Positions, rows, pages and flags are int32: a tensor of another type (torch's
+# own default is int64) is refused.
 
 
 def _ref(m):
     return None if m is None else ctypes.byref(m)
+
+
+_INT32 = set()      # element types that were seen to be 32-bit integers
+
+
+def _ints(x, name: str) -> int:
+    """Address of int32 values: a tensor of them, side by side, or an address."""
+    try:
+        if x.dtype in _INT32 and x.is_contiguous():
+            return x.data_ptr()
+    except AttributeError:
+        pass
+    if hasattr(x, "data_ptr"):
+        if x.element_size() != 4 or x.is_floating_point():
+            raise TypeError(f"{name} has to be int32, not {x.dtype}")
+        if not x.is_contiguous():
+            raise ValueError(f"{name} has to lie side by side")
+        _INT32.add(x.dtype)
+    return _addr(x)
 
 
 def _nbytes(ws) -> int:
@@ -362,7 +384,7 @@ def rope_encode(rot_dim: int, layout="half", base: float = 10000.0, scaling="non
 
 
 def rope_apply(r: rope_t, x: tmap_t, y: tmap_t, d_pos, inverse=False, stream=0) -> None:
-    _check(lib().rope_apply(ctypes.byref(r), ctypes.byref(x), ctypes.byref(y), _addr(d_pos), int(inverse),
+    _check(lib().rope_apply(ctypes.byref(r), ctypes.byref(x), ctypes.byref(y), _ints(d_pos, "d_pos"), int(inverse),
                             _addr(stream)), "rope_apply")
 
 
@@ -370,7 +392,8 @@ def rope_append(r, q, q_out, k: tmap_t, v: tmap_t, k_pool: tmap_t, v_pool: tmap_
                 d_pos, stream=0) -> None:
     """r, and q with q_out, may be None (see kvcache.h)."""
     _check(lib().rope_append(_ref(r), _ref(q), _ref(q_out), _ref(k), _ref(v), _ref(k_pool), _ref(v_pool), _ref(pt),
-                             _addr(d_rows), _addr(d_at), _addr(d_pos), _addr(stream)), "rope_append")
+                             _ints(d_rows, "d_rows"), _ints(d_at, "d_at"), _ints(d_pos, "d_pos"), _addr(stream)),
+           "rope_append")
 
 
 def page_table(d_table, d_lens, d_refs, pages: int, slots: int, rows: int = 0, row_pages: int = 0,
@@ -387,6 +410,9 @@ def page_table(d_table, d_lens, d_refs, pages: int, slots: int, rows: int = 0, r
     for name, t in (("d_table", d_table), ("d_lens", d_lens), ("d_refs", d_refs)):
         if hasattr(t, "element_size") and (t.element_size() != 4 or t.is_floating_point()):
             raise TypeError(f"page_table: {name} has to be int32")
+    for name, t, n in (("d_lens", d_lens, rows), ("d_refs", d_refs, pages)):
+        if hasattr(t, "numel") and (t.numel() < n or not t.is_contiguous()):
+            raise ValueError(f"page_table: {name} has to hold {n} values side by side")
     return page_table_t(_addr(d_table), _addr(d_lens), _addr(d_refs), pitch or row_pages, rows, row_pages,
                         int(pages), int(slots))
 
@@ -397,29 +423,29 @@ def page_workspace(pt: page_table_t, n: int) -> int:
 
 def page_copy(pools, d_src, d_dst, n: int, stream=0) -> None:
     arr, k = _pool_array(pools)
-    _check(lib().page_copy(arr, k, _addr(d_src), _addr(d_dst), int(n), _addr(stream)), "page_copy")
+    _check(lib().page_copy(arr, k, _ints(d_src, "d_src"), _ints(d_dst, "d_dst"), int(n), _addr(stream)), "page_copy")
 
 
 def page_extend(pt: page_table_t, d_rows, d_add, n: int, d_ok, d_ws, stream=0, ws_bytes: int = 0) -> None:
     """d_ws is a tensor, or an address with ws_bytes; so in the calls below."""
-    _check(lib().page_extend(_ref(pt), _addr(d_rows), _addr(d_add), int(n), _addr(d_ok), _addr(d_ws),
-                             ws_bytes or _nbytes(d_ws), _addr(stream)), "page_extend")
+    _check(lib().page_extend(_ref(pt), _ints(d_rows, "d_rows"), _ints(d_add, "d_add"), int(n), _ints(d_ok, "d_ok"),
+                             _addr(d_ws), ws_bytes or _nbytes(d_ws), _addr(stream)), "page_extend")
 
 
 def page_fork(pt: page_table_t, pools, d_src, d_dst, n: int, d_ok, d_ws, stream=0, ws_bytes: int = 0) -> None:
     """pools: a map, several, or a tmap_array of them; None for the tables alone."""
     arr, k = _pool_array(pools)
-    _check(lib().page_fork(_ref(pt), arr, k, _addr(d_src), _addr(d_dst), int(n), _addr(d_ok), _addr(d_ws),
-                           ws_bytes or _nbytes(d_ws), _addr(stream)), "page_fork")
+    _check(lib().page_fork(_ref(pt), arr, k, _ints(d_src, "d_src"), _ints(d_dst, "d_dst"), int(n),
+                           _ints(d_ok, "d_ok"), _addr(d_ws), ws_bytes or _nbytes(d_ws), _addr(stream)), "page_fork")
 
 
 def page_free(pt: page_table_t, d_rows, n: int, stream=0) -> None:
-    _check(lib().page_free(_ref(pt), _addr(d_rows), int(n), _addr(stream)), "page_free")
+    _check(lib().page_free(_ref(pt), _ints(d_rows, "d_rows"), int(n), _addr(stream)), "page_free")
 
 
 def page_compact(pt: page_table_t, pt_to: page_table_t, pools, d_used, d_ws, stream=0, ws_bytes: int = 0) -> None:
     arr, k = _pool_array(pools)
-    _check(lib().page_compact(_ref(pt), _ref(pt_to), arr, k, _addr(d_used), _addr(d_ws),
+    _check(lib().page_compact(_ref(pt), _ref(pt_to), arr, k, _ints(d_used, "d_used"), _addr(d_ws),
                               ws_bytes or _nbytes(d_ws), _addr(stream)), "page_compact")
 
 
@@ -430,6 +456,9 @@ def attn_workspace(q: tmap_t, k_pool: tmap_t, prefix_len: int, suffix_hint: int)
 def attn_shared_prefix(q: tmap_t, k_pool: tmap_t, v_pool: tmap_t, pt: page_table_t, prefix_row: int,
                        prefix_len: int, d_rows, suffix_hint: int, scale: float, o: tmap_t, d_lse, d_ws, stream=0,
                        ws_bytes: int = 0) -> None:
+    if hasattr(d_lse, "data_ptr") and (d_lse.element_size() != 4 or not d_lse.is_floating_point() or
+                                       not d_lse.is_contiguous()):
+        raise TypeError("d_lse has to be float32 values side by side")
     _check(lib().attn_shared_prefix(_ref(q), _ref(k_pool), _ref(v_pool), _ref(pt), int(prefix_row), int(prefix_len),
-                                    _addr(d_rows), int(suffix_hint), float(scale), _ref(o), _addr(d_lse),
+                                    _ints(d_rows, "d_rows"), int(suffix_hint), float(scale), _ref(o), _addr(d_lse),
                                     _addr(d_ws), ws_bytes or _nbytes(d_ws), _addr(stream)), "attn_shared_prefix")

@@ -67,3 +67,50 @@ def test_pages_above_256_mib():
            u8_pool((1 << 20, 1 << 32, 1 << 32, 2), (1 << 24, 1 << 39, 1 << 39))]      # 2^84, rows apart
     for p in big:
         refused(lambda: att.page_copy(p, BASE, BASE, 0), "ERR_UNSUPPORTED")
+
+
+def test_tensors_of_other_types_and_strides_are_refused():
+    """torch's own integers are int64: read as int32, every other value is 0."""
+    torch = pytest.importorskip("torch")
+    wrong = [(torch.zeros(16, dtype=torch.int64), TypeError), (torch.zeros(16), TypeError),
+             (torch.zeros(16, dtype=torch.int16), TypeError), (torch.zeros(32, dtype=torch.int32)[::2], ValueError)]
+    good = torch.zeros(16, dtype=torch.int32)
+    r, x, k, p, t, q = att.rope_encode(64), heads(), heads(n=2), pool(), table(), queries()
+    ws = torch.empty(att.page_workspace(t, 4), dtype=torch.uint8)
+    calls = {
+        "d_pos": lambda a: att.rope_apply(r, x, x, a),
+        "d_rows": lambda a: att.rope_append(r, None, None, k, k, p, p, t, a, good, good),
+        "d_at": lambda a: att.rope_append(r, None, None, k, k, p, p, t, good, a, good),
+        "d_pos ": lambda a: att.rope_append(r, None, None, k, k, p, p, t, good, good, a),
+        "d_src": lambda a: att.page_copy(p, a, good, 4),
+        "d_dst": lambda a: att.page_copy(p, good, a, 4),
+        "d_rows ": lambda a: att.page_extend(t, a, good, 4, good, ws),
+        "d_add": lambda a: att.page_extend(t, good, a, 4, good, ws),
+        "d_ok": lambda a: att.page_extend(t, good, good, 4, a, ws),
+        "d_src ": lambda a: att.page_fork(t, p, a, good, 4, good, ws),
+        "d_dst ": lambda a: att.page_fork(t, p, good, a, 4, good, ws),
+        "d_ok ": lambda a: att.page_fork(t, p, good, good, 4, a, ws),
+        "d_rows  ": lambda a: att.page_free(t, a, 4),
+        "d_used": lambda a: att.page_compact(t, t, p, a, ws),
+        "d_rows   ": lambda a: att.attn_shared_prefix(q, p, p, t, 0, 0, a, 0, 0.1, q, 0, ws),
+    }
+    for name, call in calls.items():
+        for a, error in wrong:
+            with pytest.raises(error, match=name.strip()):
+                call(a)
+    for a in (torch.zeros(16, dtype=torch.float64), torch.zeros(16, dtype=torch.int32), torch.zeros(32)[::2]):
+        with pytest.raises(TypeError, match="d_lse"):
+            att.attn_shared_prefix(q, p, p, t, 0, 0, 0, 0, 0.1, q, a, ws)
+
+
+def test_page_tables_of_short_tensors_are_refused():
+    torch = pytest.importorskip("torch")
+
+    def new(n):
+        return torch.zeros(n, dtype=torch.int32)
+
+    att.page_table(new((4, 5)), new(4), new(9), 9, 16)
+    att.page_table(new((4, 5)), new(6), new(12), 9, 16)
+    for lens, refs in ((new(3), new(9)), (new(4), new(8)), (new(8)[::2], new(9)), (new(4), new(18)[::2])):
+        with pytest.raises(ValueError):
+            att.page_table(new((4, 5)), lens, refs, 9, 16)
