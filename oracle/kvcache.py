@@ -178,3 +178,43 @@ def attention(q, k_pool, v_pool, table, lens, slots, prefix_row, prefix_len, row
                 score_size[b, j, h] = abs(scale) * (np.abs(k) @ np.abs(q[b, j, h])).max()
                 seen[b, j, h] = len(keys)
     return o, lse, weight, score_size, seen
+
+
+def attention_by_head(q, k_pool, v_pool, table, lens, slots, prefix_row, prefix_len, rows, scale):
+    """attention() for long prefixes: a head's queries meet the prefix in one
+    product, and each sequence's own tokens behind it."""
+    batch, q_len, heads, dim = q.shape
+    group = heads // k_pool.shape[2]
+    o, lse = np.zeros(q.shape), np.full(q.shape[:3], -np.inf)
+    weight, score_size = np.zeros(q.shape), np.zeros(q.shape[:3])
+    seen = np.zeros(q.shape[:3], dtype=np.int64)
+
+    def keys(row, n, g):
+        t = np.arange(n)
+        page, slot = np.asarray(table[row])[t // slots], t % slots
+        return k_pool[page, slot, g], v_pool[page, slot, g]
+
+    for h in range(heads):
+        k0, v0 = keys(prefix_row, prefix_len, h // group)
+        shared = scale * (q[:, :, h] @ k0.T)
+        size = np.zeros((batch, q_len))
+        if prefix_len:
+            size = abs(scale) * (np.abs(q[:, :, h]) @ np.abs(k0).T).max(-1)
+        for b in range(batch):
+            row = rows[b] if rows is not None else b
+            k1, v1 = keys(row, int(lens[row]), h // group)
+            for j in range(q_len):
+                n = max(0, int(lens[row]) - q_len + 1 + j)
+                if prefix_len + n == 0:
+                    continue
+                s = np.concatenate((shared[b, j], scale * (k1[:n] @ q[b, j, h])))
+                m = s.max()
+                w = np.exp(s - m)
+                w0, w1, total = w[:prefix_len], w[prefix_len:], w.sum()
+                o[b, j, h] = (w0 @ v0 + w1 @ v1[:n]) / total
+                weight[b, j, h] = (w0 @ np.abs(v0) + w1 @ np.abs(v1[:n])) / total
+                lse[b, j, h] = m + math.log(total)
+                own = abs(scale) * (np.abs(k1[:n]) @ np.abs(q[b, j, h])).max(initial=0.0)
+                score_size[b, j, h] = max(size[b, j], own)
+                seen[b, j, h] = prefix_len + n
+    return o, lse, weight, score_size, seen
