@@ -298,8 +298,6 @@ __global__ __launch_bounds__(64) void k_lds_bank_probe(int32_t layout, uint32_t 
     if (sink == 0xFFFFFFFFu) hist[0] = -1;   // keeps the timed reads alive
 }
 
-// The caller's descriptor by value for a kernel argument; copied bytewise,
-// since the caller's 128 bytes need not sit at tmap_t's 64-byte alignment.
 // The address of the error word on the current device, for kernels of other
 // source files.  It never changes, so it is looked up once per device.
 tmap_status device_error_word(uint32_t** out) {
@@ -317,6 +315,8 @@ tmap_status device_error_word(uint32_t** out) {
     return TMAP_OK;
 }
 
+// The caller's descriptor by value for a kernel argument; copied bytewise,
+// since the caller's 128 bytes need not sit at tmap_t's 64-byte alignment.
 static tmap_t map_value(const tmap_t* m) {
     tmap_t v;
     std::memcpy(&v, m, sizeof(v));

@@ -48,7 +48,7 @@ def rope(x, pos, thetas, layout="half", magnitude=1.0, inverse=False):
     half = len(thetas)
     for t in range(x.shape[0]):
         for j, theta in enumerate(thetas):
-            # the whole turns are taken out with exact integers: theta as a fraction times an integer position
+            # whole turns are taken out of the product exactly; the product itself is rounded to 64 bits, off by 2^-53 of it
             angle = math.fmod(float(pos[t]) * theta, 2 * math.pi)
             c, s = magnitude * math.cos(angle), magnitude * math.sin(-angle if inverse else angle)
             a, b = (2 * j, 2 * j + 1) if layout == "interleaved" else (j, j + half)
