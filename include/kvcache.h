@@ -167,7 +167,8 @@ uint64_t attn_workspace(const tmap_t* q, const tmap_t* k_pool, uint32_t prefix_l
  *   o   = sum_t softmax_t(scale * q . k_t) v_t
  *   lse = log sum_t exp(scale * q . k_t), fp32 [batch, q_len, heads] (NULL:
  *         not written)
- * A query that sees nothing gets o = 0 and lse = -inf.  Query head h uses
+ * A query that sees nothing, or whose scores are all -inf, gets o = 0 and
+ * lse = -inf; a NaN or +inf among its scores makes both NaN.  Query head h uses
  * key / value head h / (heads / kv heads).  Keys and values that a query does
  * not see do not reach it, whatever they hold.  Lengths are read on the
  * device, so that a captured call follows them; suffix_hint is the length

@@ -45,3 +45,43 @@ def test_scale_of_zero_keeps_what_is_not_finite():
     bad[0, 0, 1] = bad[1, 0, 0] = bad[2] = True
     assert np.array_equal(np.isnan(lse), bad)
     assert np.array_equal(np.isnan(got).all(-1), bad) and np.array_equal(np.isnan(got).any(-1), bad)
+
+
+# ---- infinite scores -----------------------------------------------------------------
+
+@pytest.mark.parametrize("batch, kv, prefix", [(3, 2, 0), (3, 2, 90), (3, 2, 2000), (80, 500, 300)])
+def test_infinite_scores(batch, kv, prefix):
+    """All of a query's scores at -inf leave it as one that sees nothing, some
+    count as keys that are not there, one at +inf makes it NaN."""
+    c = ("bf16", batch, 1, kv, kv, 64, 16, prefix, [20] * batch, False, 0)
+    q, kp, vp, table, lens, rows = base.attn_setup(c, base.gen(53))
+
+    def run():
+        return base.attn_run(q, kp, vp, table, lens, rows, 16, prefix, 0.125, "bf16")
+
+    q[..., 0].abs_().add_(0.5)                             # head 0 of every key is -inf there
+    keep = kp[:, :, 0, 0].clone()
+    kp[:, :, 0, 0] = -math.inf
+    got, lse = run()
+    assert (got[:, 0, 0] == 0).all() and np.isneginf(lse[:, 0, 0]).all()
+    assert np.isfinite(got).all() and np.isfinite(lse[:, 0, 1:]).all()
+    # the first page of each row's keys alone: as if it were not there
+    kp[:, :, 0, 0] = keep
+    first = [int(table[r][0]) for r in ([1] if prefix else []) + rows]
+    for p in first:
+        kp[p, :, 0, 0] = -math.inf
+    got, lse = run()
+    missing = table.copy()
+    missing[:, 0] = -1
+    want, lse2 = base.attn_run(q, kp, vp, missing, lens, rows, 16, prefix, 0.125, "bf16")
+    with pytest.raises(base.att.TmapError):
+        base.att.tile_device_status(base.stream())
+    assert np.isfinite(want[:, 0, 0]).all()
+    assert np.array_equal(got[:, 0, 0], want[:, 0, 0]) and np.array_equal(lse[:, 0, 0], lse2[:, 0, 0])
+    for p in first:
+        kp[p, :, 0, 0] = 0.5
+    kp[int(table[rows[1]][1]), 2, 1, 0] = math.inf
+    got, lse = run()
+    assert np.isnan(got[1, 0, 1]).all() and np.isnan(lse[1, 0, 1])
+    got[1, 0, 1] = lse[1, 0, 1] = 0
+    assert np.isfinite(got).all() and np.isfinite(lse).all()
