@@ -10,8 +10,9 @@
 // tables of a cache are small beside its pages.  Moving pages is bandwidth:
 // those kernels spread 16 KiB parts of pages over the whole GPU; compacting
 // 16384 pages of 16 KiB in 8 pools, half of them in use, moves 1.07 GB in 202 us
-// (5.3 TB/s) after 7.5 us for the plan.  A small fork is its launches: free 2.5,
-// hand out 5, rows and pages 4.5, extend 3.5 us.
+// (5.3 TB/s) after 7.8 us for the plan; 500 pages copied within two pools take
+// 10.8 us (6.1 TB/s, partly from the caches).  A small fork is its launches: free
+// 2.6, hand out 5.3, rows and pages 4.4, extend 3.8 us.
 #include <hip/hip_runtime.h>
 
 #include <cstring>
@@ -237,7 +238,8 @@ __device__ __forceinline__ int32_t entry_need(const Table& t, const int32_t* a, 
 // leaves the rows and the data to k_fork_rows.  A chain of latencies (entries,
 // their lengths, the counts, the stores), so the counts are on their way
 // before the entries are looked at and nothing passes through memory between
-// the steps: 16384 pages and 128 entries take 6 us, 1024 pages and 4 entries 5.
+// the steps: 16384 pages and 128 entries take 6.4 to 7.8 us, 1024 pages and 4
+// entries 3.8 (extend) and 5.3 (fork).
 template <bool FORK>
 __global__ __launch_bounds__(kScanThreads) void k_hand_out(const Table t, const int32_t* a, const int32_t* b,
                                                            uint32_t n, int32_t* ok, AllocWs ws, uint32_t* err) {

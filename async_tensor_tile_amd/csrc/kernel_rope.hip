@@ -11,9 +11,12 @@
 // Bound: HBM, or the launch for a few tokens.  A head's element is read once
 // and written once; the cosine and sine of a (token, pair) are computed once
 // per workgroup, into LDS, and used for every head of the token.  8192 tokens of
-// 32 x 128 bf16 take 24 us (5.5 TB/s), the step that writes 8191 tokens' keys
-// and values to their pages 41 us (4.9 TB/s); 64 tokens' step 8.4 us, of which
-// the kernel is 6.
+// 32 x 128 bf16 take 22.2 us (6.0 TB/s), the step that writes 8191 tokens' keys and
+// values to their pages 38.3 us (5.2 TB/s); 64 tokens' step 8.3 us, of which the
+// kernel is 6.8.  Short of 32 MiB the layouts differ: 4096 tokens (67 MB, 12.9 us at
+// 5.2 TB/s) take 13.7 us in pairs side by side, 16.5 in halves of the whole head,
+// 17.9 to 18.8 with part of the head turned (lanes with two chunks of a pair beside
+// lanes with one of the rest), 21.3 to 21.8 element by element.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
