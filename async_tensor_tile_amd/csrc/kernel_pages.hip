@@ -283,6 +283,9 @@ __global__ __launch_bounds__(kScanThreads) void k_hand_out(const Table t, const 
         }
         found += all;
     }
+    // The list ends at the pages wanted, also where rows that are not distinct
+    // come to need more of them further on.
+    if (found > want) found = want;
     __syncthreads();                                      // the list is written, and every count was read
     auto page_at = [&](uint64_t rank) { return rank < kFreshLds ? fresh[rank] : ws.fresh[rank]; };
     uint64_t from = 0;                                    // pages of the entries of earlier rounds
