@@ -405,6 +405,8 @@ def page_table(d_table, d_lens, d_refs, pages: int, slots: int, rows: int = 0, r
     if shape is not None and len(shape) == 2:
         if d_table.stride(1) != 1 and shape[1] > 1:
             raise ValueError("page_table: the table's columns have to lie side by side")
+        if d_table.stride(0) < shape[1] and shape[0] > 1:
+            raise ValueError("page_table: the table's rows may not share memory")
         rows, row_pages = rows or int(shape[0]), row_pages or int(shape[1])
         pitch = pitch or int(d_table.stride(0))
     for name, t in (("d_table", d_table), ("d_lens", d_lens), ("d_refs", d_refs)):

@@ -114,3 +114,15 @@ def test_page_tables_of_short_tensors_are_refused():
     for lens, refs in ((new(3), new(9)), (new(4), new(8)), (new(8)[::2], new(9)), (new(4), new(18)[::2])):
         with pytest.raises(ValueError):
             att.page_table(new((4, 5)), lens, refs, 9, 16)
+
+
+def test_page_tables_whose_rows_share_memory_are_refused():
+    """An expanded table has a stride of 0, which is not a pitch."""
+    torch = pytest.importorskip("torch")
+    t = torch.zeros((1, 5), dtype=torch.int32)
+    lens, refs = torch.zeros(4, dtype=torch.int32), torch.zeros(9, dtype=torch.int32)
+    assert att.page_table(t, lens, refs, 9, 16).pitch == 5
+    with pytest.raises(ValueError):
+        att.page_table(t.expand(4, 5), lens, refs, 9, 16)
+    with pytest.raises(ValueError):
+        att.page_table(torch.zeros(8, dtype=torch.int32).as_strided((4, 5), (1, 1)), lens, refs, 9, 16)
