@@ -33,6 +33,7 @@ STATUS = {0: "OK", 1: "ERR_NULL", 2: "ERR_RANK", 3: "ERR_DTYPE", 4: "ERR_ALIGN",
           16: "ERR_PAGE"}
 ROPE_LAYOUT = {"half": 0, "interleaved": 1}
 ROPE_SCALING = {"none": 0, "linear": 1, "base": 2, "ramp": 3}
+KV_FORMAT = {"same": 0, "int8": 1, "e4m3": 2}
 
 
 class NativeLibraryMissing(RuntimeError):
@@ -137,8 +138,13 @@ def lib():
         L.page_compact.argtypes = [pp, pp, tp, _U32, _V, _V, U64, _V]
         L.attn_workspace.argtypes = [tp, tp, _U32, _U32]
         L.attn_shared_prefix.argtypes = [tp, tp, tp, pp, _U32, _U32, _V, _U32, ctypes.c_float, tp, _V, _V, U64, _V]
+        L.kv8_rows.argtypes = [_U32, _U32]
+        L.kv8_rows.restype = _U32
+        L.kv8_append.argtypes = [rp, tp, tp, tp, tp, _I32, tp, tp, pp, _V, _V, _V, _V]
+        L.kv8_read.argtypes = [_I32, tp, tp, pp, _V, _V, tp, tp, _V]
+        L.page_keep.argtypes = [pp, tp, _U32, _V, _V, _V, _U32, _V, _U32, _V, _V]
         for name in ("rope_encode", "rope_apply", "rope_append", "page_copy", "page_extend", "page_fork", "page_free",
-                     "page_compact", "attn_shared_prefix"):
+                     "page_compact", "attn_shared_prefix", "kv8_append", "kv8_read", "page_keep"):
             getattr(L, name).restype = _I32
         L.page_workspace.restype = L.attn_workspace.restype = U64
         _lib = L
@@ -396,6 +402,35 @@ def rope_append(r, q, q_out, k: tmap_t, v: tmap_t, k_pool: tmap_t, v_pool: tmap_
            "rope_append")
 
 
+def _format(f) -> int:
+    if isinstance(f, str):
+        if f not in KV_FORMAT:
+            raise ValueError(f"unknown format {f!r}: one of {', '.join(KV_FORMAT)}")
+        return KV_FORMAT[f]
+    return int(f)
+
+
+def kv8_rows(slots: int, dim: int) -> int:
+    """Rows of dim bytes of a head of a page of 8-bit codes: the slots' codes
+    and their scales (see kvcache.h)."""
+    return int(lib().kv8_rows(int(slots), int(dim)))
+
+
+def kv8_append(r, q, q_out, k: tmap_t, v: tmap_t, format, k_pool: tmap_t, v_pool: tmap_t, pt: page_table_t, d_rows, d_at,
+               d_pos, stream=0) -> None:
+    """rope_append to pools of 8-bit codes; format "int8" or "e4m3" (or the
+    KV_* value)."""
+    _check(lib().kv8_append(_ref(r), _ref(q), _ref(q_out), _ref(k), _ref(v), _format(format), _ref(k_pool), _ref(v_pool),
+                            _ref(pt), _ints(d_rows, "d_rows"), _ints(d_at, "d_at"), _ints(d_pos, "d_pos"),
+                            _addr(stream)), "kv8_append")
+
+
+def kv8_read(format, k_pool: tmap_t, v_pool: tmap_t, pt: page_table_t, d_rows, d_at, k: tmap_t, v: tmap_t,
+             stream=0) -> None:
+    _check(lib().kv8_read(_format(format), _ref(k_pool), _ref(v_pool), _ref(pt), _ints(d_rows, "d_rows"),
+                          _ints(d_at, "d_at"), _ref(k), _ref(v), _addr(stream)), "kv8_read")
+
+
 def page_table(d_table, d_lens, d_refs, pages: int, slots: int, rows: int = 0, row_pages: int = 0,
                pitch: int = 0) -> page_table_t:
     """The struct of a table, lengths and counts.  rows, row_pages and pitch
@@ -449,6 +484,20 @@ def page_compact(pt: page_table_t, pt_to: page_table_t, pools, d_used, d_ws, str
     arr, k = _pool_array(pools)
     _check(lib().page_compact(_ref(pt), _ref(pt_to), arr, k, _ints(d_used, "d_used"), _addr(d_ws),
                               ws_bytes or _nbytes(d_ws), _addr(stream)), "page_compact")
+
+
+def page_keep(pt: page_table_t, pools, d_rows, d_from, d_keep, d_count, n: int, d_ok, stream=0, width: int = 0) -> None:
+    """pools as page_fork.  d_keep is a 2-D tensor [n, width], or an address
+    with width."""
+    arr, k = _pool_array(pools)
+    shape = getattr(d_keep, "shape", None)
+    if shape is not None:
+        if len(shape) != 2 or shape[0] < n:
+            raise ValueError(f"d_keep has to hold {n} rows")
+        width = int(shape[1])
+    _check(lib().page_keep(_ref(pt), arr, k, _ints(d_rows, "d_rows"), _ints(d_from, "d_from"), _ints(d_keep, "d_keep"),
+                           int(width), _ints(d_count, "d_count"), int(n), _ints(d_ok, "d_ok"), _addr(stream)),
+           "page_keep")
 
 
 def attn_workspace(q: tmap_t, k_pool: tmap_t, prefix_len: int, suffix_hint: int) -> int:

@@ -50,6 +50,18 @@ inline tmap_status check_table(const page_table_t* pt) {
     return TMAP_OK;
 }
 
+// Rows of dim bytes in a head of a page of 8-bit codes, 0 where there are none.
+inline uint32_t code_rows(uint64_t slots, uint64_t dim) {
+    if (dim == 0 || dim % 16 != 0 || dim > 256 || slots == 0 || slots > 0x7FFFFFFFull) return 0;
+    return (uint32_t)(slots + (2 * slots + dim - 1) / dim);
+}
+
+// Offset in a head of a page of the scale of a slot.
+__device__ __forceinline__ int64_t scale_offset(uint32_t slot, uint32_t slots, uint32_t dim, int64_t row_stride) {
+    const uint32_t row = 2u * slot / dim;                         // slot < 2^31
+    return ((int64_t)slots + row) * row_stride + (2u * slot - row * dim);
+}
+
 // Workgroups along x that one launch holds: HIP counts a grid's threads of one
 // dimension in 32 bits.  Calls with more work launch again for the rest.
 constexpr uint32_t max_groups(uint32_t threads) { return 0xFFFFFFFFu / threads; }

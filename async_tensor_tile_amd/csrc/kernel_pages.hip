@@ -1,5 +1,5 @@
 // kernel_pages.hip -- the pages of the cache: handing out, sharing, giving
-// back, copying and compacting.
+// back, copying and compacting, and rows that keep some of their last tokens.
 //
 // A page's use count says how many rows hold it.  Handing pages out takes a
 // rank over the free pages (lowest index first) and a running sum over the
@@ -579,6 +579,126 @@ __global__ __launch_bounds__(kScanThreads) void k_compact_one(const Table t, int
     move_pages(p, moves, mover, hole, blockIdx.x * groups + tid / kCopyThreads, gridDim.x * groups, tid % kCopyThreads);
 }
 
+// ---- keeping some of the last tokens ------------------------------------------------
+
+// Pools of one geometry by token: a token of a head is `bytes` bytes, and in a
+// pool of codes a scale of two more.
+template <uint32_t N>
+struct TokensOf {
+    int64_t page, slot, head;     // byte strides
+    uint32_t npool, heads, bytes, codes, dim;
+    uint64_t base[N];
+};
+typedef TokensOf<kMaxPools> Tokens;
+typedef TokensOf<kFewPools> FewTokens;
+
+constexpr uint32_t kKeepThreads = 128;
+constexpr uint32_t kKeepTokens = 128;     // tokens whose places are worked out together
+
+// Entry i and one pool: the checks, the same in every workgroup of the entry and
+// all on what no workgroup of this launch changes, then the moves.  Kept tokens
+// ascend, so token j comes from index j or above: a thread that moves its piece
+// of each token in their order, a few loads ahead, never reads what it wrote.
+template <uint32_t N>
+__global__ __launch_bounds__(kKeepThreads) void k_page_keep(const Table t, const TokensOf<N> p, const int32_t* rows,
+                                                            const int32_t* from, const int32_t* keep, uint32_t width,
+                                                            const int32_t* count, int32_t* ok, uint32_t* err) {
+    __shared__ int64_t src[kKeepTokens], dst[kKeepTokens];              // of the tokens; -1: stays where it is
+    __shared__ int64_t src_scale[kKeepTokens], dst_scale[kKeepTokens];
+    const uint32_t tid = threadIdx.x, i = blockIdx.x;
+    const uint32_t row = (uint32_t)rows[i];
+    const int64_t first = from[i], n = count[i], room = (int64_t)t.slots * t.row_pages;
+    const int32_t* kept = keep + (uint64_t)i * width;
+    int64_t len = -1;
+    if (row < t.rows) len = t.lens[row];
+    if ((len < 0 || len > room) && tid == 0 && blockIdx.y == 0) record_page_error(err);
+    bool good = len >= 0 && len <= room && first >= 0 && first <= len && n >= 0 && n <= (int64_t)width;
+    const int32_t* entries = t.table + (uint64_t)row * t.pitch;
+    if (good) {
+        for (uint32_t j = tid; j < (uint32_t)n; j += kKeepThreads) {
+            const int64_t k = kept[j], before = j ? kept[j - 1] : -1;
+            if (k <= before || first + k >= len) {
+                good = false;
+                break;
+            }
+            if (k == (int64_t)j) continue;
+            const int32_t a = entries[(uint32_t)(first + k) / t.slots], b = entries[(uint32_t)(first + j) / t.slots];
+            if ((uint32_t)a >= t.pages || (uint32_t)b >= t.pages) {
+                record_page_error(err);
+                good = false;
+            } else if (t.refs[b] > 1) {
+                good = false;
+            }
+        }
+    }
+    good = __syncthreads_and(good);
+    if (blockIdx.y == 0 && tid == 0) ok[i] = good;
+    if (!good || p.npool == 0) return;
+    gbyte* const pool = gptr(p.base[blockIdx.y]);
+    const uint32_t chunks = (p.bytes + 15u) / 16u, pieces = p.heads * chunks, units = pieces + (p.codes ? p.heads : 0u);
+    for (uint32_t j0 = 0; j0 < (uint32_t)n; j0 += kKeepTokens) {
+        const uint32_t m = (uint32_t)n - j0 < kKeepTokens ? (uint32_t)n - j0 : kKeepTokens;
+        if (j0) __syncthreads();                                        // the places before are used
+        if (tid < m) {
+            const uint32_t j = j0 + tid, k = (uint32_t)kept[j];
+            src[tid] = dst[tid] = -1;
+            if (k != j) {
+                const uint32_t from_at = (uint32_t)first + k, to_at = (uint32_t)first + j;
+                const uint32_t from_slot = from_at % t.slots, to_slot = to_at % t.slots;
+                const int64_t a = entries[from_at / t.slots] * p.page, b = entries[to_at / t.slots] * p.page;
+                src[tid] = a + (int64_t)from_slot * p.slot;
+                dst[tid] = b + (int64_t)to_slot * p.slot;
+                if (p.codes) {
+                    src_scale[tid] = a + scale_offset(from_slot, t.slots, p.dim, p.slot);
+                    dst_scale[tid] = b + scale_offset(to_slot, t.slots, p.dim, p.slot);
+                }
+            }
+        }
+        __syncthreads();
+        for (uint32_t u = tid; u < units; u += kKeepThreads) {
+            const bool scale = u >= pieces;
+            const uint32_t h = scale ? u - pieces : u / chunks, c = scale ? 0u : u - h * chunks;
+            const int64_t off = (int64_t)h * p.head + c * 16u;
+            const uint32_t left = scale ? 2u : p.bytes - c * 16u < 16u ? p.bytes - c * 16u : 16u;
+            constexpr uint32_t U = 8;                                   // loads in flight
+            for (uint32_t j = 0; j < m; j += U) {
+                u32x4 v[U];
+                uint16_t s[U];
+#pragma unroll
+                for (uint32_t x = 0; x < U; ++x) {
+                    if (j + x >= m || src[j + x] < 0) continue;
+                    if (scale) s[x] = *(const ATT_GLOBAL uint16_t*)(pool + src_scale[j + x] + off);
+                    else if (left == 16u) v[x] = *(const ATT_GLOBAL u32x4*)(pool + src[j + x] + off);
+                }
+#pragma unroll
+                for (uint32_t x = 0; x < U; ++x) {
+                    if (j + x >= m || src[j + x] < 0) continue;
+                    if (scale) *(ATT_GLOBAL uint16_t*)(pool + dst_scale[j + x] + off) = s[x];
+                    else if (left == 16u) *(ATT_GLOBAL u32x4*)(pool + dst[j + x] + off) = v[x];
+                    else for (uint32_t e = 0; e < left; ++e) pool[dst[j + x] + off + e] = pool[src[j + x] + off + e];
+                }
+            }
+        }
+    }
+}
+
+// The rows of served entries end behind what they kept, one wave a row.
+__global__ __launch_bounds__(64) void k_page_end(const Table t, const int32_t* rows, const int32_t* from,
+                                                 const int32_t* count, const int32_t* ok, uint32_t* err) {
+    const uint32_t i = blockIdx.x;
+    if (!ok[i]) return;
+    const uint32_t row = (uint32_t)rows[i], len = (uint32_t)t.lens[row], end = (uint32_t)from[i] + (uint32_t)count[i];
+    const uint32_t c0 = (end + t.slots - 1u) / t.slots, c1 = (len + t.slots - 1u) / t.slots;
+    int32_t* const entries = t.table + (uint64_t)row * t.pitch;
+    for (uint32_t c = c0 + threadIdx.x; c < c1; c += 64u) {
+        const int32_t page = entries[c];
+        entries[c] = -1;
+        if ((uint32_t)page < t.pages) atomicSub(&t.refs[page], 1);
+        else record_page_error(err);
+    }
+    if (threadIdx.x == 0) t.lens[row] = (int32_t)end;
+}
+
 // ---- host ------------------------------------------------------------------------
 
 static tmap_status pools_of(const tmap_t* maps, uint32_t npool, const page_table_t* pt, Pools* out, uint32_t* pages) {
@@ -605,7 +725,9 @@ static tmap_status pools_of(const tmap_t* maps, uint32_t npool, const page_table
         out->base[i] = w.base;
     }
     if (v.dim[3] > 0x7FFFFFFF) return TMAP_ERR_UNSUPPORTED;
-    if (pt && ((uint64_t)v.dim[1] != pt->slots || (uint64_t)v.dim[3] != pt->pages)) return TMAP_ERR_UNSUPPORTED;
+    const bool codes = pt && type == TMAP_U8 && (uint64_t)v.dim[1] == code_rows(pt->slots, (uint64_t)v.dim[0]);
+    if (pt && (((uint64_t)v.dim[1] != pt->slots && !codes) || (uint64_t)v.dim[3] != pt->pages))
+        return TMAP_ERR_UNSUPPORTED;
     // 256 MiB of one page; a map's dimensions may count more bytes than 64 bits
     constexpr uint64_t most = 1ull << 28;
     if ((unsigned __int128)v.dim[0] * v.stride[0] * v.dim[1] > most ||
@@ -851,4 +973,56 @@ extern "C" tmap_status page_compact(const page_table_t* from, const page_table_t
         hipLaunchKernelGGL(k_compact_move, grid, block, 0, s, table_of(from), to->d_table, to->pitch, to->d_refs, p,
                            ws, table_blocks, err);
     return check_launch("page_compact");
+}
+
+extern "C" tmap_status page_keep(const page_table_t* pt, const tmap_t* pools, uint32_t npool, const int32_t* d_rows,
+                                 const int32_t* d_from, const int32_t* d_keep, uint32_t width, const int32_t* d_count,
+                                 uint32_t n, int32_t* d_ok, void* stream) {
+    tmap_status st = check_table(pt);
+    if (st) return st;
+    if (!pt->d_lens || !pt->d_refs) return TMAP_ERR_NULL;
+    Pools checked;
+    uint32_t pages = 0;
+    st = pools_of(pools, npool, pt, &checked, &pages);
+    if (st) return st;
+    if (n == 0) return TMAP_OK;
+    if (!d_rows || !d_from || (!d_keep && width) || !d_count || !d_ok) return TMAP_ERR_NULL;
+    Tokens p;
+    std::memset(&p, 0, sizeof(p));
+    p.npool = npool;
+    if (npool) {
+        View v;
+        int32_t type;
+        st = view_of(pools, 4, &v, &type);
+        if (st) return st;
+        p.page = v.stride[3];
+        p.slot = v.stride[1];
+        p.head = v.stride[2];
+        p.heads = (uint32_t)v.dim[2];                          // a page's bytes are at most 2^28
+        p.dim = (uint32_t)v.dim[0];
+        p.bytes = (uint32_t)(v.dim[0] * v.stride[0]);
+        p.codes = (uint64_t)v.dim[1] != pt->slots;
+        std::memcpy(p.base, checked.base, sizeof(p.base));
+    }
+    FewTokens few_tokens;
+    std::memcpy(&few_tokens, &p, sizeof(few_tokens));          // the same fields, fewer bases
+    uint32_t* err = nullptr;
+    st = device_error_word(&err);
+    if (st) return st;
+    const hipStream_t s = as_stream(stream);
+    const Table t = table_of(pt);
+    constexpr uint32_t most = max_groups(kKeepThreads);
+    for (uint32_t i = 0, m = 0; i < n; i += m) {
+        m = n - i < most ? n - i : most;
+        const dim3 grid(m, npool ? npool : 1u);
+        const int32_t* keep = d_keep + (uint64_t)i * width;
+        if (npool <= kFewPools)
+            hipLaunchKernelGGL(k_page_keep, grid, dim3(kKeepThreads), 0, s, t, few_tokens, d_rows + i, d_from + i, keep,
+                               width, d_count + i, d_ok + i, err);
+        else
+            hipLaunchKernelGGL(k_page_keep, grid, dim3(kKeepThreads), 0, s, t, p, d_rows + i, d_from + i, keep, width,
+                               d_count + i, d_ok + i, err);
+        hipLaunchKernelGGL(k_page_end, dim3(m), dim3(64), 0, s, t, d_rows + i, d_from + i, d_count + i, d_ok + i, err);
+    }
+    return check_launch("page_keep");
 }

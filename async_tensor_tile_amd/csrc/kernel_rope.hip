@@ -1,6 +1,6 @@
 // kernel_rope.hip -- rotary positions: the plan's encoder, the rotation of a
-// tensor of heads, and the step that writes a token's keys and values to
-// their page.
+// tensor of heads, and the steps that write a token's keys and values to
+// their page, as they are or as 8-bit codes.
 //
 // Pair j of a head turns by position * theta_j.  The plan holds theta_j / 2 pi
 // (turns per position) in 64 bits; a kernel takes the product with the
@@ -113,16 +113,12 @@ __device__ __forceinline__ void store_chunk(const Chunk<T>& c, gbyte* p, uint32_
     }
 }
 
-// STREAM: the call writes more than the L2s hold, so its output is not kept
-// there.
-template <typename T, int MODE, bool STREAM, uint32_t P>
-__global__ __launch_bounds__(kRopeThreads) void k_rope(const RopeTurns<P> plan, const RopeArgs a) {
-    constexpr uint32_t N = Chunk<T>::N;
-    __shared__ float2 turn[kTokMax][P];           // magnitude * (cos, sin)
-    __shared__ int2 where[kTokMax];               // page (-1: none) and slot
-    const uint32_t tid = threadIdx.x;
-    const uint32_t t0 = blockIdx.x * a.tok_block;
-    const uint32_t pairs = a.rot / 2;
+// What a workgroup's threads share: the turned pairs of its tokens, and where in
+// the pools the tokens go.
+template <uint32_t P>
+__device__ __forceinline__ void place_tokens(const RopeTurns<P>& plan, const RopeArgs& a, uint32_t t0,
+                                             float2 (&turn)[kTokMax][P], int2 (&where)[kTokMax]) {
+    const uint32_t tid = threadIdx.x, pairs = a.rot / 2;
     for (uint32_t i = tid; i < a.tok_block * pairs; i += kRopeThreads) {
         const uint32_t k = i / pairs, j = i - k * pairs;
         if (t0 + k < a.tokens) {
@@ -148,6 +144,19 @@ __global__ __launch_bounds__(kRopeThreads) void k_rope(const RopeTurns<P> plan, 
         where[tid] = w;
     }
     __syncthreads();
+}
+
+// STREAM: the call writes more than the L2s hold, so its output is not kept
+// there.
+template <typename T, int MODE, bool STREAM, uint32_t P>
+__global__ __launch_bounds__(kRopeThreads) void k_rope(const RopeTurns<P> plan, const RopeArgs a) {
+    constexpr uint32_t N = Chunk<T>::N;
+    __shared__ float2 turn[kTokMax][P];           // magnitude * (cos, sin)
+    __shared__ int2 where[kTokMax];               // page (-1: none) and slot
+    const uint32_t tid = threadIdx.x;
+    const uint32_t t0 = blockIdx.x * a.tok_block;
+    const uint32_t pairs = a.rot / 2;
+    place_tokens(plan, a, t0, turn, where);
 
     const uint32_t u = tid % a.units, hl = (tid / a.units) % a.head_lanes, k = tid / (a.units * a.head_lanes);
     if (k >= a.tok_block || t0 + k >= a.tokens) return;
@@ -249,6 +258,147 @@ __global__ __launch_bounds__(kRopeThreads) void k_rope(const RopeTurns<P> plan, 
     }
 }
 
+// ---- 8-bit codes ------------------------------------------------------------------
+
+// One head of a pool's row, or of the queries, by a group of lanes: each holds 8
+// elements and reads their partners too, so that the largest magnitude of the
+// head is a few exchanges away and the codes are written from registers.  A
+// group lies in one wave, whose loads of a head precede its stores: the queries
+// may be turned in place.
+struct CodeArgs {
+    RopeArgs r;
+    uint32_t group;          // lanes of a head, a power of two
+    uint32_t lanes;          // heads that the workgroup's lanes of one token hold at once
+    float top;               // largest code
+    uint32_t e4m3;
+};
+
+// Codes of 8 elements.  y / s is rounded to fp32 as the division itself would
+// be: s has 8 significant bits and the elements 8 or 11 (a value) or 24 (a turned
+// key), so values that lie on the border between two codes stay on it.
+__device__ __forceinline__ uint64_t codes_of(const float (&y)[8], float s, float top, bool e4m3) {
+    float z[8];
+#pragma unroll
+    for (uint32_t i = 0; i < 8; ++i) z[i] = fminf(fmaxf(y[i] / s, -top), top);
+    uint32_t lo = 0, hi = 0;
+    if (e4m3) {
+        int32_t a = 0, b = 0;
+        a = __builtin_amdgcn_cvt_pk_fp8_f32(z[0], z[1], a, false);
+        a = __builtin_amdgcn_cvt_pk_fp8_f32(z[2], z[3], a, true);
+        b = __builtin_amdgcn_cvt_pk_fp8_f32(z[4], z[5], b, false);
+        b = __builtin_amdgcn_cvt_pk_fp8_f32(z[6], z[7], b, true);
+        lo = (uint32_t)a;
+        hi = (uint32_t)b;
+    } else {
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i) {
+            lo |= ((uint32_t)(int32_t)rintf(z[i]) & 0xFFu) << (8u * i);
+            hi |= ((uint32_t)(int32_t)rintf(z[i + 4]) & 0xFFu) << (8u * i);
+        }
+    }
+    return (uint64_t)hi << 32 | lo;
+}
+
+template <typename T, int MODE, bool STREAM, uint32_t P>
+__global__ __launch_bounds__(kRopeThreads) void k_rope_codes(const RopeTurns<P> plan, const CodeArgs c) {
+    const RopeArgs& a = c.r;
+    __shared__ float2 turn[kTokMax][P];
+    __shared__ int2 where[kTokMax];
+    const uint32_t t0 = blockIdx.x * a.tok_block, half = a.rot / 2;
+    place_tokens(plan, a, t0, turn, where);
+
+    const uint32_t u = threadIdx.x & (c.group - 1u), first = threadIdx.x / c.group;
+    const uint32_t k = first / c.lanes, hl = first - k * c.lanes, t = t0 + k;
+    if (k >= a.tok_block || t >= a.tokens) return;              // whole groups
+    const uint32_t e0 = u * 8u;
+    const bool there = e0 < a.dim;
+    // each element's cosine, sine (below 0 for the first of a pair) and partner
+    float cs[8], sn[8];
+    uint32_t partner[8];
+    bool any = false;
+#pragma unroll
+    for (uint32_t i = 0; i < 8; ++i) {
+        const uint32_t e = e0 + i;
+        const bool on = e < a.rot, second = MODE == PAIRED ? i & 1u : e >= half;
+        partner[i] = !on ? e : MODE == PAIRED ? e ^ 1u : second ? e - half : e + half;
+        const float2 v = on ? turn[k][MODE == PAIRED ? e / 2u : second ? e - half : e] : make_float2(1.0f, 0.0f);
+        cs[i] = v.x;
+        sn[i] = second ? v.y : -v.y;
+        any |= on;
+    }
+    constexpr uint32_t U = 2;                                   // heads in flight per group
+    for (uint32_t s = 0; s < a.nseg; ++s) {
+        const RopeSeg& g = a.seg[s];
+        int64_t off = (int64_t)t * g.dst_tok, tail = 0;
+        if (g.dst_page) {
+            const int2 w = where[k];
+            if (w.x < 0) continue;
+            off = (int64_t)w.x * g.dst_page;
+            tail = off + scale_offset((uint32_t)w.y, a.slots, a.dim, g.dst_tok);
+            off += (int64_t)w.y * g.dst_tok;
+        }
+        const gbyte* src = gptr(g.src) + (int64_t)t * g.src_tok;
+        gbyte* dst = gptr(g.dst);
+        const bool rot = any && g.rotate;
+        for (uint32_t h0 = hl; h0 < g.heads; h0 += U * c.lanes) {
+            Chunk<T> x[U], y[U];
+#pragma unroll
+            for (uint32_t i = 0; i < U; ++i) {
+                const uint32_t h = h0 + i * c.lanes;
+                const u32x4 none = (u32x4)(0u);
+                __builtin_memcpy(&x[i], &none, 16);
+                if (h >= g.heads || !there) continue;
+                const gbyte* p = src + (int64_t)h * g.src_head;
+                load_chunk(x[i], p + e0 * sizeof(T), 8u);
+                if (MODE == PAIRED || !rot) continue;
+                if (MODE == SPLIT) {
+                    load_chunk(y[i], p + partner[0] * sizeof(T), 8u);
+                } else {
+#pragma unroll
+                    for (uint32_t q = 0; q < 8; ++q) y[i].e[q] = ((const ATT_GLOBAL T*)p)[partner[q]];
+                }
+            }
+#pragma unroll
+            for (uint32_t i = 0; i < U; ++i) {
+                const uint32_t h = h0 + i * c.lanes;
+                if (h >= g.heads) break;                        // whole groups
+                float z[8];
+#pragma unroll
+                for (uint32_t q = 0; q < 8; ++q) {
+                    const float own = (float)x[i].e[q];
+                    const float other = (float)(MODE == PAIRED ? x[i].e[q ^ 1u] : y[i].e[q]);
+                    z[q] = rot && e0 + q < a.rot ? own * cs[q] + other * sn[q] : own;
+                }
+                gbyte* p = dst + (int64_t)h * g.dst_head;
+                if (!g.dst_page) {
+                    Chunk<T> w;
+#pragma unroll
+                    for (uint32_t q = 0; q < 8; ++q) w.e[q] = (T)z[q];
+                    if (there) store_chunk<STREAM>(w, p + off + e0 * sizeof(T), 8u);
+                    continue;
+                }
+                uint32_t most = 0;                              // as bits: infinities and NaN are above all numbers
+#pragma unroll
+                for (uint32_t q = 0; q < 8; ++q) {
+                    const uint32_t b = __builtin_bit_cast(uint32_t, z[q]) & 0x7FFFFFFFu;
+                    most = b > most ? b : most;
+                }
+                for (uint32_t d = 1; d < c.group; d <<= 1) {
+                    const uint32_t b = __shfl_xor(most, d);
+                    most = b > most ? b : most;
+                }
+                const bool odd = most >= 0x7F800000u;
+                const uint32_t up = __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, most) / c.top) + 0xFFFFu;
+                const uint32_t bits = odd ? 0x7FC0u : up >> 16;
+                const float scale = __builtin_bit_cast(float, bits << 16);
+                const uint64_t code = odd || bits == 0 ? 0ull : codes_of(z, scale, c.top, c.e4m3);
+                if (there) *(ATT_GLOBAL uint64_t*)(p + off + e0) = code;
+                if (u == 0) *(ATT_GLOBAL uint16_t*)(p + tail) = (uint16_t)bits;
+            }
+        }
+    }
+}
+
 // The arguments of the tokens behind the first n.
 static void skip_tokens(RopeArgs& a, uint32_t n) {
     for (uint32_t i = 0; i < a.nseg; ++i) {
@@ -311,6 +461,44 @@ static void launch_mode(const RopePlan& plan, RopeArgs& a, hipStream_t stream) {
     if (mode == PAIRED) launch_size<T, PAIRED>(plan, a, stream_out, stream);
     else if (mode == SPLIT) launch_size<T, SPLIT>(plan, a, stream_out, stream);
     else launch_size<T, ELEMENTS>(plan, a, stream_out, stream);
+}
+
+template <typename T, int MODE, bool STREAM, uint32_t P>
+static void launch_code_pairs(const RopePlan& plan, const CodeArgs& c, hipStream_t stream) {
+    RopeTurns<P> turns;
+    std::memcpy(&turns, plan.turns, sizeof(turns));
+    constexpr uint32_t most = max_groups(kRopeThreads);
+    CodeArgs part = c;
+    for (uint32_t left = c.r.tokens; left; left -= part.r.tokens) {
+        const uint32_t groups = (left - 1) / c.r.tok_block + 1;
+        part.r.tokens = groups <= most ? left : most * c.r.tok_block;
+        const dim3 grid((part.r.tokens - 1) / c.r.tok_block + 1);
+        hipLaunchKernelGGL((k_rope_codes<T, MODE, STREAM, P>), grid, dim3(kRopeThreads), 0, stream, turns, part);
+        skip_tokens(part.r, part.r.tokens);
+    }
+}
+
+template <typename T, int MODE>
+static void launch_code_size(const RopePlan& plan, const CodeArgs& c, bool stream_out, hipStream_t stream) {
+    if (stream_out) launch_code_pairs<T, MODE, true, kMaxPairs>(plan, c, stream);
+    else if (c.r.rot <= 128) launch_code_pairs<T, MODE, false, 64>(plan, c, stream);
+    else launch_code_pairs<T, MODE, false, kMaxPairs>(plan, c, stream);
+}
+
+template <typename T>
+static void launch_codes(const RopePlan& plan, CodeArgs& c, hipStream_t stream) {
+    RopeArgs& a = c.r;
+    c.group = 1;
+    while (c.group * 8u < a.dim) c.group *= 2u;
+    // two tokens a workgroup share its start once there are enough to fill the GPU
+    a.tok_block = a.tokens < 1024u ? 1u : kTokMax;
+    c.lanes = kRopeThreads / (c.group * a.tok_block);
+    uint64_t heads = 0;
+    for (uint32_t i = 0; i < a.nseg; ++i) heads += a.seg[i].heads;
+    const bool stream_out = heads * a.tokens * a.dim * sizeof(T) > (32ull << 20);
+    if (plan.layout == ROPE_INTERLEAVED) launch_code_size<T, PAIRED>(plan, c, stream_out, stream);
+    else if (a.rot / 2 % 8 == 0) launch_code_size<T, SPLIT>(plan, c, stream_out, stream);
+    else launch_code_size<T, ELEMENTS>(plan, c, stream_out, stream);
 }
 
 static tmap_status launch_rope(const RopePlan& plan, RopeArgs& a, bool inverse, int32_t dtype, void* stream,
@@ -411,13 +599,14 @@ extern "C" tmap_status rope_apply(const rope_t* r, const tmap_t* x, const tmap_t
     return launch_rope(plan, a, inverse != 0, tx, stream, "rope_apply");
 }
 
-extern "C" tmap_status rope_append(const rope_t* r, const tmap_t* q, const tmap_t* q_out, const tmap_t* k,
-                                   const tmap_t* v, const tmap_t* k_pool, const tmap_t* v_pool,
-                                   const page_table_t* pt, const int32_t* d_rows, const int32_t* d_at,
-                                   const int32_t* d_pos, void* stream) {
+// The checks and arguments of a step's tokens; codes: the pools hold 8-bit codes.
+static tmap_status append_args(const rope_t* r, const tmap_t* q, const tmap_t* q_out, const tmap_t* k,
+                               const tmap_t* v, bool codes, const tmap_t* k_pool, const tmap_t* v_pool,
+                               const page_table_t* pt, const int32_t* d_rows, const int32_t* d_at,
+                               const int32_t* d_pos, RopePlan* plan_out, RopeArgs* out, int32_t* dtype) {
     if (!k || !v || !k_pool || !v_pool || !pt || !d_rows || !d_at) return TMAP_ERR_NULL;
     if ((r && !d_pos) || (q != nullptr) != (q_out != nullptr)) return TMAP_ERR_NULL;
-    RopeArgs a;
+    RopeArgs& a = *out;
     std::memset(&a, 0, sizeof(a));
     View vk, vv, pk, pv;
     int32_t tk, tv, tpk, tpv;
@@ -427,14 +616,16 @@ extern "C" tmap_status rope_append(const rope_t* r, const tmap_t* q, const tmap_
     if (st == TMAP_OK) st = view_of(v_pool, 4, &pv, &tpv);
     if (st == TMAP_OK) st = check_table(pt);
     if (st) return st;
-    if (!rope_type(tk)) return TMAP_ERR_DTYPE;
-    RopePlan plan;
+    if (!rope_type(tk) || (codes && tk == TMAP_F32)) return TMAP_ERR_DTYPE;
+    RopePlan& plan = *plan_out;
     std::memset(&plan, 0, sizeof(plan));
     if (r) plan = load_plan(r);
     if (r && plan.rot < 2) return TMAP_ERR_UNSUPPORTED;
-    if (tv != tk || tpk != tk || tpv != tk || !same_dims(vk, vv) || !same_dims(pk, pv) ||
+    const int32_t tp = codes ? (int32_t)TMAP_U8 : tk;
+    const int64_t rows = codes ? code_rows(pt->slots, (uint64_t)pk.dim[0]) : pt->slots;
+    if (tv != tk || tpk != tp || tpv != tp || !same_dims(vk, vv) || !same_dims(pk, pv) ||
         !heads_fit(vk, plan.rot) || pk.dim[0] != vk.dim[0] || pk.dim[2] != vk.dim[1] ||
-        pk.dim[1] != pt->slots || pk.dim[3] != pt->pages)
+        pk.dim[1] != rows || pk.dim[3] != pt->pages)
         return TMAP_ERR_UNSUPPORTED;
     if (q) {
         View vq, vo;
@@ -462,7 +653,41 @@ extern "C" tmap_status rope_append(const rope_t* r, const tmap_t* q, const tmap_
     a.slots = pt->slots;
     a.tokens = (uint32_t)vk.dim[2];
     a.dim = (uint32_t)vk.dim[0];
-    st = device_error_word(&a.err);
+    *dtype = tk;
+    return TMAP_OK;
+}
+
+extern "C" tmap_status rope_append(const rope_t* r, const tmap_t* q, const tmap_t* q_out, const tmap_t* k,
+                                   const tmap_t* v, const tmap_t* k_pool, const tmap_t* v_pool,
+                                   const page_table_t* pt, const int32_t* d_rows, const int32_t* d_at,
+                                   const int32_t* d_pos, void* stream) {
+    RopePlan plan;
+    RopeArgs a;
+    int32_t type;
+    tmap_status st = append_args(r, q, q_out, k, v, false, k_pool, v_pool, pt, d_rows, d_at, d_pos, &plan, &a, &type);
+    if (st == TMAP_OK) st = device_error_word(&a.err);
     if (st) return st;
-    return launch_rope(plan, a, false, tk, stream, "rope_append");
+    return launch_rope(plan, a, false, type, stream, "rope_append");
+}
+
+extern "C" tmap_status kv8_append(const rope_t* r, const tmap_t* q, const tmap_t* q_out, const tmap_t* k,
+                                  const tmap_t* v, int32_t format, const tmap_t* k_pool, const tmap_t* v_pool,
+                                  const page_table_t* pt, const int32_t* d_rows, const int32_t* d_at,
+                                  const int32_t* d_pos, void* stream) {
+    RopePlan plan;
+    CodeArgs c;
+    std::memset(&c, 0, sizeof(c));
+    int32_t type;
+    tmap_status st = append_args(r, q, q_out, k, v, true, k_pool, v_pool, pt, d_rows, d_at, d_pos, &plan, &c.r, &type);
+    if (st) return st;
+    if (format != KV_INT8 && format != KV_E4M3) return TMAP_ERR_UNSUPPORTED;
+    st = device_error_word(&c.r.err);
+    if (st) return st;
+    c.e4m3 = format == KV_E4M3;
+    c.top = c.e4m3 ? 448.0f : 127.0f;
+    c.r.rot = plan.rot;
+    c.r.magnitude = c.r.sine = plan.magnitude;
+    if (type == TMAP_F16) launch_codes<_Float16>(plan, c, as_stream(stream));
+    else launch_codes<__bf16>(plan, c, as_stream(stream));
+    return check_launch("kv8_append");
 }

@@ -1,6 +1,7 @@
 /*
  * kvcache.h -- C ABI of a paged key / value cache on MI355X (gfx950): rotary
- * positions, the pages, and attention behind a shared prefix.
+ * positions, the pages, pools of 8 bits an element, and attention: behind a
+ * shared prefix, with a sliding window, and of a tree of drafted tokens.
  *
  * Keys and values live in pools of pages.  A pool is described by a tensor
  * map (tmap.h) of rank 4 with dims {dim, slots, heads, pages}: page p holds
@@ -99,6 +100,39 @@ tmap_status rope_append(const rope_t* r, const tmap_t* q, const tmap_t* q_out, c
                         const tmap_t* k_pool, const tmap_t* v_pool, const page_table_t* pt, const int32_t* d_rows,
                         const int32_t* d_at, const int32_t* d_pos, void* stream);
 
+/* ---- pools of 8 bits an element ------------------------------------------------ */
+
+/* What a pool's elements are: of the queries' type, or 8-bit codes c that
+ * stand for c * s, with a scale s for each token and head.  A pool of codes is
+ * a map of type u8 with dims {dim, kv8_rows(slots, dim), heads, pages}, dim a
+ * multiple of 16: in each head of a page the slots' codes are followed by the
+ * slots' scales, bf16 side by side, that of slot i at row slots + 2i / dim,
+ * byte 2i % dim.  page_copy, page_fork, page_compact and page_keep take such
+ * pools like any others. */
+enum { KV_SAME = 0, KV_INT8 = 1, KV_E4M3 = 2 };
+
+/* Rows of dim bytes that a head of a page with `slots` tokens takes, codes and
+ * scales (0 for a dim that is no multiple of 16 or above 256, or no slots). */
+uint32_t kv8_rows(uint32_t slots, uint32_t dim);
+
+/* rope_append to pools of codes.  With y the rotated key (or the value) of a
+ * head in fp32, and Z the largest code, 127 or 448: s is max |y| / Z rounded up
+ * to bf16, and c is y / s rounded to the nearest code, ties to even (0 where s
+ * is 0).  A head that holds an infinity or a NaN gets the scale NaN: it reads
+ * as NaN.  Types f16 and bf16; everything else, q_out among it, as
+ * rope_append.  Errors as rope_append, and UNSUPPORTED for another format. */
+tmap_status kv8_append(const rope_t* r, const tmap_t* q, const tmap_t* q_out, const tmap_t* k, const tmap_t* v,
+                       int32_t format, const tmap_t* k_pool, const tmap_t* v_pool, const page_table_t* pt,
+                       const int32_t* d_rows, const int32_t* d_at, const int32_t* d_pos, void* stream);
+
+/* Tokens of pools of codes read back: token t of k and v (dims {dim, heads,
+ * tokens}, types f16, bf16, f32) is token d_at[t] of row d_rows[t], c * s
+ * rounded once to the type.  Where d_rows[t] is negative, or there is no such
+ * token's page, k and v stay as they were.  Of pt only the table is read.
+ * Errors as kv8_append. */
+tmap_status kv8_read(int32_t format, const tmap_t* k_pool, const tmap_t* v_pool, const page_table_t* pt,
+                     const int32_t* d_rows, const int32_t* d_at, const tmap_t* k, const tmap_t* v, void* stream);
+
 /* ---- pages ------------------------------------------------------------------- */
 
 /* Bytes of workspace that page_fork and page_extend with up to n entries, and
@@ -151,6 +185,21 @@ tmap_status page_free(const page_table_t* pt, const int32_t* d_rows, uint32_t n,
  * above U as -1.  *d_used (may be NULL) receives U.  Errors as page_fork. */
 tmap_status page_compact(const page_table_t* from, const page_table_t* to, const tmap_t* pools, uint32_t npool,
                          int32_t* d_used, void* d_ws, uint64_t ws_bytes, void* stream);
+
+/* The tokens of row d_rows[i] from index d_from[i] on are replaced by some of
+ * them, i < n: token d_from[i] + d_keep[i * width + j] becomes token d_from[i] +
+ * j for j < d_count[i], in every pool, and the row then ends; the pages between
+ * its new end and the old one are given back.  So a row keeps the accepted ones
+ * of its drafted tokens.
+ * The d_count[i] <= width kept indices ascend from 0 or above and end below the
+ * row's length (none: the row is cut to d_from[i]).  d_ok[i] = 1, or 0 for an
+ * entry that is left as it was: where that does not hold, or where a page that
+ * would be written is shared (count above 1).  Rows are distinct.  pools may be
+ * NULL with npool == 0: the tables alone.  Errors: NULL, RANK, UNSUPPORTED
+ * (table, pools), HIP.  n == 0 is a no-op. */
+tmap_status page_keep(const page_table_t* pt, const tmap_t* pools, uint32_t npool, const int32_t* d_rows,
+                      const int32_t* d_from, const int32_t* d_keep, uint32_t width, const int32_t* d_count, uint32_t n,
+                      int32_t* d_ok, void* stream);
 
 /* ---- attention ---------------------------------------------------------------- */
 

@@ -58,6 +58,60 @@ def rope(x, pos, thetas, layout="half", magnitude=1.0, inverse=False):
     return y, size
 
 
+# ---- 8-bit codes -------------------------------------------------------------------
+
+LARGEST = {"int8": 127.0, "e4m3": 448.0}
+
+
+def code_rows(slots, dim):
+    return slots + -(-2 * slots // dim)
+
+
+def code_scale(y, fmt):
+    """Scale of each head of y [..., dim] (float64): the largest magnitude over
+    the largest code, rounded up to eight significant bits; NaN for a head with
+    an element that is not finite."""
+    odd = ~np.isfinite(y).all(-1)
+    s = np.where(odd, 0.0, np.abs(np.where(np.isfinite(y), y, 0.0)).max(-1)) / LARGEST[fmt]
+    _, e = np.frexp(s)                       # s = m * 2^e, m in [1/2, 1)
+    step = np.ldexp(1.0, np.maximum(e - 8, -133))
+    return np.where(odd, np.nan, np.ceil(s / step) * step)
+
+
+def code_step(z, fmt):
+    """The distance of the codes around z."""
+    if fmt == "int8":
+        return np.ones_like(z)
+    _, e = np.frexp(np.maximum(np.abs(z), 2.0 ** -6))
+    return np.ldexp(1.0, e - 4)              # four significant bits, steps of 2^-9 at least
+
+
+def codes(y, scale, fmt):
+    """The codes (as numbers) of y under scales of its heads."""
+    s = scale[..., None]
+    z = np.where(s > 0, np.where(np.isfinite(y), y, 0.0) / np.where(s > 0, s, 1.0), 0.0)
+    step = code_step(z, fmt)
+    return np.rint(z / step) * step
+
+
+def code_values(raw, fmt):
+    """The numbers that code bytes stand for."""
+    if fmt == "int8":
+        return raw.view(np.int8).astype(np.float64)
+    e, m = (raw >> 3 & 15).astype(np.int64), (raw & 7).astype(np.float64)
+    v = np.where(e == 0, np.ldexp(m, -9), np.ldexp(8 + m, e - 10))
+    v = np.where((raw & 0x7F) == 0x7F, np.nan, v)
+    return np.where(raw & 0x80, -v, v)
+
+
+def split_codes(pool, slots, fmt):
+    """Codes [pages, heads, slots, dim] and scales [pages, heads, slots] of a
+    pool of bytes [pages, heads, rows, dim]."""
+    p, h, _, _ = pool.shape
+    tail = np.ascontiguousarray(pool[:, :, slots:]).reshape(p, h, -1).view(np.uint16)[..., :slots]
+    return code_values(pool[:, :, :slots], fmt), to_f64(np.ascontiguousarray(tail), "bf16")
+
+
 # ---- page tables -------------------------------------------------------------------
 
 class Pages:
@@ -99,6 +153,31 @@ class Pages:
                     p = free[total - (end - k)]
                     self.table[r, k], self.refs[p] = p, 1
                 self.lens[r] = start[r] + n
+        return ok
+
+    def keep(self, rows, first, keep, count):
+        """Pools are [pages, slots, ...], token by token."""
+        ok, refs = [], self.refs.copy()
+        for r, f, ks, n in zip(rows, first, keep, count):
+            good = self._row_ok(r) and 0 <= f <= self.lens[r] and 0 <= n <= len(ks)
+            ks = [int(k) for k in ks[:max(0, n)]]
+            good = good and all(k > b for k, b in zip(ks, [-1] + ks)) and (not ks or f + ks[-1] < self.lens[r])
+            where = lambda i: (int(self.table[r, i // self.slots]), i % self.slots)  # noqa: E731
+            moves = [(where(f + k), where(f + j)) for j, k in enumerate(ks) if k != j] if good else []
+            good = good and all(0 <= p < len(refs) for m in moves for p, _ in m)
+            good = good and all(refs[p] <= 1 for _, (p, _) in moves)
+            ok.append(int(good))
+            if not good:
+                continue
+            for pool in self.pools:
+                for (sp, ss), (dp, ds) in moves:
+                    pool[dp, ds] = pool[sp, ss]
+            for c in range(-(-(f + n) // self.slots), -(-int(self.lens[r]) // self.slots)):
+                p = self.table[r, c]
+                if 0 <= p < len(self.refs):
+                    self.refs[p] -= 1
+                self.table[r, c] = -1
+            self.lens[r] = f + n
         return ok
 
     def fork(self, src, dst):
