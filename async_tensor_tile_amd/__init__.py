@@ -143,10 +143,14 @@ def lib():
         L.kv8_append.argtypes = [rp, tp, tp, tp, tp, _I32, tp, tp, pp, _V, _V, _V, _V]
         L.kv8_read.argtypes = [_I32, tp, tp, pp, _V, _V, tp, tp, _V]
         L.page_keep.argtypes = [pp, tp, _U32, _V, _V, _V, _U32, _V, _U32, _V, _V]
+        L.attn_cache_workspace.argtypes = [tp, tp, _U32, _U32, _U32]
+        L.attn_window.argtypes = [tp, tp, tp, _I32, pp, _V, _V, _U32, _U32, _U32, ctypes.c_float, tp, _V, _V, U64, _V]
+        L.attn_tree.argtypes = [tp, tp, tp, _I32, pp, _V, _V, _V, _U32, _U32, _U32, ctypes.c_float, tp, _V, _V, U64, _V]
         for name in ("rope_encode", "rope_apply", "rope_append", "page_copy", "page_extend", "page_fork", "page_free",
-                     "page_compact", "attn_shared_prefix", "kv8_append", "kv8_read", "page_keep"):
+                     "page_compact", "attn_shared_prefix", "kv8_append", "kv8_read", "page_keep", "attn_window",
+                     "attn_tree"):
             getattr(L, name).restype = _I32
-        L.page_workspace.restype = L.attn_workspace.restype = U64
+        L.page_workspace.restype = L.attn_workspace.restype = L.attn_cache_workspace.restype = U64
         _lib = L
     return _lib
 
@@ -504,12 +508,41 @@ def attn_workspace(q: tmap_t, k_pool: tmap_t, prefix_len: int, suffix_hint: int)
     return int(lib().attn_workspace(_ref(q), _ref(k_pool), int(prefix_len), int(suffix_hint)))
 
 
-def attn_shared_prefix(q: tmap_t, k_pool: tmap_t, v_pool: tmap_t, pt: page_table_t, prefix_row: int,
-                       prefix_len: int, d_rows, suffix_hint: int, scale: float, o: tmap_t, d_lse, d_ws, stream=0,
-                       ws_bytes: int = 0) -> None:
+def _check_lse(d_lse):
     if hasattr(d_lse, "data_ptr") and (d_lse.element_size() != 4 or not d_lse.is_floating_point() or
                                        not d_lse.is_contiguous()):
         raise TypeError("d_lse has to be float32 values side by side")
+
+
+def attn_shared_prefix(q: tmap_t, k_pool: tmap_t, v_pool: tmap_t, pt: page_table_t, prefix_row: int,
+                       prefix_len: int, d_rows, suffix_hint: int, scale: float, o: tmap_t, d_lse, d_ws, stream=0,
+                       ws_bytes: int = 0) -> None:
+    _check_lse(d_lse)
     _check(lib().attn_shared_prefix(_ref(q), _ref(k_pool), _ref(v_pool), _ref(pt), int(prefix_row), int(prefix_len),
                                     _ints(d_rows, "d_rows"), int(suffix_hint), float(scale), _ref(o), _addr(d_lse),
                                     _addr(d_ws), ws_bytes or _nbytes(d_ws), _addr(stream)), "attn_shared_prefix")
+
+
+def attn_cache_workspace(q: tmap_t, k_pool: tmap_t, window: int, sinks: int, len_hint: int) -> int:
+    return int(lib().attn_cache_workspace(_ref(q), _ref(k_pool), int(window), int(sinks), int(len_hint)))
+
+
+def attn_window(q: tmap_t, k_pool: tmap_t, v_pool: tmap_t, format, pt: page_table_t, d_rows, d_count, window: int,
+                sinks: int, len_hint: int, scale: float, o: tmap_t, d_lse, d_ws, stream=0, ws_bytes: int = 0) -> None:
+    """format: "same", "int8" or "e4m3" (or the KV_* value); d_rows, d_count and
+    d_lse may be None."""
+    _check_lse(d_lse)
+    _check(lib().attn_window(_ref(q), _ref(k_pool), _ref(v_pool), _format(format), _ref(pt), _ints(d_rows, "d_rows"),
+                             _ints(d_count, "d_count"), int(window), int(sinks), int(len_hint), float(scale), _ref(o),
+                             _addr(d_lse), _addr(d_ws), ws_bytes or _nbytes(d_ws), _addr(stream)), "attn_window")
+
+
+def attn_tree(q: tmap_t, k_pool: tmap_t, v_pool: tmap_t, format, pt: page_table_t, d_rows, d_count, d_parent,
+              window: int, sinks: int, len_hint: int, scale: float, o: tmap_t, d_lse, d_ws, stream=0,
+              ws_bytes: int = 0) -> None:
+    """As attn_window; d_parent holds q_len parents for each sequence."""
+    _check_lse(d_lse)
+    _check(lib().attn_tree(_ref(q), _ref(k_pool), _ref(v_pool), _format(format), _ref(pt), _ints(d_rows, "d_rows"),
+                           _ints(d_count, "d_count"), _ints(d_parent, "d_parent"), int(window), int(sinks),
+                           int(len_hint), float(scale), _ref(o), _addr(d_lse), _addr(d_ws), ws_bytes or _nbytes(d_ws),
+                           _addr(stream)), "attn_tree")

@@ -415,6 +415,53 @@ struct Wave {
         odd_values<true>(vals, from, to);
     }
 
+    // Whether share `part` of `parts` of a tile of `rows` values holds infinities
+    // or NaN (CLEAR: and those become 0); the same in every lane of the wave.
+    template <bool CLEAR>
+    __device__ __forceinline__ static bool odd_share(uint8_t* vals, uint32_t part, uint32_t parts, uint32_t rows) {
+        bool odd = false;
+        for (uint32_t i = part * 64u + lane_id(); i < rows * Geo<DP>::cpr; i += parts * 64u) {
+            union { u32x4 v; uint16_t e[8]; } x;
+            x.v = *reinterpret_cast<const u32x4*>(vals + i * 16u);
+#pragma unroll
+            for (uint32_t e = 0; e < 8; ++e)
+                if (not_finite(x.e[e])) {
+                    odd = true;
+                    x.e[e] = 0;
+                }
+            if (CLEAR) *reinterpret_cast<u32x4*>(vals + i * 16u) = x.v;
+        }
+        return __any(odd);
+    }
+
+    // The infinities and NaN among a tile's values, added to the rows that see
+    // their keys (a bit of `sees` each).
+    template <uint32_t NB>
+    __device__ __forceinline__ void add_odd(const uint8_t* vals, const f32x16 (&p)[NB], uint64_t sees) {
+        const uint32_t hh = lane_id() / 32u;
+        for (uint32_t key = 0; key < 32u * NB; ++key) {
+            const uint32_t at = 4u * (key % 32u / 8u) + key % 4u;
+            float x = 0.0f;
+#pragma unroll
+            for (uint32_t n = 0; n < NB; ++n)
+#pragma unroll
+                for (uint32_t i = 0; i < 16; ++i)
+                    if (n == key / 32u && i == at && (key >> 2 & 1u) == hh) x = p[n][i];
+            x = (float)(T)add_halves(x);
+            const uint8_t* row = vals + key * (DP * 2u) + 8u * hh;
+#pragma unroll
+            for (uint32_t f = 0; f < DP / 8u; ++f) {
+                const uint64_t bits = *reinterpret_cast<const uint64_t*>(row + (f ^ Geo<DP>::key_v(key)) * 16u);
+#pragma unroll
+                for (uint32_t e = 0; e < 4; ++e) {
+                    const uint16_t h = (uint16_t)(bits >> (16u * e));
+                    if (not_finite(h) && (sees >> key & 1u))
+                        o[f / 4u][4u * (f % 4u) + e] += x * (float)__builtin_bit_cast(T, h);
+                }
+            }
+        }
+    }
+
     // Sum of the weights over both halves.
     __device__ __forceinline__ float total() const { return add_halves(l); }
 };

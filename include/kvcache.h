@@ -236,6 +236,46 @@ tmap_status attn_shared_prefix(const tmap_t* q, const tmap_t* k_pool, const tmap
                                float scale, const tmap_t* o, float* d_lse, void* d_ws, uint64_t ws_bytes,
                                void* stream);
 
+/* Bytes of workspace that attn_window and attn_tree need for these queries,
+ * this pool, window, sinks and len_hint (0 if they are not valid). */
+uint64_t attn_cache_workspace(const tmap_t* q, const tmap_t* k_pool, uint32_t window, uint32_t sinks,
+                              uint32_t len_hint);
+
+/* Causal attention of sequences over the cache.  q and o have dims {dim, heads,
+ * q_len, batch}; of sequence b the first n = d_count[b] queries (NULL: q_len)
+ * are there, and what o and d_lse hold for the others stays as it was.  Its
+ * tokens are those of row r = d_rows[b] (NULL: b), and its queries the last n of
+ * them: query j stands at p = d_lens[r] - n + j and sees the tokens t <= p that
+ * are within the window, t > p - window, or among the first `sinks` ones
+ * (window 0: every t <= p).  o, lse, heads, types, scale and the rounding as
+ * attn_shared_prefix; a query that sees nothing gets o = 0 and lse = -inf, and
+ * what a query does not see does not reach it, whatever it holds.  The pools are
+ * of the queries' type (KV_SAME) or hold codes; a key is c * s, and a value is
+ * c * s rounded to the queries' type.  len_hint is the length that the work is
+ * split for (any value is right).  A count or row out of range is recorded: no
+ * query is there, or none sees a token.  Errors as attn_shared_prefix, and
+ * UNSUPPORTED for pools that are not of the format (more than 2^24 - 1
+ * workgroups: about one for each sequence, key / value head and 128 of its
+ * queries). */
+tmap_status attn_window(const tmap_t* q, const tmap_t* k_pool, const tmap_t* v_pool, int32_t format,
+                        const page_table_t* pt, const int32_t* d_rows, const int32_t* d_count, uint32_t window,
+                        uint32_t sinks, uint32_t len_hint, float scale, const tmap_t* o, float* d_lse, void* d_ws,
+                        uint64_t ws_bytes, void* stream);
+
+/* Attention of drafted tokens that form a tree.  As attn_window, but the last n
+ * tokens of the row are the tree's nodes: node j follows node d_parent[b * q_len
+ * + j], below j, or the context itself (-1), and stands at the position of what
+ * it follows and one, the context being the row's first d_lens[r] - n tokens.
+ * It sees the context, the nodes on its way up and itself, each if its position
+ * is within the window or below `sinks` (window 0: always).  q_len is at most
+ * 1024.  A parent out of range is recorded, and its node taken to follow the
+ * context; a row shorter than its tree is recorded, and its nodes see nothing.
+ * Errors as attn_window. */
+tmap_status attn_tree(const tmap_t* q, const tmap_t* k_pool, const tmap_t* v_pool, int32_t format,
+                      const page_table_t* pt, const int32_t* d_rows, const int32_t* d_count, const int32_t* d_parent,
+                      uint32_t window, uint32_t sinks, uint32_t len_hint, float scale, const tmap_t* o, float* d_lse,
+                      void* d_ws, uint64_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -107,8 +107,8 @@ def code_values(raw, fmt):
 def split_codes(pool, slots, fmt):
     """Codes [pages, heads, slots, dim] and scales [pages, heads, slots] of a
     pool of bytes [pages, heads, rows, dim]."""
-    p, h, _, _ = pool.shape
-    tail = np.ascontiguousarray(pool[:, :, slots:]).reshape(p, h, -1).view(np.uint16)[..., :slots]
+    p, h, rows, dim = pool.shape
+    tail = np.ascontiguousarray(pool[:, :, slots:]).reshape(p, h, (rows - slots) * dim).view(np.uint16)[..., :slots]
     return code_values(pool[:, :, :slots], fmt), to_f64(np.ascontiguousarray(tail), "bf16")
 
 
@@ -297,3 +297,62 @@ def attention_by_head(q, k_pool, v_pool, table, lens, slots, prefix_row, prefix_
                 score_size[b, j, h] = max(size[b, j], own)
                 seen[b, j, h] = prefix_len + n
     return o, lse, weight, score_size, seen
+
+
+# ---- attention over the cache: windows and trees -------------------------------------
+
+def in_window(t, p, window, sinks):
+    return window == 0 or t > p - window or t < sinks
+
+
+def causal_sees(length, n, window, sinks):
+    """Which of `length` tokens each of the last n sees, [n, length]."""
+    p = (length - n + np.arange(n))[:, None]
+    t = np.arange(length)[None]
+    sees = t <= p
+    return sees & ((t > p - window) | (t < sinks)) if window else sees
+
+
+def tree_sees(length, parents, window, sinks):
+    """The same for the last len(parents) tokens as the nodes of a tree."""
+    n = len(parents)
+    context = length - n
+    sees, place = np.zeros((n, length), bool), []
+    for j, up in enumerate(parents):
+        place.append(context if up < 0 else place[up] + 1)
+        for t in range(context):
+            sees[j, t] = in_window(t, place[j], window, sinks)
+        i = j
+        while i >= 0:
+            sees[j, context + i] = in_window(place[i], place[j], window, sinks)
+            i = parents[i]
+    return sees
+
+
+def attend(q, k, v, sees, scale):
+    """q [n, heads, dim], k and v [length, kv, dim], sees [n, length]: the result
+    [n, heads, dim], lse, and what errors scale with: the weights times the
+    values' magnitudes, the largest sum of a score's absolute terms, and how many
+    keys a query sees.  Keys that a query does not see are not looked at."""
+    n, heads, dim = q.shape
+    kv = k.shape[1]
+    group = heads // kv
+    out, weight = np.zeros((n, heads, dim)), np.zeros((n, heads, dim))
+    lse, size = np.full((n, heads), -np.inf), np.zeros((n, heads))
+    seen = sees.sum(1)
+    some = sees.any(0)
+    for h in range(heads):
+        kk, vv, m = k[some, h // group], v[some, h // group], sees[:, some]
+        with np.errstate(all="ignore"):
+            s = np.where(m, scale * (q[:, h] @ kk.T), -np.inf)
+            terms = np.where(m, abs(scale) * (np.abs(q[:, h]) @ np.abs(kk).T), 0.0)
+        if not kk.shape[0]:
+            continue
+        top = s.max(1, keepdims=True)
+        with np.errstate(all="ignore"):
+            e = np.where(m, np.exp(s - np.where(np.isneginf(top), 0.0, top)), 0.0)
+            total = e.sum(1, keepdims=True)
+            w = np.divide(e, total, out=np.zeros_like(e), where=total > 0)
+            lse[:, h] = np.where(total[:, 0] > 0, top[:, 0] + np.log(total[:, 0]), -np.inf)
+        out[:, h], weight[:, h], size[:, h] = w @ vv, w @ np.abs(vv), terms.max(1)
+    return out, lse, weight, size, np.broadcast_to(seen[:, None], (n, heads))

@@ -1,0 +1,317 @@
+"""The attention over the cache where it can go wrong: what is masked holds
+infinities and NaN, what the device's arrays say is out of range, graphs,
+streams, scales, far offsets."""
+import math
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import async_tensor_tile_amd as att  # noqa: E402
+from oracle import kvcache as ok  # noqa: E402
+
+from gpu_util import require_native, stream  # noqa: E402
+from test_gpu_attn_cache import Setup, parents_of  # noqa: E402
+from test_gpu_kvcache import f64, gen, ints, tensor_map  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+def setup_module(module):
+    require_native()
+
+
+def spoil(s, token, b, what, keys=True, values=True):
+    """A sequence's token holds `what`: in codes, its heads' scales do."""
+    page, slot = int(s.table[s.rows[b], token // s.slots]), token % s.slots
+    for on, p in ((keys, s.k), (values, s.v)):
+        if not on:
+            continue
+        x = p[page] if s.heads_first else p[page].transpose(0, 1)        # [heads, rows, dim]
+        if s.fmt == "same":
+            x[:, slot] = what
+            continue
+        bits = torch.tensor([what]).bfloat16().view(torch.uint8).cuda()
+        at = 2 * slot
+        x[:, s.slots + at // s.dim, at % s.dim:at % s.dim + 2] = bits
+
+
+def seen_by(s, b, parents, window, sinks):
+    n = s.q_len if s.counts is None else s.counts[b]
+    if parents is None:
+        return ok.causal_sees(s.seq_lens[b], n, window, sinks)
+    return ok.tree_sees(s.seq_lens[b], [int(p) for p in parents[b][:n]], window, sinks)
+
+
+SHAPES = [  # dtype, fmt, lens, counts, q_len, heads, kv, dim, slots, heads_first, window, sinks, kind
+    ("bf16", "same", [90, 300], None, 1, 8, 2, 128, 16, False, 50, 3, None),
+    ("f16", "same", [90, 300], None, 6, 8, 2, 64, 7, True, 50, 3, None),
+    ("bf16", "same", [200, 500], [150, 99], 150, 4, 2, 128, 16, False, 70, 5, None),
+    ("f16", "same", [200, 40], None, 20, 2, 1, 96, 16, False, 0, 0, "near"),
+    ("bf16", "same", [400, 130], None, 130, 2, 1, 192, 16, False, 33, 4, "near"),
+    ("f16", "int8", [90, 300], None, 3, 8, 2, 128, 16, False, 50, 3, None),
+    ("bf16", "e4m3", [200, 500], [150, 99], 150, 4, 2, 64, 48, True, 70, 5, None),
+    ("bf16", "int8", [300, 70], None, 70, 2, 2, 80, 16, False, 0, 0, "far"),
+]
+
+
+@pytest.mark.parametrize("what", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("case", range(len(SHAPES)))
+def test_what_is_not_seen_does_not_count(case, what):
+    """Slots behind the lengths, pages of no row and tokens that no query sees hold infinities and NaN; then so does a
+    token that some queries see: the others' results stay as they were, bit for bit."""
+    dtype, fmt, lens, counts, q_len, heads, kv, dim, slots, first, window, sinks, kind = SHAPES[case]
+    g = gen(600 + case)
+    s = Setup(g, dtype, fmt, lens, counts, q_len, heads, kv, dim, slots, first)
+    parents = None if kind is None else parents_of(g, len(lens), q_len, kind)
+    d_parents = None if parents is None else ints(parents)
+    clean = s.run(window, sinks, d_parents)
+    held = np.zeros((s.pages, slots), bool)
+    sees = [seen_by(s, b, parents, window, sinks) for b in range(len(lens))]
+    for b, r in enumerate(s.rows):
+        for t in range(lens[b]):
+            if sees[b][:, t].any():
+                held[int(s.table[r, t // slots]), t % slots] = True
+    for page, slot in np.argwhere(~held):
+        for p in (s.k, s.v):
+            x = p[page] if first else p[page].transpose(0, 1)
+            if fmt == "same":
+                x[:, slot] = what
+            else:
+                at = 2 * slot
+                x[:, slots + at // dim, at % dim:at % dim + 2] = torch.tensor([what]).bfloat16().view(torch.uint8).cuda()
+                x[:, slot] = 0x7F
+    got = s.run(window, sinks, d_parents)
+    assert all(np.array_equal(a, c) for a, c in zip(got, clean))
+    if q_len == 1:
+        return
+    # one that some queries see and others do not, of each sequence
+    some = [np.argwhere(m.any(0) & ~m.all(0))[:, 0] for m in sees]
+    tokens = [int(t[len(t) // 2]) for t in some]
+    for b, t in enumerate(tokens):
+        spoil(s, t, b, what, keys=False)
+    got = s.run(window, sinks, d_parents)
+    for b, t in enumerate(tokens):
+        n, see = sees[b].shape[0], sees[b][:, t]
+        assert np.array_equal(got[0][b, :n][~see], clean[0][b, :n][~see])
+        assert np.array_equal(got[1][b, :n], clean[1][b, :n])
+        assert not np.isfinite(got[0][b, :n][see]).any()
+        if fmt == "same" and not math.isnan(what):
+            assert (got[0][b, :n][see] == what).all()
+    for b, t in enumerate(tokens):
+        spoil(s, t, b, float("nan"), values=False)
+    got = s.run(window, sinks, d_parents)
+    for b, t in enumerate(tokens):
+        n, see = sees[b].shape[0], sees[b][:, t]
+        for a, c in zip(got, clean):
+            assert np.array_equal(a[b, :n][~see], c[b, :n][~see]) and np.isnan(a[b, :n][see]).all()
+
+
+@pytest.mark.parametrize("what", [float("nan"), float("inf")])
+@pytest.mark.parametrize("q_len", [5, 100])
+def test_single_odd_elements(q_len, what):
+    """One element of one value: the others of the row stay as they were."""
+    g = gen(620)
+    s = Setup(g, "bf16", "same", [300], None, q_len, 4, 2, 128, 16)
+    clean = s.run(64, 2)
+    see = ok.causal_sees(300, q_len, 64, 2)
+    t = int(np.argwhere(see.any(0) & ~see.all(0))[3, 0])
+    page, slot = int(s.table[s.rows[0], t // 16]), t % 16
+    s.v[page, slot, 1, 77] = what
+    got = s.run(64, 2)
+    at = np.zeros(clean[0].shape, bool)
+    at[0, see[:, t], 2:, 77] = True                                      # of the heads that share the second one
+    assert np.array_equal(got[0][~at], clean[0][~at]) and np.array_equal(got[1], clean[1])
+    assert (np.isnan(got[0][at]) if math.isnan(what) else got[0][at] == what).all()
+
+
+@pytest.mark.parametrize("scale", [-0.3, 0.0, 1e-30, 6.0])
+@pytest.mark.parametrize("q_len", [2, 90])
+def test_scales(q_len, scale):
+    s = Setup(gen(630), "f16", "same", [200, 90, 3], None, q_len, 4, 2, 64, 16)
+    s.check(40, 3, scale=scale)
+    s = Setup(gen(631), "bf16", "int8", [200, 90], None, q_len, 4, 2, 64, 16)
+    s.check(40, 3, parents_of(gen(1), 2, q_len, "near"), scale=scale)
+
+
+@pytest.mark.parametrize("window,sinks", [(2 ** 32 - 1, 5), (1 << 31, 2 ** 32 - 1), (5, 2 ** 32 - 1), (300, 1 << 31)])
+@pytest.mark.parametrize("q_len", [1, 70])
+def test_windows_and_sinks_beyond_everything(q_len, window, sinks):
+    s = Setup(gen(632), "f16", "same", [300, 69], None, q_len, 2, 1, 64, 16)
+    s.check(window, sinks)
+    if q_len < 69:
+        s.check(window, sinks, parents_of(gen(2), 2, q_len, "near"))
+
+
+def test_arguments_that_may_be_left_out():
+    """No rows: sequence b is row b.  No lse."""
+    s = Setup(gen(633), "f16", "same", [40, 9], None, 2, 2, 1, 64, 16)
+    with_rows = s.run(10, 2)
+    order = s.table[s.d_rows.long()].clone(), s.lens[s.d_rows.long()].clone()
+    s.table[:2], s.lens[:2] = order
+    s.o.fill_(0), s.lse.fill_(-3.0)
+    got = s.run(10, 2, rows=False, lse=False)
+    assert np.array_equal(got[0], with_rows[0]) and (got[1] == -3.0).all()
+
+
+def recorded():
+    with pytest.raises(att.TmapError) as e:
+        att.tile_device_status(stream())
+    assert e.value.name == "ERR_PAGE"
+
+
+@pytest.mark.parametrize("q_len", [2, 80])
+def test_out_of_range(q_len):
+    """Rows, counts, lengths and pages out of range are recorded; the other sequences' results stay as they were."""
+    s = Setup(gen(640), "bf16", "same", [90, 100, 200, 120, 130], [2] * 5, q_len, 4, 2, 64, 16)
+    clean = s.run(0, 0)
+    s.o.fill_(-3.0), s.lse.fill_(-3.0)
+    s.d_rows[0] = 7                                                      # there are seven rows
+    s.count[1] = q_len + 1
+    s.count[3] = -1
+    got = s.run(0, 0)
+    recorded()
+    assert (got[0][0, :2] == 0).all() and np.isneginf(got[1][0, :2]).all()
+    assert (got[0][[1, 3]] == -3.0).all() and (got[1][[1, 3]] == -3.0).all()
+    for a, c in zip(got, clean):
+        assert np.array_equal(a[[2, 4]], c[[2, 4]])
+    s.d_rows[0] = s.rows[0]
+    s.count.fill_(2)
+    s.lens[s.rows[1]] = 1 << 30
+    s.lens[s.rows[2]] = -5
+    s.table[s.rows[4], 2] = s.pages                                      # tokens 32 .. 47 are left out
+    got = s.run(0, 0)
+    recorded()
+    assert (got[0][2, :2] == 0).all() and np.isneginf(got[1][2, :2]).all()
+    for a, c in zip(got, clean):
+        assert np.array_equal(a[[0, 3]], c[[0, 3]])
+    assert np.isfinite(got[0][4, :2]).all() and not np.array_equal(got[0][4, :2], clean[0][4, :2])
+
+
+@pytest.mark.parametrize("n", [9, 100])
+def test_trees_out_of_range(n):
+    g = gen(641)
+    s = Setup(g, "f16", "same", [150, 200, 120], [n] * 3, n, 2, 1, 64, 16)
+    parents = parents_of(g, 3, n, "near")
+    good = parents.copy()
+    good[0, 3], good[1, 5] = -1, -1
+    want = s.run(0, 0, ints(good))
+    bad = parents.copy()
+    bad[0, 3], bad[1, 5] = 3, -2                                         # itself, and no node
+    got = s.run(0, 0, ints(bad))
+    recorded()
+    assert all(np.array_equal(a, b) for a, b in zip(got, want))
+    bad[0, 3], bad[1, 5] = 2 ** 31 - 1, -2 ** 31
+    got = s.run(0, 0, ints(bad))
+    recorded()
+    assert all(np.array_equal(a, b) for a, b in zip(got, want))
+    s.lens[s.rows[2]] = n - 1                                            # a row shorter than its tree
+    got = s.run(0, 0, ints(good))
+    recorded()
+    assert (got[0][2] == 0).all() and np.isneginf(got[1][2]).all()
+    assert np.array_equal(got[0][:2], want[0][:2])
+
+
+@pytest.mark.parametrize("fmt", ["same", "e4m3"])
+def test_offsets_beyond_32_bits(fmt):
+    """Pages that lie more than 4 GiB behind the pool's start."""
+    g = gen(650)
+    s = Setup(g, "bf16", fmt, [100, 60], None, 3, 2, 1, 128, 16)
+    clean = s.run(40, 4)
+    page_bytes = s.k[0].numel() * s.k.element_size()
+    pages = (9 << 29) // page_bytes + s.pages
+    for name in "kv":
+        old = getattr(s, name)
+        big = torch.empty((pages,) + tuple(old.shape[1:]), dtype=old.dtype, device="cuda")
+        big[pages - s.pages:] = old
+        setattr(s, name, big)
+    s.table.copy_(torch.where(s.table >= 0, s.table + (pages - s.pages), s.table))
+    s.pt = att.page_table(s.table, s.lens, None, pages, s.slots)
+    got = s.run(40, 4)
+    assert all(np.array_equal(a, b) for a, b in zip(got, clean))
+
+
+def test_graphs_that_share_a_workspace():
+    """Two captured calls of different shapes in one workspace, replayed in turn with other lengths, counts and parents."""
+    g = gen(660)
+    a = Setup(g, "f16", "same", [3000, 2000], [1, 1], 1, 4, 2, 64, 16)
+    b = Setup(g, "bf16", "int8", [1500, 700], [70, 30], 70, 4, 2, 64, 16)
+    parents = ints(parents_of(g, 2, 70, "near"))
+    calls = [(a, (1000, 4, None)), (b, (0, 0, parents))]
+    size = max(att.attn_cache_workspace(tensor_map(s.q, s.dtype), s.map(s.k), w, k, max(s.seq_lens))
+               for s, (w, k, _) in calls)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    graphs = []
+    for s, args in calls:
+        hint = max(s.seq_lens)
+        maps = (tensor_map(s.q, s.dtype), s.map(s.k), s.map(s.v))
+        mo, scale = tensor_map(s.o, s.dtype), 1 / math.sqrt(s.dim)
+
+        def call(st, s=s, args=args, maps=maps, mo=mo, hint=hint, scale=scale):
+            w, k, up = args
+            if up is None:
+                att.attn_window(*maps, s.fmt, s.pt, s.d_rows, s.count, w, k, hint, scale, mo, s.lse, ws, st)
+            else:
+                att.attn_tree(*maps, s.fmt, s.pt, s.d_rows, s.count, up, w, k, hint, scale, mo, s.lse, ws, st)
+
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            call(side.cuda_stream)
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=side):
+                call(torch.cuda.current_stream().cuda_stream)
+        torch.cuda.current_stream().wait_stream(side)
+        graphs.append((graph, call))
+    lens = [[3000, 2000, 1500, 700], [1234, 1, 800, 100], [2999, 1999, 71, 699], [17, 1500, 1499, 70]]
+    for n in lens:
+        a.lens[a.d_rows.long()] = ints(n[:2])
+        b.lens[b.d_rows.long()] = ints(n[2:])
+        parents.copy_(ints(parents_of(g, 2, 70, "far")))
+        for (s, _), (graph, call) in zip(calls, graphs):
+            s.q.copy_(torch.randn(s.q.shape, generator=g))
+            s.o.fill_(-3.0), s.lse.fill_(-3.0)
+            graph.replay()
+            got = s.o.clone(), s.lse.clone()
+            torch.cuda.synchronize()
+            s.o.fill_(-3.0), s.lse.fill_(-3.0)
+            ws.fill_(255)
+            call(stream())
+            assert torch.equal(got[0], s.o) and torch.equal(got[1], s.lse)
+
+
+def test_two_streams_at_once():
+    """Calls on two streams, each with its workspace, do not disturb each other."""
+    g = gen(661)
+    both = [Setup(g, "bf16", f, [4000, 3000, 100], None, n, 8, 2, 128, 16) for f, n in (("same", 1), ("e4m3", 80))]
+    want = [s.run(2000, 4) for s in both]
+    for s in both:
+        s.o.fill_(0), s.lse.fill_(0)
+    streams = [torch.cuda.Stream() for _ in both]
+    spaces = [torch.empty(att.attn_cache_workspace(tensor_map(s.q, s.dtype), s.map(s.k), 2000, 4, 4000),
+                          dtype=torch.uint8, device="cuda") for s in both]
+    maps = [(tensor_map(s.q, s.dtype), s.map(s.k), s.map(s.v), tensor_map(s.o, s.dtype)) for s in both]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, (q, k, v, o), st, ws in zip(both, maps, streams, spaces):
+            att.attn_window(q, k, v, s.fmt, s.pt, s.d_rows, s.count, 2000, 4, 4000, 1 / math.sqrt(128), o, s.lse, ws,
+                            st.cuda_stream)
+    torch.cuda.synchronize()
+    for s, w in zip(both, want):
+        assert np.array_equal(f64(s.o), w[0]) and np.array_equal(f64(s.lse), w[1])
+
+
+def test_results_do_not_depend_on_the_batch():
+    """A sequence's result is the same alone and beside others, run after run."""
+    g = gen(662)
+    s = Setup(g, "bf16", "same", [900, 50, 400], [100, 20, 64], 100, 4, 2, 128, 16)
+    first = s.run(300, 2, hint=300)
+    for _ in range(3):
+        again = s.run(300, 2, hint=300)
+        assert all(np.array_equal(a, b) for a, b in zip(first, again))
+    s.count[0] = 0
+    s.o.fill_(-3.0), s.lse.fill_(-3.0)
+    got = s.run(300, 2, hint=300)
+    assert (got[0][0] == -3.0).all()
+    assert all(np.array_equal(a[1:], b[1:]) for a, b in zip(got, first))
