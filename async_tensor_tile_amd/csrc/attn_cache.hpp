@@ -1,0 +1,749 @@
+// attn_cache.hpp -- the kernels of attention over the paged cache: causal with a sliding
+// window and a few first tokens that stay visible, or of a tree of drafted
+// tokens; pools of the queries' type or of 8-bit codes.
+//
+// The rows of a sequence's key / value head are its queries times the heads of
+// the group.  A workgroup takes a block of them over the keys that any of them
+// sees, as one list: the first tokens, those from the window's reach on, and
+// (a tree) the drafted ones, whose tiles stand in descending order so that a
+// row's way up its ancestors is walked once.  Few rows (a token a sequence): 32
+// in a workgroup, whose waves take tiles of 32 keys in turn.  Many (a prompt):
+// 128, 32 a wave, over shared tiles of 64 keys.  Where that leaves the GPU
+// unfilled the list is cut into parts, joined by a second launch.
+//
+// A tile that every row sees whole is not masked.  In the others each lane masks
+// the scores of its own row, and infinities and NaN among the values are added
+// outside of the product, to the rows that see them.
+//
+// Codes.  Keys go to the matrix cores as they are (a code is exact in 16 bits)
+// and the fp32 scores are multiplied by the keys' scales; a value is its code
+// times its scale, rounded to the queries' type, as a 16-bit cache would hold it.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "attn_wave.hpp"
+
+namespace att {
+
+constexpr uint32_t kMaxNodes = 1024;
+
+struct CacheArgs {
+    View q, o, k, v;                 // q, o {dim, heads, q_len, batch}; pools {dim, slots, heads, pages}
+    const int32_t* table;
+    const int32_t* lens;
+    const int32_t* rows;
+    const int32_t* count;
+    const int32_t* parent;           // a tree's; else causal
+    uint64_t pitch;
+    float* lse;
+    uint32_t* err;
+    f32x4* part_o;
+    float2* part_ml;
+    uint32_t table_rows, row_pages, pages, slots;
+    uint32_t window, sinks;          // window 0: none
+    uint32_t dim, q_len, group, kv, batch;
+    uint32_t rows_own;               // rows of a sequence's key / value head
+    uint32_t blocks32, blocks;       // of 32 rows, of a workgroup's
+    uint32_t parts;                  // along the keys
+    uint32_t tall;                   // 128 rows a workgroup
+    uint32_t inner;                  // (sequence, block, part) triples, a multiple of 8
+    uint32_t hint;
+    uint32_t direct;                 // one part: the result is written at once
+    float scale;                     // |scale| * log2(e), 1 if that is 0
+    uint32_t flip;                   // sign bits to turn in the queries (scale below 0)
+    uint32_t zero;                   // the scale is 0
+};
+
+typedef __attribute__((address_space(4))) const CacheArgs cargs;
+__device__ __forceinline__ cargs& kernel_args() { return *(cargs*)__builtin_amdgcn_kernarg_segment_ptr(); }
+// The arguments read again where they are used, not kept in scalar registers.
+__device__ __forceinline__ cargs& fresh() {
+    cargs* p = &kernel_args();
+    asm volatile("" : "+s"(p));
+    return *p;
+}
+
+// One sequence as the device's arrays say it is.
+struct Sequence {
+    uint32_t row;        // of the table
+    uint32_t len;        // tokens
+    uint32_t count;      // queries; 0 where there are none, or something is out of range
+};
+
+__device__ __forceinline__ Sequence sequence_of(cargs& a, uint32_t b, bool record) {
+    Sequence s = {a.rows ? (uint32_t)scalar_load(a.rows, b) : b, 0u, a.q_len};
+    bool bad = false;
+    if (a.count) {
+        const uint32_t n = (uint32_t)scalar_load(a.count, b);
+        bad = n > a.q_len;
+        s.count = bad ? 0u : n;
+        if (s.count == 0u) {
+            if (bad && record && threadIdx.x == 0) record_page_error(a.err);
+            return s;
+        }
+    }
+    if (s.row < a.table_rows) {
+        const int64_t room = (int64_t)a.slots * a.row_pages, len = scalar_load(a.lens, s.row);
+        s.len = (uint32_t)(len < 0 ? 0 : len > room ? room : len);
+        bad = s.len != len || (a.parent && s.len < s.count);
+    } else {
+        bad = true;
+    }
+    if (bad && record && threadIdx.x == 0) record_page_error(a.err);
+    return s;
+}
+
+// The keys of a block of rows as one list, i = 0 .. n - 1:
+//   [0, few)             tokens 0 ..
+//   [few, context)       tokens low .., for causal rows up to the block's last, else up to the drafted ones
+//   [drafted, n)         a tree's nodes 0 .. nodes - 1, tile by tile from the last tile to the first
+// Indices between and behind these are no keys.
+struct Span {
+    uint32_t few, low, context, drafted, nodes, tiles, n;
+    int32_t first;                   // token of the sequence's first query
+    uint32_t all_from, all_to;       // [0, few) and [all_from, all_to) are seen by every row
+};
+
+template <uint32_t TILE>
+__device__ __forceinline__ Span span_of(cargs& a, const Sequence& s, uint32_t j0, uint32_t j1) {
+    Span x = {};
+    x.first = (int32_t)s.len - (int32_t)s.count;
+    const bool tree = a.parent != nullptr;
+    if (tree && x.first < 0) return x;                                   // the nodes are not all there
+    const int32_t p0 = tree ? x.first : x.first + (int32_t)j0, p1 = x.first + (int32_t)j1;
+    if (!tree && p1 < 0) return x;
+    const uint32_t end = tree ? (uint32_t)x.first : (uint32_t)p1 + 1u;   // context tokens
+    const uint32_t sinks = a.sinks < end ? a.sinks : end;
+    const int64_t reach = (int64_t)p0 - a.window + 1;
+    uint32_t from = a.window && reach > 0 ? (uint32_t)reach : 0u;
+    from = from < end ? from : end;
+    if (from > sinks) {
+        x.few = sinks;
+        x.low = from;
+    }
+    x.context = x.few + (end - x.low);
+    x.n = x.drafted = x.context;
+    if (tree) {
+        x.nodes = j1 + 1u;
+        x.tiles = (x.nodes + TILE - 1u) / TILE;
+        x.drafted = (x.context + TILE - 1u) / TILE * TILE;
+        x.n = x.drafted + x.tiles * TILE;
+    }
+    const int64_t last_reach = (int64_t)p1 - a.window + 1 - x.low;
+    x.all_from = x.few + (a.window && last_reach > 0 ? (uint32_t)last_reach : 0u);
+    x.all_to = tree ? x.context : p0 < 0 ? 0u : x.few + ((uint32_t)p0 + 1u - x.low);
+    return x;
+}
+
+// Whether all rows see all of the keys [i, i + TILE).
+template <uint32_t TILE>
+__device__ __forceinline__ bool seen_by_all(const Span& x, uint32_t i) {
+    return i + TILE <= x.all_to && (x.all_from == x.few || i >= x.all_from || i + TILE <= x.few);
+}
+
+// The token of key i, -1 where there is none.
+template <uint32_t TILE>
+__device__ __forceinline__ int32_t token_of(const Span& x, uint32_t i, uint32_t end) {
+    if (i >= end) return -1;
+    if (i < x.context) return (int32_t)(i < x.few ? i : i - x.few + x.low);
+    if (i < x.drafted) return -1;
+    const uint32_t u = i - x.drafted, node = (x.tiles - 1u - u / TILE) * TILE + u % TILE;
+    return node < x.nodes ? x.first + (int32_t)node : -1;
+}
+
+template <uint32_t DP, int FMT>
+struct Shared {
+    uint8_t ring[Geo<DP>::ring_bytes];
+    uint64_t kaddr[2 * kSegment];     // address of each key's row in the pools
+    uint64_t vaddr[2 * kSegment];
+    uint64_t there[2 * kSegment / 64];
+    float kscale[FMT == KV_SAME ? 4 : 2 * kSegment];
+    float vscale[FMT == KV_SAME ? 4 : 2 * kSegment];
+    uint32_t odd[4];                  // whether a tile's values hold infinities or NaN
+    uint16_t parent[kMaxNodes];       // of each node, 0xFFFF: the context
+};
+
+// What a lane's row sees: keys below `few`, keys of [low, high), and of the
+// drafted nodes the way up from `node`.
+struct Sees {
+    uint32_t few, low, high;
+    int32_t node;                     // next on the way up, -1: none
+    uint32_t steps;                   // from the row's own node to it
+    int32_t at;                       // position of the row
+};
+
+__device__ __forceinline__ int32_t parent_of(const uint16_t* parent, int32_t node) {
+    const uint32_t p = parent[node];
+    return p == 0xFFFFu ? -1 : (int32_t)p;
+}
+
+__device__ __forceinline__ Sees sees_of(cargs& a, const Span& x, const uint16_t* parent, uint32_t j, bool valid) {
+    Sees s = {0u, 0u, 0u, -1, 0u, 0};
+    if (!valid || x.n == 0) return s;
+    s.at = x.first + (int32_t)j;
+    if (a.parent) {
+        s.node = (int32_t)j;
+        if (a.window) {                                                  // the depth says where the row stands
+            int32_t depth = -1;
+            for (int32_t up = (int32_t)j; up >= 0; up = parent_of(parent, up)) ++depth;
+            s.at = x.first + depth;
+        }
+    }
+    if (s.at < 0) return s;
+    const uint32_t end = (uint32_t)s.at + 1u, last = x.context - x.few + x.low;   // tokens, and those of the list
+    const int64_t reach = (int64_t)s.at - a.window + 1 - x.low;
+    s.few = x.few;
+    if (a.window && x.few == 0) s.few = a.sinks < end ? a.sinks : end;
+    s.few = s.few < x.context ? s.few : x.context;
+    s.low = x.few + (a.window && reach > 0 ? (uint32_t)reach : 0u);
+    s.high = x.few + ((end < last ? end : last) - x.low);
+    return s;
+}
+
+__device__ __forceinline__ uint64_t bits_below(uint32_t x, uint32_t i) {
+    return x <= i ? 0ull : x - i >= 64u ? ~0ull : (1ull << (x - i)) - 1ull;
+}
+
+// A bit for each of the keys i .. i + TILE - 1 that the lane's row sees.
+template <uint32_t TILE>
+__device__ __forceinline__ uint64_t seen_bits(cargs& a, const Span& x, Sees& s, const uint16_t* parent, uint32_t i) {
+    if (i < x.context || x.tiles == 0)
+        return (bits_below(s.high, i) & ~bits_below(s.low, i)) | bits_below(s.few, i);
+    if (i >= x.n) return 0;
+    const int32_t n0 = (int32_t)((x.tiles - 1u - (i - x.drafted) / TILE) * TILE);
+    uint64_t bits = 0;
+    while (s.node >= n0) {
+        const int32_t in = s.node - n0;
+        if (in < (int32_t)TILE &&
+            (!a.window || s.steps < a.window || s.at - (int64_t)s.steps < (int64_t)a.sinks))
+            bits |= 1ull << in;
+        s.node = parent_of(parent, s.node);
+        ++s.steps;
+    }
+    return bits;
+}
+
+// Where the keys of the list lie, thread after thread a key: its page first.
+template <uint32_t TILE>
+__device__ __forceinline__ int32_t page_of_key(cargs& a, const Span& x, uint32_t row, uint32_t i, uint32_t end) {
+    const int32_t t = token_of<TILE>(x, i, end);
+    if (t < 0) return -1;
+    return *(const ATT_GLOBAL int32_t*)(gptr(a.table) + ((uint64_t)row * a.pitch + (uint32_t)t / a.slots) * 4u);
+}
+
+// Then its addresses, and where its scales lie.
+struct Scales {
+    uint64_t k, v;                    // 0: no such key
+};
+template <uint32_t TILE, uint32_t DP, int FMT>
+__device__ __forceinline__ Scales place_key(cargs& a, const Span& x, uint32_t head, uint32_t i, uint32_t end,
+                                            int32_t page, Shared<DP, FMT>& sh, uint32_t at) {
+    const int32_t t = token_of<TILE>(x, i, end);
+    const bool ok = t >= 0 && (uint32_t)page < a.pages;
+    if (t >= 0 && !ok) record_page_error(a.err);
+    const uint32_t slot = (uint32_t)t % a.slots;
+    const uint64_t kh = a.k.base + (uint64_t)(page * a.k.stride[3] + head * a.k.stride[2]);
+    const uint64_t vh = a.v.base + (uint64_t)(page * a.v.stride[3] + head * a.v.stride[2]);
+    sh.kaddr[at] = ok ? kh + (uint64_t)(slot * a.k.stride[1]) : zero_row();
+    sh.vaddr[at] = ok ? vh + (uint64_t)(slot * a.v.stride[1]) : zero_row();
+    const uint64_t mask = __ballot(ok);
+    if (at % 64u == 0) sh.there[at / 64u] = mask;
+    Scales s = {0, 0};
+    if (FMT != KV_SAME && ok) {
+        s.k = kh + (uint64_t)scale_offset(slot, a.slots, a.dim, a.k.stride[1]);
+        s.v = vh + (uint64_t)scale_offset(slot, a.slots, a.dim, a.v.stride[1]);
+    }
+    return s;
+}
+
+__device__ __forceinline__ uint32_t scale_bits(uint64_t at) {
+    return at ? (uint32_t)*(const ATT_GLOBAL uint16_t*)at << 16 : 0u;
+}
+
+// ---- codes ------------------------------------------------------------------------
+
+// 16 codes as elements: two chunks of 8.  SCALED: times a scale, rounded once.
+template <typename T, int FMT, bool SCALED>
+__device__ __forceinline__ void elements_of(u32x4 code, float scale, typename Vec<T>::v8 (&y)[2]) {
+#pragma unroll
+    for (uint32_t w = 0; w < 4; ++w) {
+        float f[4];
+        if (FMT == KV_E4M3) {
+            const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int32_t)code[w], false);
+            const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8((int32_t)code[w], true);
+            f[0] = lo[0], f[1] = lo[1], f[2] = hi[0], f[3] = hi[1];
+        } else {
+#pragma unroll
+            for (uint32_t i = 0; i < 4; ++i) f[i] = (float)(int8_t)(code[w] >> (8u * i));
+        }
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i) y[w / 2u][4u * (w % 2u) + i] = (T)(SCALED ? f[i] * scale : f[i]);
+    }
+}
+
+// A share of a tile of codes: chunks of 16, THREADS apart, from memory to
+// registers and, as elements, to the tile's image in LDS.
+template <typename T, uint32_t DP, int FMT, uint32_t ROWS, uint32_t THREADS, bool VALUES>
+struct CodeCopy {
+    static constexpr uint32_t cpr = DP / 16, N = (ROWS * cpr + THREADS - 1u) / THREADS;
+    static constexpr bool whole = ROWS * cpr % THREADS == 0;
+    u32x4 raw[N];
+    __device__ __forceinline__ void load(uint32_t thread, uint32_t dim, const uint64_t* addr) {
+#pragma unroll
+        for (uint32_t n = 0; n < N; ++n) {
+            const uint32_t i = n * THREADS + thread, row = i / cpr, c = i - row * cpr;
+            if (!whole && i >= ROWS * cpr) break;
+            raw[n] = c * 16u < dim ? *(const ATT_GLOBAL u32x4*)gptr(addr[row] + c * 16u) : (u32x4)(0u);
+        }
+    }
+    __device__ __forceinline__ void store(uint32_t thread, const float* scales, uint8_t* tile) const {
+#pragma unroll
+        for (uint32_t n = 0; n < N; ++n) {
+            const uint32_t i = n * THREADS + thread, row = i / cpr, c = i - row * cpr;
+            if (!whole && i >= ROWS * cpr) break;
+            typename Vec<T>::v8 y[2];
+            elements_of<T, FMT, VALUES>(raw[n], VALUES ? scales[row] : 1.0f, y);
+            const uint32_t key = VALUES ? Geo<DP>::key_v(row) : Geo<DP>::key_k(row);
+            uint8_t* at = tile + row * (DP * 2u);
+            *reinterpret_cast<typename Vec<T>::v8*>(at + ((2u * c) ^ key) * 16u) = y[0];
+            *reinterpret_cast<typename Vec<T>::v8*>(at + ((2u * c + 1u) ^ key) * 16u) = y[1];
+        }
+    }
+};
+
+// Scores times their keys' scales.
+template <uint32_t NB>
+__device__ __forceinline__ void scale_scores(f32x16 (&s)[NB], const float* scales) {
+    const uint32_t hh = lane_id() / 32u;
+#pragma unroll
+    for (uint32_t n = 0; n < NB; ++n)
+#pragma unroll
+        for (uint32_t g = 0; g < 4; ++g) {
+            const f32x4 k = *reinterpret_cast<const f32x4*>(scales + 32u * n + 8u * g + 4u * hh);
+#pragma unroll
+            for (uint32_t i = 0; i < 4; ++i) s[n][4u * g + i] *= k[i];
+        }
+}
+
+// ---- results ----------------------------------------------------------------------
+
+template <uint32_t DP>
+__device__ __forceinline__ f32x4* part_at(cargs& a, uint64_t block) {
+    return a.part_o + block * (DP / 8u * 64u);
+}
+__device__ __forceinline__ uint64_t part_index(cargs& a, uint32_t b, uint32_t head, uint32_t block32, uint32_t part) {
+    return (((uint64_t)b * a.kv + head) * a.blocks32 + block32) * a.parts + part;
+}
+
+// Elements d .. d + 3 of row r of a sequence's head.
+template <typename T>
+__device__ __forceinline__ void store_result(cargs& a, uint32_t b, uint32_t head, uint32_t r, uint32_t d, f32x4 x) {
+    const uint32_t j = r / a.group, g = r - j * a.group;
+    gbyte* p = gptr(a.o.base) + (int64_t)b * a.o.stride[3] + (int64_t)j * a.o.stride[2] +
+               (int64_t)(head * a.group + g) * a.o.stride[1];
+    typename Vec<T>::v4 y;
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i) y[i] = (T)x[i];
+    *(ATT_GLOBAL uint64_t*)(p + d * 2u) = __builtin_bit_cast(uint64_t, y);
+}
+
+__device__ __forceinline__ void store_lse(cargs& a, uint32_t b, uint32_t head, uint32_t r, float m, float l) {
+    const uint32_t j = r / a.group, g = r - j * a.group;
+    a.lse[((uint64_t)b * a.q_len + j) * ((uint64_t)a.kv * a.group) + head * a.group + g] =
+        l == 0.0f ? -INFINITY : m * 0.6931471805599453f + logf(l);
+}
+
+struct Job {
+    uint32_t b, head, block, part;
+    Sequence seq;
+};
+
+// ---- many rows ----------------------------------------------------------------------
+
+// Four waves of 32 rows over shared tiles of 64 keys.  Two stages: while a tile
+// is used the next is on its way; a barrier a tile.
+template <typename T, uint32_t DP, int FMT>
+__device__ __forceinline__ void tall_part(cargs& a, Shared<DP, FMT>& sh, const Job& job) {
+    const uint32_t tid = threadIdx.x, wave = uniform(tid / 64u), lane = lane_id();
+    const uint32_t rows = job.seq.count * a.group, first_row = job.block * kWgRows;
+    const uint32_t last_row = first_row + kWgRows < rows ? first_row + kWgRows - 1u : rows - 1u;
+    const Span x = span_of<kTile>(a, job.seq, first_row / a.group, last_row / a.group);
+    const uint32_t per = part_keys(x.n, a.parts, kTile);
+    const uint32_t k0 = part_begin(x.n, job.part, per), k1 = part_begin(x.n, job.part + 1u, per);
+    const uint32_t tiles = (k1 - k0 + kTile - 1u) / kTile;
+    const uint32_t r = first_row + wave * kRows + lane % 32u;
+    const bool valid = r < rows, busy = first_row + wave * kRows < rows;
+    constexpr uint32_t SEG = kSegment / kTile;                            // tiles of a segment
+    constexpr uint32_t NG = Geo<DP>::cpr / kWaves;                        // groups a wave copies of a tile's keys
+    constexpr bool CODES = FMT != KV_SAME;
+    Wave<T, DP> w;
+    w.load(a, job.head, job.b * a.rows_own + r, valid);
+    int32_t page = page_of_key<kTile>(a, x, job.seq.row, k0 + tid, k1);
+    Scales scales = place_key<kTile, DP, FMT>(a, x, job.head, k0 + tid, k1, page, sh, tid);
+    if (CODES) {
+        sh.kscale[tid] = __builtin_bit_cast(float, scale_bits(scales.k));
+        sh.vscale[tid] = __builtin_bit_cast(float, scale_bits(scales.v));
+        page = page_of_key<kTile>(a, x, job.seq.row, k0 + kSegment + tid, k1);
+    }
+    if (tid < 4u) sh.odd[tid] = 0u;
+    __syncthreads();
+    Sees sees = sees_of(a, x, sh.parent, r / a.group, valid);
+    // Stages of keys first, of values behind them.
+    auto keys = [&](uint32_t t) { return sh.ring + (t & 1u) * Geo<DP>::tile_bytes; };
+    auto vals = [&](uint32_t t) { return sh.ring + (2u + (t & 1u)) * Geo<DP>::tile_bytes; };
+    auto there = [&](uint32_t t) { return uniform64(sh.there[t % (2u * SEG)]); };
+    auto in = [&](uint32_t t) { return t % (2u * SEG) * kTile; };         // where a tile's keys are placed
+    const RowCopy<DP, kWaves, false> kcopy{wave, a.dim};
+    const RowCopy<DP, kWaves, true> vcopy{wave, a.dim};
+    CodeCopy<T, DP, FMT == KV_SAME ? KV_INT8 : FMT, kTile, kThreads, false> kcode;
+    CodeCopy<T, DP, FMT == KV_SAME ? KV_INT8 : FMT, kTile, kThreads, true> vcode;
+    // What is on its way has arrived, for every wave, and every wave is done
+    // with the stages that are filled next.
+    auto meet = [&] {
+        if (!CODES) wait_vmcnt<0>();
+        wait_lgkm0();
+        wg_barrier();
+    };
+    // Addresses of the next segment's keys: pages a step ahead, scales a step behind.
+    // Codes are asked for a tile earlier, so they are placed a step earlier.
+    constexpr uint32_t PLACE = CODES ? 0u : 1u, FETCH = CODES ? SEG - 1u : 0u, AHEAD = CODES ? 2u : 1u;
+    auto begin = [&](uint32_t t) {
+        meet();
+        if (t % SEG == PLACE) {
+            const uint32_t s = t / SEG + 1u, at = (s & 1u) * kSegment + tid;
+            scales = place_key<kTile, DP, FMT>(fresh(), x, job.head, k0 + s * kSegment + tid, k1, page, sh, at);
+        }
+        if (CODES && t % SEG == 1u) {
+            const uint32_t at = ((t / SEG + 1u) & 1u) * kSegment + tid;
+            sh.kscale[at] = __builtin_bit_cast(float, scale_bits(scales.k));
+            sh.vscale[at] = __builtin_bit_cast(float, scale_bits(scales.v));
+        }
+        if (t % SEG == FETCH)
+            page = page_of_key<kTile>(fresh(), x, job.seq.row, k0 + (t / SEG + AHEAD) * kSegment + tid, k1);
+        if (tid == 0) sh.odd[(t + 1u) % 3u] = 0u;
+    };
+    const uint32_t dim = a.dim;
+    if (CODES) {
+        kcode.load(tid, dim, sh.kaddr + in(0));
+        vcode.load(tid, dim, sh.vaddr + in(0));
+        kcode.store(tid, nullptr, keys(0));
+        vcode.store(tid, sh.vscale + in(0), vals(0));
+        kcode.load(tid, dim, sh.kaddr + in(1));
+        kcode.store(tid, nullptr, keys(1));
+        kcode.load(tid, dim, sh.kaddr + in(2));
+        vcode.load(tid, dim, sh.vaddr + in(1));
+    } else if (tiles) {
+        kcopy.template all<NG>(sh.kaddr + in(0), keys(0));
+        kcopy.template all<NG>(sh.kaddr + in(1), keys(1));
+        vcopy.template all<NG>(sh.vaddr + in(0), vals(0));
+    }
+    meet();
+    // Behind the last tile, keys that are not there are copied and multiplied:
+    // two tiles' work at most, and every tile is like the others.
+    auto fill = [&](uint32_t t) {
+        if (CODES) {
+            kcode.store(tid, nullptr, keys(t));
+            vcode.store(tid, sh.vscale + in(t + 1u), vals(t + 1u));
+            kcode.load(tid, dim, sh.kaddr + in(t + 3u));
+            vcode.load(tid, dim, sh.vaddr + in(t + 2u));
+        } else {
+            kcopy.template all<NG>(sh.kaddr + in(t + 2u), keys(t));
+            vcopy.template all<NG>(sh.vaddr + in(t + 1u), vals(t + 1u));
+        }
+    };
+    const float scale = a.scale;
+    f32x16 s[2][2];
+    float top = 0.0f;
+    uint64_t seen = ~0ull;                                                // of the tile whose scores are at hand, by the lane's row
+    // Tile t's scores are there; `known`: so is the largest of them as they are.
+    auto finish = [&](uint32_t t, f32x16 (&y)[2], bool known) {
+        if (CODES) scale_scores(y, sh.kscale + in(t));
+        uint64_t bits = there(t);
+        const bool all = seen_by_all<kTile>(x, k0 + t * kTile);
+        if (!all) bits &= seen_bits<kTile>(fresh(), x, sees, sh.parent, k0 + t * kTile);
+        seen = bits;
+        if (!all || bits != ~0ull) w.mask(y, bits);
+        if (CODES || !all || bits != ~0ull || !known) top = w.largest(scale, y);
+    };
+    // Infinities and NaN among the values of a tile that some rows do not see
+    // whole are added to the rows that see them, and are 0 for the product.
+    auto odd_values = [&](uint32_t t, const f32x16 (&p)[2]) {
+        uint8_t* const v = vals(t);
+        const bool odd = Wave<T, DP>::template odd_share<false>(v, wave, kWaves, kTile);
+        if (odd && lane == 0) sh.odd[t % 3u] = 1u;
+        wait_lgkm0();
+        wg_barrier();
+        if (uniform(sh.odd[t % 3u]) == 0u) return;
+        if (busy) w.template add_odd<2>(v, p, seen);
+        wait_lgkm0();
+        wg_barrier();
+        Wave<T, DP>::template odd_share<true>(v, wave, kWaves, kTile);
+        wait_lgkm0();
+        wg_barrier();
+    };
+    auto step = [&](uint32_t t, f32x16 (&y)[2], f32x16 (&next)[2]) {       // a tile that every row sees whole
+        begin(t);
+        fill(t);
+        if (!busy) return;
+        top = w.advance(scale, keys(t + 1u), vals(t), top, y, next);
+        finish(t + 1u, next, true);
+    };
+    if (busy) {
+        w.scores(keys(0), s[0]);
+        finish(0, s[0], false);
+    }
+    // Tiles of both kinds in loops of their own: in one loop their registers do not fit beside each other.
+    for (uint32_t t = 0; t < tiles;) {
+        for (; t < tiles && !seen_by_all<kTile>(x, k0 + t * kTile); ++t) {
+            begin(t);
+            fill(t);
+            if (busy) w.weights(scale, s[0]);
+            odd_values(t, s[0]);
+            if (!busy) continue;
+            typename Wave<T, DP>::Piece z[2][DP / 32];
+            w.read_values(vals(t), 0, z[0]);
+            w.values(vals(t), s[0], z);
+            w.scores(keys(t + 1u), s[0]);
+            finish(t + 1u, s[0], false);
+        }
+        uint32_t n = 0;
+        while (t + n < tiles && seen_by_all<kTile>(x, k0 + (t + n) * kTile)) ++n;
+        for (; n > 1u; n -= 2u, t += 2u) {
+            step(t, s[0], s[1]);
+            step(t + 1u, s[1], s[0]);
+        }
+        if (n) {
+            step(t++, s[0], s[1]);
+            s[0][0] = s[1][0];
+            s[0][1] = s[1][1];
+        }
+    }
+    wait_vmcnt<0>();                                                       // nothing may land in LDS of a later workgroup
+    if (!busy) return;
+    cargs& e = fresh();
+    const uint32_t hh = lane / 32u;
+    const float l = w.total();
+    if (e.direct) {
+        if (!valid) return;
+#pragma unroll
+        for (uint32_t i = 0; i < DP / 8u; ++i) {
+            const uint32_t b = i / 4u, g = i % 4u, d = 8u * i + 4u * hh;
+            const f32x4 y = {w.o[b][4u * g], w.o[b][4u * g + 1u], w.o[b][4u * g + 2u], w.o[b][4u * g + 3u]};
+            if (d < e.dim) store_result<T>(e, job.b, job.head, r, d, l == 0.0f ? (f32x4)(0.0f) : y / l);
+        }
+        if (lane < 32u && e.lse) store_lse(e, job.b, job.head, r, w.m, l);
+        return;
+    }
+    const uint64_t at = part_index(e, job.b, job.head, job.block * kWaves + wave, job.part);
+    f32x4* out = part_at<DP>(e, at);
+#pragma unroll
+    for (uint32_t b = 0; b < DP / 32u; ++b)
+#pragma unroll
+        for (uint32_t g = 0; g < 4; ++g)
+            out[(4u * b + g) * 64u + lane] =
+                f32x4{w.o[b][4u * g], w.o[b][4u * g + 1u], w.o[b][4u * g + 2u], w.o[b][4u * g + 3u]};
+    if (lane < 32u) e.part_ml[at * 32u + lane] = make_float2(w.m, l);
+}
+
+// ---- few rows -------------------------------------------------------------------------
+
+// 32 rows: the waves take tiles of 32 keys in turn, each in LDS of its own, so
+// that no barrier is needed: keys are fetched anew while the weights are worked
+// out, values while the next scores are.  At the end the waves' sums are joined
+// in LDS.
+template <typename T, uint32_t DP, int FMT>
+__device__ __forceinline__ void short_part(cargs& a, Shared<DP, FMT>& sh, const Job& job) {
+    const uint32_t tid = threadIdx.x, wave = uniform(tid / 64u), lane = lane_id(), n32 = lane % 32u;
+    const uint32_t rows = job.seq.count * a.group, first_row = job.block * kRows;
+    const uint32_t last_row = first_row + kRows < rows ? first_row + kRows - 1u : rows - 1u;
+    const Span x = span_of<kOwnTile>(a, job.seq, first_row / a.group, last_row / a.group);
+    const uint32_t per = part_keys(x.n, a.parts, kOwnTile);
+    const uint32_t k0 = part_begin(x.n, job.part, per), k1 = part_begin(x.n, job.part + 1u, per);
+    const uint32_t r = first_row + n32;
+    const bool valid = r < rows;
+    constexpr uint32_t NP = Geo<DP>::cpr / 2;                             // copies of a tile's keys
+    constexpr uint32_t SEG = 2 * kSegment;
+    constexpr bool CODES = FMT != KV_SAME;
+    int32_t page[SEG / kThreads];                                         // of the next segment's keys
+    auto pages = [&](uint32_t base) {
+        cargs& e = fresh();
+#pragma unroll
+        for (uint32_t i = 0; i < SEG / kThreads; ++i)
+            page[i] = page_of_key<kOwnTile>(e, x, job.seq.row, base + i * kThreads + tid, k1);
+    };
+    pages(k0);                                                            // on its way while the queries are
+    Wave<T, DP> w;
+    w.load(a, job.head, job.b * a.rows_own + r, valid);
+    if (a.parent) __syncthreads();                                        // the parents are there
+    Sees sees = sees_of(a, x, sh.parent, r / a.group, valid);
+    uint8_t* const keys = sh.ring + wave * 2u * Geo<DP>::own_bytes;
+    uint8_t* const vals = keys + Geo<DP>::own_bytes;
+    const float scale = a.scale;
+    const uint32_t dim = a.dim;
+    const RowCopy<DP, 1, false> kcopy{0, dim};
+    const RowCopy<DP, 1, true> vcopy{0, dim};
+    CodeCopy<T, DP, FMT == KV_SAME ? KV_INT8 : FMT, kOwnTile, 64, false> kcode;
+    CodeCopy<T, DP, FMT == KV_SAME ? KV_INT8 : FMT, kOwnTile, 64, true> vcode;
+    for (uint32_t base = k0; base < k1; base += SEG) {
+        if (base != k0) __syncthreads();                                  // the segment before is used up
+        Scales scales[SEG / kThreads];
+#pragma unroll
+        for (uint32_t i = 0; i < SEG / kThreads; ++i)
+            scales[i] = place_key<kOwnTile, DP, FMT>(a, x, job.head, base + i * kThreads + tid, k1, page[i], sh,
+                                                     i * kThreads + tid);
+        __syncthreads();
+        const uint32_t left = k1 - base, n = left < SEG ? left : SEG, tiles = (n + kOwnTile - 1u) / kOwnTile;
+        auto mask_of = [&](uint32_t t) { return (uint32_t)(uniform64(sh.there[t / 2u]) >> (32u * (t & 1u))); };
+        auto ask_k = [&](uint32_t t) {
+            if (CODES) kcode.load(lane, dim, sh.kaddr + t * kOwnTile);
+            else kcopy.template all<NP>(sh.kaddr + t * kOwnTile, keys);
+        };
+        auto ask_v = [&](uint32_t t) {
+            if (CODES) vcode.load(lane, dim, sh.vaddr + t * kOwnTile);
+            else vcopy.template all<NP>(sh.vaddr + t * kOwnTile, vals);
+        };
+        if (wave < tiles) {
+            ask_k(wave);
+            ask_v(wave);
+        }
+        if (CODES) {
+            float ks[SEG / kThreads], vs[SEG / kThreads];
+#pragma unroll
+            for (uint32_t i = 0; i < SEG / kThreads; ++i) {
+                ks[i] = __builtin_bit_cast(float, scale_bits(scales[i].k));
+                vs[i] = __builtin_bit_cast(float, scale_bits(scales[i].v));
+            }
+#pragma unroll
+            for (uint32_t i = 0; i < SEG / kThreads; ++i) {
+                sh.kscale[i * kThreads + tid] = ks[i];
+                sh.vscale[i * kThreads + tid] = vs[i];
+            }
+            __syncthreads();
+        }
+        pages(base + SEG);
+        for (uint32_t t = wave; t < tiles; t += kWaves) {
+            const uint32_t there = mask_of(t), next = t + kWaves, k = base + t * kOwnTile;
+            if (CODES) {
+                kcode.store(lane, nullptr, keys);
+                if (next < tiles) ask_k(next);
+                wait_lgkm0();
+            } else {
+                wait_vmcnt<NP>();
+            }
+            f32x16 s[1];
+            w.scores(keys, s);
+            wait_lgkm0();
+            if (!CODES && next < tiles) ask_k(next);
+            if (CODES) scale_scores(s, sh.kscale + t * kOwnTile);
+            const bool all = seen_by_all<kOwnTile>(x, k);
+            uint32_t bits = there;
+            if (!all) bits &= (uint32_t)seen_bits<kOwnTile>(fresh(), x, sees, sh.parent, k);
+            if (!all || there != ~0u) w.mask(s, bits);
+            w.weights(scale, s);
+            if (CODES) {
+                vcode.store(lane, sh.vscale + t * kOwnTile, vals);
+                if (next < tiles) ask_v(next);
+                wait_lgkm0();
+            } else if (next < tiles) {
+                wait_vmcnt<NP>();
+            } else {
+                wait_vmcnt<0>();
+            }
+            if (!all && Wave<T, DP>::template odd_share<false>(vals, 0, 1, kOwnTile)) {
+                w.template add_odd<1>(vals, s, bits);
+                wait_lgkm0();
+                Wave<T, DP>::template odd_share<true>(vals, 0, 1, kOwnTile);
+                wait_lgkm0();
+            }
+            typename Wave<T, DP>::Piece z[2][DP / 32];
+            w.read_values(vals, 0, z[0]);
+            w.values(vals, s, z);
+            wait_lgkm0();
+            if (!CODES && next < tiles) ask_v(next);
+        }
+    }
+    // join the waves
+    cargs& e = fresh();
+    constexpr uint32_t NF = DP / 8u;
+    __syncthreads();
+    float2* const ml = reinterpret_cast<float2*>(sh.kaddr);
+    f32x4* const sums = reinterpret_cast<f32x4*>(sh.ring);
+    const uint32_t tiles = (k1 - k0 + kOwnTile - 1u) / kOwnTile, working = tiles < kWaves ? tiles : kWaves;
+    const float total = w.total();
+    if (lane < 32u) ml[wave * 32u + lane] = make_float2(w.m, total);
+    __syncthreads();
+    float m = -INFINITY, l = 0.0f;
+    for (uint32_t i = 0; i < working; ++i) m = fmaxf(m, ml[i * 32u + n32].x);
+    const float at = m == -INFINITY ? 0.0f : m;
+    for (uint32_t i = 0; i < working; ++i) l += ml[i * 32u + n32].y * __builtin_amdgcn_exp2f(ml[i * 32u + n32].x - at);
+    if (wave < working) {
+        const float fade = __builtin_amdgcn_exp2f(w.m - at);
+#pragma unroll
+        for (uint32_t b = 0; b < DP / 32u; ++b)
+#pragma unroll
+            for (uint32_t g = 0; g < 4; ++g)
+                sums[(wave * NF + 4u * b + g) * 64u + lane] =
+                    f32x4{w.o[b][4u * g], w.o[b][4u * g + 1u], w.o[b][4u * g + 2u], w.o[b][4u * g + 3u]} * fade;
+    }
+    __syncthreads();
+    const uint64_t block = part_index(e, job.b, job.head, job.block, job.part);
+    f32x4* const out = part_at<DP>(e, block);
+    for (uint32_t f = wave; f < NF; f += kWaves) {
+        f32x4 y = (f32x4)(0.0f);
+        for (uint32_t i = 0; i < working; ++i) y += sums[(i * NF + f) * 64u + lane];
+        if (!valid) continue;
+        const uint32_t d = 8u * f + 4u * (lane / 32u);
+        if (!e.direct) out[f * 64u + lane] = y;
+        else if (d < e.dim) store_result<T>(e, job.b, job.head, r, d, l == 0.0f ? (f32x4)(0.0f) : y / l);
+    }
+    if (wave == 0 && valid && lane < 32u) {
+        if (!e.direct) e.part_ml[block * 32u + lane] = make_float2(m, l);
+        else if (e.lse) store_lse(e, job.b, job.head, r, m, l);
+    }
+}
+
+// TALL: 128 rows a workgroup, else 32.
+template <typename T, uint32_t DP, int FMT, bool TALL>
+__global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_attn_cache(const CacheArgs) {
+    cargs& a = kernel_args();
+    __shared__ __attribute__((aligned(1024))) Shared<DP, FMT> sh;
+    // Workgroups go to the 8 XCDs in turn.  The heads of one (sequence, block,
+    // part) meet in one XCD: where they lie side by side in a token's row, one
+    // head alone would keep few of the L2's channels busy.  A sequence's last
+    // blocks, which see the most, go first.
+    const uint32_t i8 = blockIdx.x % 8u, y = blockIdx.x / 8u;
+    Job job;
+    job.head = y % a.kv;
+    uint32_t item = y / a.kv * 8u + i8;
+    if (item >= a.inner) return;
+    job.part = item % a.parts;
+    item /= a.parts;
+    job.b = item % a.batch;
+    job.block = a.blocks - 1u - item / a.batch;
+    job.seq = sequence_of(a, job.b, job.head == 0 && job.part == 0 && job.block == 0);
+    const uint32_t rows = job.seq.count * a.group;
+    if (job.block * (TALL ? kWgRows : kRows) >= rows) return;
+    if (a.parent) {
+        for (uint32_t n = threadIdx.x; n < job.seq.count; n += kThreads) {
+            const int32_t p = a.parent[(uint64_t)job.b * a.q_len + n];
+            const bool ok = p >= -1 && p < (int32_t)n;
+            if (!ok) record_page_error(a.err);
+            sh.parent[n] = ok ? (uint16_t)p : (uint16_t)0xFFFFu;
+        }
+    }
+    if constexpr (TALL) tall_part<T, DP, FMT>(a, sh, job);
+    else short_part<T, DP, FMT>(a, sh, job);
+}
+
+// ---- launches (each type and format in a file of its own, so that they build side by side) ----
+
+static inline uint32_t padded_dim(uint32_t dim) {
+    return dim <= 64 ? 64 : dim <= 96 ? 96 : dim <= 128 ? 128 : dim <= 192 ? 192 : 256;
+}
+
+// The products' launch; defined where it is instantiated.
+template <typename T, int FMT>
+void launch_attn_cache(const CacheArgs& a, uint32_t groups, hipStream_t stream);
+
+}  // namespace att

@@ -1,0 +1,6 @@
+// kernel_attn_cache_f16_e4m3.hip -- attention over the cache: queries of f16, pools of e4m3 codes.
+#include "attn_cache_launch.hpp"
+
+namespace att {
+template void launch_attn_cache<_Float16, KV_E4M3>(const CacheArgs& a, uint32_t groups, hipStream_t stream);
+}
