@@ -16,8 +16,9 @@
 // outside of the product, to the rows that see them.
 //
 // Codes.  Keys go to the matrix cores as they are (a code is exact in 16 bits)
-// and the fp32 scores are multiplied by the keys' scales; a value is its code
-// times its scale, rounded to the queries' type, as a 16-bit cache would hold it.
+// and the fp32 scores are multiplied by the keys' scales.  So do values for bf16,
+// whose scales multiply the fp32 weights before their rounding; for f16 a value is
+// its code times its scale, rounded, as a 16-bit cache would hold it.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -266,16 +267,31 @@ __device__ __forceinline__ uint32_t scale_bits(uint64_t at) {
 // 16 codes as elements: two chunks of 8.  SCALED: times a scale, rounded once.
 template <typename T, int FMT, bool SCALED>
 __device__ __forceinline__ void elements_of(u32x4 code, float scale, typename Vec<T>::v8 (&y)[2]) {
+    constexpr bool F16 = std::is_same<T, _Float16>::value;
 #pragma unroll
     for (uint32_t w = 0; w < 4; ++w) {
+        uint32_t c = code[w];
+        asm("" : "+v"(c));                                               // a whole word, not four loads of a byte
+        if constexpr (FMT == KV_INT8 && F16 && !SCALED) {
+            // 1024 + 128 + c has its bits in place: c with its sign bit turned, below the exponent of 1024
+            const uint32_t u = c ^ 0x80808080u;
+#pragma unroll
+            for (uint32_t i = 0; i < 2; ++i) {
+                const uint32_t pair = __builtin_amdgcn_perm(0x64646464u, u, i ? 0x04030402u : 0x04010400u);
+                const f16x2_t f = __builtin_bit_cast(f16x2_t, pair) - (_Float16)1152.0f;
+                y[w / 2u][4u * (w % 2u) + 2u * i] = f[0];
+                y[w / 2u][4u * (w % 2u) + 2u * i + 1u] = f[1];
+            }
+            continue;
+        }
         float f[4];
         if (FMT == KV_E4M3) {
-            const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int32_t)code[w], false);
-            const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8((int32_t)code[w], true);
+            const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int32_t)c, false);
+            const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8((int32_t)c, true);
             f[0] = lo[0], f[1] = lo[1], f[2] = hi[0], f[3] = hi[1];
         } else {
 #pragma unroll
-            for (uint32_t i = 0; i < 4; ++i) f[i] = (float)(int8_t)(code[w] >> (8u * i));
+            for (uint32_t i = 0; i < 4; ++i) f[i] = (float)(int8_t)(c >> (8u * i));
         }
 #pragma unroll
         for (uint32_t i = 0; i < 4; ++i) y[w / 2u][4u * (w % 2u) + i] = (T)(SCALED ? f[i] * scale : f[i]);
@@ -297,13 +313,15 @@ struct CodeCopy {
             raw[n] = c * 16u < dim ? *(const ATT_GLOBAL u32x4*)gptr(addr[row] + c * 16u) : (u32x4)(0u);
         }
     }
+    // scales: of the rows, for values that take theirs here.
+    template <bool SCALED>
     __device__ __forceinline__ void store(uint32_t thread, const float* scales, uint8_t* tile) const {
 #pragma unroll
         for (uint32_t n = 0; n < N; ++n) {
             const uint32_t i = n * THREADS + thread, row = i / cpr, c = i - row * cpr;
             if (!whole && i >= ROWS * cpr) break;
             typename Vec<T>::v8 y[2];
-            elements_of<T, FMT, VALUES>(raw[n], VALUES ? scales[row] : 1.0f, y);
+            elements_of<T, FMT, SCALED>(raw[n], SCALED ? scales[row] : 1.0f, y);
             const uint32_t key = VALUES ? Geo<DP>::key_v(row) : Geo<DP>::key_k(row);
             uint8_t* at = tile + row * (DP * 2u);
             *reinterpret_cast<typename Vec<T>::v8*>(at + ((2u * c) ^ key) * 16u) = y[0];
@@ -311,6 +329,29 @@ struct CodeCopy {
         }
     }
 };
+
+// Where the values' scales go.  bf16 holds a weight times any of them: the codes
+// go to the product as they are.  f16 does not (a weight of 2^-10 times a scale of
+// 2^-17), so there a value is its code times its scale, rounded.
+template <typename T>
+constexpr bool kScaledWeights = std::is_same<T, __bf16>::value;
+
+// Weights times their values' scales; a key that the row does not see (a bit of
+// `sees` each) has no weight, whatever its scale.
+template <uint32_t NB>
+__device__ __forceinline__ void scale_weights(f32x16 (&p)[NB], const float* scales, uint64_t sees) {
+    const uint32_t hh = lane_id() / 32u;
+#pragma unroll
+    for (uint32_t n = 0; n < NB; ++n) {
+        const uint32_t bits = (uint32_t)(sees >> (32u * n)) >> (4u * hh);
+#pragma unroll
+        for (uint32_t g = 0; g < 4; ++g) {
+            const f32x4 k = *reinterpret_cast<const f32x4*>(scales + 32u * n + 8u * g + 4u * hh);
+#pragma unroll
+            for (uint32_t i = 0; i < 4; ++i) p[n][4u * g + i] = bits & (1u << (8u * g + i)) ? p[n][4u * g + i] * k[i] : 0.0f;
+        }
+    }
+}
 
 // Scores times their keys' scales.
 template <uint32_t NB>
@@ -376,7 +417,7 @@ __device__ __forceinline__ void tall_part(cargs& a, Shared<DP, FMT>& sh, const J
     const bool valid = r < rows, busy = first_row + wave * kRows < rows;
     constexpr uint32_t SEG = kSegment / kTile;                            // tiles of a segment
     constexpr uint32_t NG = Geo<DP>::cpr / kWaves;                        // groups a wave copies of a tile's keys
-    constexpr bool CODES = FMT != KV_SAME;
+    constexpr bool CODES = FMT != KV_SAME, WEIGHTS = CODES && kScaledWeights<T>;
     Wave<T, DP> w;
     w.load(a, job.head, job.b * a.rows_own + r, valid);
     int32_t page = page_of_key<kTile>(a, x, job.seq.row, k0 + tid, k1);
@@ -427,10 +468,10 @@ __device__ __forceinline__ void tall_part(cargs& a, Shared<DP, FMT>& sh, const J
     if (CODES) {
         kcode.load(tid, dim, sh.kaddr + in(0));
         vcode.load(tid, dim, sh.vaddr + in(0));
-        kcode.store(tid, nullptr, keys(0));
-        vcode.store(tid, sh.vscale + in(0), vals(0));
+        kcode.template store<false>(tid, nullptr, keys(0));
+        vcode.template store<!WEIGHTS>(tid, sh.vscale + in(0), vals(0));
         kcode.load(tid, dim, sh.kaddr + in(1));
-        kcode.store(tid, nullptr, keys(1));
+        kcode.template store<false>(tid, nullptr, keys(1));
         kcode.load(tid, dim, sh.kaddr + in(2));
         vcode.load(tid, dim, sh.vaddr + in(1));
     } else if (tiles) {
@@ -443,8 +484,8 @@ __device__ __forceinline__ void tall_part(cargs& a, Shared<DP, FMT>& sh, const J
     // two tiles' work at most, and every tile is like the others.
     auto fill = [&](uint32_t t) {
         if (CODES) {
-            kcode.store(tid, nullptr, keys(t));
-            vcode.store(tid, sh.vscale + in(t + 1u), vals(t + 1u));
+            kcode.template store<false>(tid, nullptr, keys(t));
+            vcode.template store<!WEIGHTS>(tid, sh.vscale + in(t + 1u), vals(t + 1u));
             kcode.load(tid, dim, sh.kaddr + in(t + 3u));
             vcode.load(tid, dim, sh.vaddr + in(t + 2u));
         } else {
@@ -458,13 +499,12 @@ __device__ __forceinline__ void tall_part(cargs& a, Shared<DP, FMT>& sh, const J
     uint64_t seen = ~0ull;                                                // of the tile whose scores are at hand, by the lane's row
     // Tile t's scores are there; `known`: so is the largest of them as they are.
     auto finish = [&](uint32_t t, f32x16 (&y)[2], bool known) {
-        if (CODES) scale_scores(y, sh.kscale + in(t));
         uint64_t bits = there(t);
         const bool all = seen_by_all<kTile>(x, k0 + t * kTile);
         if (!all) bits &= seen_bits<kTile>(fresh(), x, sees, sh.parent, k0 + t * kTile);
         seen = bits;
         if (!all || bits != ~0ull) w.mask(y, bits);
-        if (CODES || !all || bits != ~0ull || !known) top = w.largest(scale, y);
+        if (!all || bits != ~0ull || !known) top = w.largest(scale, y);
     };
     // Infinities and NaN among the values of a tile that some rows do not see
     // whole are added to the rows that see them, and are 0 for the product.
@@ -486,11 +526,13 @@ __device__ __forceinline__ void tall_part(cargs& a, Shared<DP, FMT>& sh, const J
         begin(t);
         fill(t);
         if (!busy) return;
-        top = w.advance(scale, keys(t + 1u), vals(t), top, y, next);
+        top = w.template advance<CODES, WEIGHTS>(scale, keys(t + 1u), vals(t), top, y, next, sh.kscale + in(t + 1u),
+                                                 sh.vscale + in(t));
         finish(t + 1u, next, true);
     };
     if (busy) {
         w.scores(keys(0), s[0]);
+        if (CODES) scale_scores(s[0], sh.kscale + in(0));
         finish(0, s[0], false);
     }
     // Tiles of both kinds in loops of their own: in one loop their registers do not fit beside each other.
@@ -499,12 +541,14 @@ __device__ __forceinline__ void tall_part(cargs& a, Shared<DP, FMT>& sh, const J
             begin(t);
             fill(t);
             if (busy) w.weights(scale, s[0]);
-            odd_values(t, s[0]);
+            if (WEIGHTS && busy) scale_weights(s[0], sh.vscale + in(t), seen);
+            if (!WEIGHTS || FMT != KV_INT8) odd_values(t, s[0]);           // an int8 code is a number
             if (!busy) continue;
             typename Wave<T, DP>::Piece z[2][DP / 32];
             w.read_values(vals(t), 0, z[0]);
             w.values(vals(t), s[0], z);
             w.scores(keys(t + 1u), s[0]);
+            if (CODES) scale_scores(s[0], sh.kscale + in(t + 1u));
             finish(t + 1u, s[0], false);
         }
         uint32_t n = 0;
@@ -564,7 +608,7 @@ __device__ __forceinline__ void short_part(cargs& a, Shared<DP, FMT>& sh, const 
     const bool valid = r < rows;
     constexpr uint32_t NP = Geo<DP>::cpr / 2;                             // copies of a tile's keys
     constexpr uint32_t SEG = 2 * kSegment;
-    constexpr bool CODES = FMT != KV_SAME;
+    constexpr bool CODES = FMT != KV_SAME, WEIGHTS = CODES && kScaledWeights<T>;
     int32_t page[SEG / kThreads];                                         // of the next segment's keys
     auto pages = [&](uint32_t base) {
         cargs& e = fresh();
@@ -625,7 +669,7 @@ __device__ __forceinline__ void short_part(cargs& a, Shared<DP, FMT>& sh, const 
         for (uint32_t t = wave; t < tiles; t += kWaves) {
             const uint32_t there = mask_of(t), next = t + kWaves, k = base + t * kOwnTile;
             if (CODES) {
-                kcode.store(lane, nullptr, keys);
+                kcode.template store<false>(lane, nullptr, keys);
                 if (next < tiles) ask_k(next);
                 wait_lgkm0();
             } else {
@@ -642,7 +686,8 @@ __device__ __forceinline__ void short_part(cargs& a, Shared<DP, FMT>& sh, const 
             if (!all || there != ~0u) w.mask(s, bits);
             w.weights(scale, s);
             if (CODES) {
-                vcode.store(lane, sh.vscale + t * kOwnTile, vals);
+                vcode.template store<!WEIGHTS>(lane, sh.vscale + t * kOwnTile, vals);
+                if (WEIGHTS) scale_weights(s, sh.vscale + t * kOwnTile, bits);
                 if (next < tiles) ask_v(next);
                 wait_lgkm0();
             } else if (next < tiles) {
@@ -650,7 +695,7 @@ __device__ __forceinline__ void short_part(cargs& a, Shared<DP, FMT>& sh, const 
             } else {
                 wait_vmcnt<0>();
             }
-            if (!all && Wave<T, DP>::template odd_share<false>(vals, 0, 1, kOwnTile)) {
+            if ((!WEIGHTS || FMT != KV_INT8) && !all && Wave<T, DP>::template odd_share<false>(vals, 0, 1, kOwnTile)) {
                 w.template add_odd<1>(vals, s, bits);
                 wait_lgkm0();
                 Wave<T, DP>::template odd_share<true>(vals, 0, 1, kOwnTile);
@@ -712,8 +757,17 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_attn_cache(cons
     // part) meet in one XCD: where they lie side by side in a token's row, one
     // head alone would keep few of the L2's channels busy.  A sequence's last
     // blocks, which see the most, go first.
-    const uint32_t i8 = blockIdx.x % 8u, y = blockIdx.x / 8u;
     Job job;
+    if constexpr (TALL) {
+        const uint32_t units = a.batch * a.kv, unit = blockIdx.x % units;
+        uint32_t item = blockIdx.x / units;
+        job.head = unit % a.kv;
+        job.b = unit / a.kv;
+        job.part = item % a.parts;
+        job.block = a.blocks - 1u - item / a.parts;
+        if (item >= a.blocks * a.parts) return;
+    } else {
+    const uint32_t i8 = blockIdx.x % 8u, y = blockIdx.x / 8u;
     job.head = y % a.kv;
     uint32_t item = y / a.kv * 8u + i8;
     if (item >= a.inner) return;
@@ -721,6 +775,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_attn_cache(cons
     item /= a.parts;
     job.b = item % a.batch;
     job.block = a.blocks - 1u - item / a.batch;
+    }
     job.seq = sequence_of(a, job.b, job.head == 0 && job.part == 0 && job.block == 0);
     const uint32_t rows = job.seq.count * a.group;
     if (job.block * (TALL ? kWgRows : kRows) >= rows) return;

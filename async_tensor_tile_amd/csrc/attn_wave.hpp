@@ -301,9 +301,13 @@ struct Wave {
     // sequence of matrix instructions with the reads of the ones to come and
     // the arithmetic of the weights spread evenly between them: the matrix
     // cores and the other units work at the same time within a wave.
-    // Returns the largest of the next scores.
+    // Returns the largest of the next scores.  KEYS, VALUES: the next scores are
+    // multiplied by scales of their keys, this tile's weights (but not their sum)
+    // by scales of theirs.
+    template <bool KEYS = false, bool VALUES = false>
     __device__ __forceinline__ float advance(float scale, const uint8_t* keys, const uint8_t* vals, float top,
-                                             f32x16 (&s)[2], f32x16 (&next)[2]) {
+                                             f32x16 (&s)[2], f32x16 (&next)[2], const float* key_scales = nullptr,
+                                             const float* value_scales = nullptr) {
         constexpr uint32_t NS = 2 * NK, NP = 4 * NO, AHEAD = 5;           // products of scores, of values
         const uint32_t lane = lane_id(), row = lane % 32u, key = Geo<DP>::key_k(row);
         const uint8_t* kat = keys + row * (DP * 2u);
@@ -329,9 +333,14 @@ struct Wave {
         float sum[2] = {0.0f, 0.0f};
         v8 w[4];
         float best = 0.0f;
+        f32x4 ks[2], vs[2];                                               // of 4 keys each, read 4 keys ahead
+        const float* const ksat = key_scales + 4u * (lane / 32u);
+        const float* const vsat = value_scales + 4u * (lane / 32u);
+        if (VALUES) vs[0] = *reinterpret_cast<const f32x4*>(vsat);
         static_for<(int)(NS + NP)>([&](auto slot) {
             constexpr uint32_t i = decltype(slot)::value;
             read(i + AHEAD);
+            if constexpr (KEYS && i == NS) ks[0] = *reinterpret_cast<const f32x4*>(ksat);
             const v8 y = x[i % (AHEAD + 1u)].v;
             if constexpr (i < NS) {
                 constexpr uint32_t k = i / 2u, n = i % 2u;
@@ -348,12 +357,19 @@ struct Wave {
                 const float p = __builtin_amdgcn_exp2f(fmaf(s[e / 16u][e % 16u], scale, -at));
                 sum[e % 2u] += p;
                 asm volatile("" : "+v"(sum[e % 2u]));                     // here, not behind the last product
-                w[e / 8u][e % 8u] = (T)p;
+                if constexpr (VALUES && e % 4u == 0 && e + 4u < 32u)
+                    vs[(e / 4u + 1u) & 1u] = *reinterpret_cast<const f32x4*>(vsat + 2u * (e + 4u));
+                w[e / 8u][e % 8u] = (T)(VALUES ? p * vs[e / 4u & 1u][e % 4u] : p);
             });
             // the next scores' largest, from the third product of values on
             constexpr uint32_t per = (32u + NP - 3u) / (NP - 2u), j0 = i < NS + 2u ? 32u : (i - NS - 2u) * per;
             static_for<(int)(j0 < 32u ? (32u - j0 < per ? 32u - j0 : per) : 0u)>([&](auto which) {
                 constexpr uint32_t j = j0 + decltype(which)::value;
+                if constexpr (KEYS) {
+                    if constexpr (j % 4u == 0 && j + 4u < 32u)
+                        ks[(j / 4u + 1u) & 1u] = *reinterpret_cast<const f32x4*>(ksat + 2u * (j + 4u));
+                    next[j / 16u][j % 16u] *= ks[j / 4u & 1u][j % 4u];
+                }
                 if constexpr (j == 0) best = next[0][0];
                 else best = fmaxf(best, next[j / 16u][j % 16u]);
             });

@@ -82,7 +82,7 @@ static uint64_t plan(CacheArgs* a, uint32_t hint, uint64_t* groups_out) {
     const uint64_t rows = (uint64_t)a->q_len * a->group;
     if (rows * a->batch > 0x7FFFFFFFull) return 0;
     a->rows_own = (uint32_t)rows;
-    a->tall = rows > 2 * kRows;
+    a->tall = rows > kRows;
     a->blocks = (uint32_t)ceil_div(rows, a->tall ? kWgRows : kRows);
     a->blocks32 = a->tall ? a->blocks * kWaves : a->blocks;
     // keys of a block of rows: those of the window, or all

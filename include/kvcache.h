@@ -250,8 +250,8 @@ uint64_t attn_cache_workspace(const tmap_t* q, const tmap_t* k_pool, uint32_t wi
  * (window 0: every t <= p).  o, lse, heads, types, scale and the rounding as
  * attn_shared_prefix; a query that sees nothing gets o = 0 and lse = -inf, and
  * what a query does not see does not reach it, whatever it holds.  The pools are
- * of the queries' type (KV_SAME) or hold codes; a key is c * s, and a value is
- * c * s rounded to the queries' type.  len_hint is the length that the work is
+ * of the queries' type (KV_SAME) or hold codes; a key is c * s, and so is a value
+ * (f16: rounded to the type).  len_hint is the length that the work is
  * split for (any value is right).  A count or row out of range is recorded: no
  * query is there, or none sees a token.  Errors as attn_shared_prefix, and
  * UNSUPPORTED for pools that are not of the format (more than 2^24 - 1
