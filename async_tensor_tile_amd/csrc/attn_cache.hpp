@@ -42,6 +42,7 @@ struct CacheArgs {
     f32x4* part_o;
     float2* part_ml;
     uint32_t table_rows, row_pages, pages, slots;
+    uint32_t slot_shift;             // slots = 1 << slot_shift; 32: not a power of two
     uint32_t window, sinks;          // window 0: none
     uint32_t dim, q_len, group, kv, batch;
     uint32_t rows_own;               // rows of a sequence's key / value head
@@ -154,7 +155,7 @@ __device__ __forceinline__ int32_t token_of(const Span& x, uint32_t i, uint32_t 
 }
 
 template <uint32_t DP, int FMT>
-struct Shared {
+struct Shared {                       // of many rows
     uint8_t ring[Geo<DP>::ring_bytes];
     uint64_t kaddr[2 * kSegment];     // address of each key's row in the pools
     uint64_t vaddr[2 * kSegment];
@@ -163,6 +164,17 @@ struct Shared {
     float vscale[FMT == KV_SAME ? 4 : 2 * kSegment];
     uint32_t odd[4];                  // whether a tile's values hold infinities or NaN
     uint16_t parent[kMaxNodes];       // of each node, 0xFFFF: the context
+};
+
+constexpr uint32_t kPages = 1024;     // pages of a row that are looked up in LDS
+
+template <uint32_t DP, int FMT>
+struct ShortShared {                  // of few rows
+    uint8_t ring[Geo<DP>::ring_bytes];
+    uint64_t addr[kWaves][2][2 * kOwnTile];   // of a wave's tiles: the keys' rows in the pools, the values'
+    float scale[kWaves][2][FMT == KV_SAME ? 4 : 2 * kOwnTile];
+    int32_t page[kPages];
+    uint16_t parent[kMaxNodes];
 };
 
 // What a lane's row sees: keys below `few`, keys of [low, high), and of the
@@ -225,12 +237,17 @@ __device__ __forceinline__ uint64_t seen_bits(cargs& a, const Span& x, Sees& s, 
     return bits;
 }
 
+// The page of a row that holds a token.
+__device__ __forceinline__ uint32_t column_of(cargs& a, uint32_t token) {
+    return a.slot_shift < 32u ? token >> a.slot_shift : token / a.slots;
+}
+
 // Where the keys of the list lie, thread after thread a key: its page first.
 template <uint32_t TILE>
 __device__ __forceinline__ int32_t page_of_key(cargs& a, const Span& x, uint32_t row, uint32_t i, uint32_t end) {
     const int32_t t = token_of<TILE>(x, i, end);
     if (t < 0) return -1;
-    return *(const ATT_GLOBAL int32_t*)(gptr(a.table) + ((uint64_t)row * a.pitch + (uint32_t)t / a.slots) * 4u);
+    return *(const ATT_GLOBAL int32_t*)(gptr(a.table) + ((uint64_t)row * a.pitch + column_of(a, (uint32_t)t)) * 4u);
 }
 
 // Then its addresses, and where its scales lie.
@@ -243,7 +260,7 @@ __device__ __forceinline__ Scales place_key(cargs& a, const Span& x, uint32_t he
     const int32_t t = token_of<TILE>(x, i, end);
     const bool ok = t >= 0 && (uint32_t)page < a.pages;
     if (t >= 0 && !ok) record_page_error(a.err);
-    const uint32_t slot = (uint32_t)t % a.slots;
+    const uint32_t slot = (uint32_t)t - column_of(a, (uint32_t)t) * a.slots;
     const uint64_t kh = a.k.base + (uint64_t)(page * a.k.stride[3] + head * a.k.stride[2]);
     const uint64_t vh = a.v.base + (uint64_t)(page * a.v.stride[3] + head * a.v.stride[2]);
     sh.kaddr[at] = ok ? kh + (uint64_t)(slot * a.k.stride[1]) : zero_row();
@@ -284,6 +301,22 @@ __device__ __forceinline__ void elements_of(u32x4 code, float scale, typename Ve
             }
             continue;
         }
+        if constexpr (FMT == KV_E4M3 && !SCALED) {                       // exact in both types
+#pragma unroll
+            for (uint32_t i = 0; i < 2; ++i) {
+                T* const z = reinterpret_cast<T*>(&y[w / 2u]) + 4u * (w % 2u) + 2u * i;
+                if constexpr (F16) {
+                    const auto f = i ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c, 1.0f, true)
+                                     : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c, 1.0f, false);
+                    z[0] = f[0], z[1] = f[1];
+                } else {
+                    const auto f = i ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.0f, true)
+                                     : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.0f, false);
+                    z[0] = f[0], z[1] = f[1];
+                }
+            }
+            continue;
+        }
         float f[4];
         if (FMT == KV_E4M3) {
             const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int32_t)c, false);
@@ -306,12 +339,17 @@ struct CodeCopy {
     static constexpr bool whole = ROWS * cpr % THREADS == 0;
     u32x4 raw[N];
     __device__ __forceinline__ void load(uint32_t thread, uint32_t dim, const uint64_t* addr) {
+        auto each = [&](auto full) {
 #pragma unroll
-        for (uint32_t n = 0; n < N; ++n) {
-            const uint32_t i = n * THREADS + thread, row = i / cpr, c = i - row * cpr;
-            if (!whole && i >= ROWS * cpr) break;
-            raw[n] = c * 16u < dim ? *(const ATT_GLOBAL u32x4*)gptr(addr[row] + c * 16u) : (u32x4)(0u);
-        }
+            for (uint32_t n = 0; n < N; ++n) {
+                const uint32_t i = n * THREADS + thread, row = i / cpr, c = i - row * cpr;
+                if (!whole && i >= ROWS * cpr) break;
+                if (decltype(full)::value || c * 16u < dim) raw[n] = *(const ATT_GLOBAL u32x4*)gptr(addr[row] + c * 16u);
+                else raw[n] = (u32x4)(0u);
+            }
+        };
+        if (dim == DP) each(std::true_type{});
+        else each(std::false_type{});
     }
     // scales: of the rows, for values that take theirs here.
     template <bool SCALED>
@@ -336,9 +374,9 @@ struct CodeCopy {
 template <typename T>
 constexpr bool kScaledWeights = std::is_same<T, __bf16>::value;
 
-// Weights times their values' scales; a key that the row does not see (a bit of
-// `sees` each) has no weight, whatever its scale.
-template <uint32_t NB>
+// Weights times their values' scales; a key that the row does not see (MASKED: a
+// bit of `sees` each) has no weight, whatever its scale.
+template <bool MASKED, uint32_t NB>
 __device__ __forceinline__ void scale_weights(f32x16 (&p)[NB], const float* scales, uint64_t sees) {
     const uint32_t hh = lane_id() / 32u;
 #pragma unroll
@@ -348,7 +386,8 @@ __device__ __forceinline__ void scale_weights(f32x16 (&p)[NB], const float* scal
         for (uint32_t g = 0; g < 4; ++g) {
             const f32x4 k = *reinterpret_cast<const f32x4*>(scales + 32u * n + 8u * g + 4u * hh);
 #pragma unroll
-            for (uint32_t i = 0; i < 4; ++i) p[n][4u * g + i] = bits & (1u << (8u * g + i)) ? p[n][4u * g + i] * k[i] : 0.0f;
+            for (uint32_t i = 0; i < 4; ++i)
+                p[n][4u * g + i] = !MASKED || bits & (1u << (8u * g + i)) ? p[n][4u * g + i] * k[i] : 0.0f;
         }
     }
 }
@@ -541,7 +580,7 @@ __device__ __forceinline__ void tall_part(cargs& a, Shared<DP, FMT>& sh, const J
             begin(t);
             fill(t);
             if (busy) w.weights(scale, s[0]);
-            if (WEIGHTS && busy) scale_weights(s[0], sh.vscale + in(t), seen);
+            if (WEIGHTS && busy) scale_weights<true>(s[0], sh.vscale + in(t), seen);
             if (!WEIGHTS || FMT != KV_INT8) odd_values(t, s[0]);           // an int8 code is a number
             if (!busy) continue;
             typename Wave<T, DP>::Piece z[2][DP / 32];
@@ -592,105 +631,146 @@ __device__ __forceinline__ void tall_part(cargs& a, Shared<DP, FMT>& sh, const J
 
 // ---- few rows -------------------------------------------------------------------------
 
-// 32 rows: the waves take tiles of 32 keys in turn, each in LDS of its own, so
-// that no barrier is needed: keys are fetched anew while the weights are worked
-// out, values while the next scores are.  At the end the waves' sums are joined
-// in LDS.
+// 32 rows: the waves take tiles of 32 keys in turn, each in LDS of its own and
+// without a barrier.  A lane works out where one row of a tile lies, a key's or a
+// value's, a tile ahead; the pages are looked up in LDS, since the wait for a load
+// would be one for the copies in flight too.  Keys are fetched anew while the
+// weights are worked out, values while the next scores are.  At the end the waves'
+// sums are joined in LDS.
 template <typename T, uint32_t DP, int FMT>
-__device__ __forceinline__ void short_part(cargs& a, Shared<DP, FMT>& sh, const Job& job) {
+__device__ __forceinline__ void short_part(cargs& a, ShortShared<DP, FMT>& sh, const Job& job) {
     const uint32_t tid = threadIdx.x, wave = uniform(tid / 64u), lane = lane_id(), n32 = lane % 32u;
     const uint32_t rows = job.seq.count * a.group, first_row = job.block * kRows;
     const uint32_t last_row = first_row + kRows < rows ? first_row + kRows - 1u : rows - 1u;
     const Span x = span_of<kOwnTile>(a, job.seq, first_row / a.group, last_row / a.group);
     const uint32_t per = part_keys(x.n, a.parts, kOwnTile);
     const uint32_t k0 = part_begin(x.n, job.part, per), k1 = part_begin(x.n, job.part + 1u, per);
+    const uint32_t tiles = (k1 - k0 + kOwnTile - 1u) / kOwnTile;
     const uint32_t r = first_row + n32;
     const bool valid = r < rows;
     constexpr uint32_t NP = Geo<DP>::cpr / 2;                             // copies of a tile's keys
-    constexpr uint32_t SEG = 2 * kSegment;
     constexpr bool CODES = FMT != KV_SAME, WEIGHTS = CODES && kScaledWeights<T>;
-    int32_t page[SEG / kThreads];                                         // of the next segment's keys
-    auto pages = [&](uint32_t base) {
+    // Pages of the list: those of the first tokens, then those from `low` on.
+    const uint32_t few_pages = x.few ? column_of(a, x.few - 1u) + 1u : 0u, low_page = column_of(a, x.low);
+    auto entry_of = [&](uint32_t column, bool few) { return few ? column : column - low_page + few_pages; };
+    auto load_pages = [&](uint32_t p0) {                                  // kPages of them from p0 on
         cargs& e = fresh();
+        const ATT_GLOBAL int32_t* const entries = (const ATT_GLOBAL int32_t*)gptr(e.table) + (uint64_t)job.seq.row * e.pitch;
+        const uint32_t last = x.n ? entry_of(column_of(e, job.seq.len - 1u), false) : 0u;
 #pragma unroll
-        for (uint32_t i = 0; i < SEG / kThreads; ++i)
-            page[i] = page_of_key<kOwnTile>(e, x, job.seq.row, base + i * kThreads + tid, k1);
+        for (uint32_t i = 0; i < kPages / kThreads; ++i) {
+            const uint32_t p = p0 + i * kThreads + tid;
+            if (x.n && p <= last) sh.page[i * kThreads + tid] = entries[p < few_pages ? p : p - few_pages + low_page];
+        }
     };
-    pages(k0);                                                            // on its way while the queries are
     Wave<T, DP> w;
+    auto first_page = [&](uint32_t i) {
+        const int32_t t = token_of<kOwnTile>(x, i < x.context ? i : x.n - kOwnTile, x.n);   // of the drafted ones the first node
+        return t < 0 ? 0u : entry_of(column_of(fresh(), (uint32_t)t), i < x.few);
+    };
+    uint32_t p0 = first_page(k0);
+    load_pages(p0);
     w.load(a, job.head, job.b * a.rows_own + r, valid);
-    if (a.parent) __syncthreads();                                        // the parents are there
+    __syncthreads();
     Sees sees = sees_of(a, x, sh.parent, r / a.group, valid);
     uint8_t* const keys = sh.ring + wave * 2u * Geo<DP>::own_bytes;
     uint8_t* const vals = keys + Geo<DP>::own_bytes;
     const float scale = a.scale;
-    const uint32_t dim = a.dim;
+    const uint32_t dim = a.dim, slots = a.slots;
+    const uint64_t base = lane < 32u ? a.k.base + (uint64_t)(job.head * a.k.stride[2]) : a.v.base + (uint64_t)(job.head * a.v.stride[2]);
+    const uint64_t page_bytes = lane < 32u ? a.k.stride[3] : a.v.stride[3], slot_bytes = lane < 32u ? a.k.stride[1] : a.v.stride[1];
+    // Tile t's addresses, and where its keys are there.
+    uint64_t scale_at = 0;
+    auto place = [&](uint32_t t) -> uint32_t {
+        cargs& e = fresh();
+        const uint32_t i = k0 + t * kOwnTile + n32;
+        const int32_t tok = token_of<kOwnTile>(x, i, k1);
+        const uint32_t col = column_of(e, (uint32_t)tok), slot = (uint32_t)tok - col * slots;
+        int32_t page = -1;
+        if (tok >= 0) {
+            const uint32_t p = entry_of(col, i < x.few) - p0;
+            page = sh.page[p < kPages ? p : 0u];
+            if (p >= kPages) {                                            // many small pages of drafted tokens
+                page = *(const ATT_GLOBAL int32_t*)(gptr(e.table) + ((uint64_t)job.seq.row * e.pitch + col) * 4u);
+                asm volatile("" : "+v"(page));                            // waited for here
+            }
+        }
+        const bool ok = (uint32_t)page < e.pages && tok >= 0;
+        if (tok >= 0 && !ok) record_page_error(e.err);
+        const uint64_t at = base + (uint64_t)(uint32_t)page * page_bytes;
+        sh.addr[wave][(t / kWaves) & 1u][lane] = ok ? at + (uint64_t)slot * slot_bytes : zero_row();
+        scale_at = CODES && ok ? at + (uint64_t)scale_offset(slot, slots, dim, (int64_t)slot_bytes) : 0u;
+        return (uint32_t)__ballot(ok);
+    };
     const RowCopy<DP, 1, false> kcopy{0, dim};
     const RowCopy<DP, 1, true> vcopy{0, dim};
     CodeCopy<T, DP, FMT == KV_SAME ? KV_INT8 : FMT, kOwnTile, 64, false> kcode;
     CodeCopy<T, DP, FMT == KV_SAME ? KV_INT8 : FMT, kOwnTile, 64, true> vcode;
-    for (uint32_t base = k0; base < k1; base += SEG) {
-        if (base != k0) __syncthreads();                                  // the segment before is used up
-        Scales scales[SEG / kThreads];
-#pragma unroll
-        for (uint32_t i = 0; i < SEG / kThreads; ++i)
-            scales[i] = place_key<kOwnTile, DP, FMT>(a, x, job.head, base + i * kThreads + tid, k1, page[i], sh,
-                                                     i * kThreads + tid);
-        __syncthreads();
-        const uint32_t left = k1 - base, n = left < SEG ? left : SEG, tiles = (n + kOwnTile - 1u) / kOwnTile;
-        auto mask_of = [&](uint32_t t) { return (uint32_t)(uniform64(sh.there[t / 2u]) >> (32u * (t & 1u))); };
-        auto ask_k = [&](uint32_t t) {
-            if (CODES) kcode.load(lane, dim, sh.kaddr + t * kOwnTile);
-            else kcopy.template all<NP>(sh.kaddr + t * kOwnTile, keys);
-        };
-        auto ask_v = [&](uint32_t t) {
-            if (CODES) vcode.load(lane, dim, sh.vaddr + t * kOwnTile);
-            else vcopy.template all<NP>(sh.vaddr + t * kOwnTile, vals);
-        };
-        if (wave < tiles) {
-            ask_k(wave);
-            ask_v(wave);
-        }
-        if (CODES) {
-            float ks[SEG / kThreads], vs[SEG / kThreads];
-#pragma unroll
-            for (uint32_t i = 0; i < SEG / kThreads; ++i) {
-                ks[i] = __builtin_bit_cast(float, scale_bits(scales[i].k));
-                vs[i] = __builtin_bit_cast(float, scale_bits(scales[i].v));
-            }
-#pragma unroll
-            for (uint32_t i = 0; i < SEG / kThreads; ++i) {
-                sh.kscale[i * kThreads + tid] = ks[i];
-                sh.vscale[i * kThreads + tid] = vs[i];
-            }
+    auto ask_k = [&](uint32_t t) {
+        const uint64_t* addr = sh.addr[wave][(t / kWaves) & 1u];
+        if (CODES) kcode.load(lane, dim, addr);
+        else kcopy.template all<NP>(addr, keys);
+    };
+    auto ask_v = [&](uint32_t t) {
+        const uint64_t* addr = sh.addr[wave][(t / kWaves) & 1u] + kOwnTile;
+        if (CODES) vcode.load(lane, dim, addr);
+        else vcopy.template all<NP>(addr, vals);
+    };
+    // Tiles in runs that one set of pages is enough for: n keys touch n / slots + 3
+    // at most (the first, the last, and a cut between the first tokens and the rest).
+    const uint64_t enough = (uint64_t)(kPages - 4u) * slots / kOwnTile;
+    const uint32_t run = (uint32_t)(enough < (1u << 26) ? enough : 1u << 26) / kWaves * kWaves;
+    for (uint32_t t0 = 0; t0 < tiles; t0 += run) {
+        if (t0) {
+            __syncthreads();                                              // the pages before are used
+            p0 = first_page(k0 + t0 * kOwnTile);
+            load_pages(p0);
             __syncthreads();
         }
-        pages(base + SEG);
-        for (uint32_t t = wave; t < tiles; t += kWaves) {
-            const uint32_t there = mask_of(t), next = t + kWaves, k = base + t * kOwnTile;
+        const uint32_t end = tiles - t0 < run ? tiles : t0 + run;
+        uint32_t there = 0;
+        uint32_t bits16 = 0;                                              // of the lane's scale
+        if (t0 + wave < end) {
+            there = place(t0 + wave);
+            if (CODES) bits16 = scale_bits(scale_at);
+            wait_lgkm0();
+            ask_k(t0 + wave);
+            ask_v(t0 + wave);
+        }
+        for (uint32_t t = t0 + wave; t < end; t += kWaves) {
+            const uint32_t next = t + kWaves, k = k0 + t * kOwnTile, now = there;
+            float* const scales = sh.scale[wave][(t / kWaves) & 1u];
             if (CODES) {
-                kcode.template store<false>(lane, nullptr, keys);
-                if (next < tiles) ask_k(next);
+                scales[lane] = __builtin_bit_cast(float, bits16);
                 wait_lgkm0();
-            } else {
+                kcode.template store<false>(lane, nullptr, keys);
+                vcode.template store<!WEIGHTS>(lane, scales + kOwnTile, vals);
+            }
+            if (next < end) {
+                there = place(next);
+                if (CODES) bits16 = scale_bits(scale_at);
+            }
+            wait_lgkm0();
+            if (!CODES) {
                 wait_vmcnt<NP>();
+            } else if (next < end) {                                      // both as early as can be: most bytes on their way
+                ask_k(next);
+                ask_v(next);
             }
             f32x16 s[1];
             w.scores(keys, s);
             wait_lgkm0();
-            if (!CODES && next < tiles) ask_k(next);
-            if (CODES) scale_scores(s, sh.kscale + t * kOwnTile);
+            if (!CODES && next < end) ask_k(next);
+            if (CODES) scale_scores(s, scales);
             const bool all = seen_by_all<kOwnTile>(x, k);
-            uint32_t bits = there;
+            uint32_t bits = now;
             if (!all) bits &= (uint32_t)seen_bits<kOwnTile>(fresh(), x, sees, sh.parent, k);
-            if (!all || there != ~0u) w.mask(s, bits);
+            if (!all || now != ~0u) w.mask(s, bits);
             w.weights(scale, s);
             if (CODES) {
-                vcode.template store<!WEIGHTS>(lane, sh.vscale + t * kOwnTile, vals);
-                if (WEIGHTS) scale_weights(s, sh.vscale + t * kOwnTile, bits);
-                if (next < tiles) ask_v(next);
-                wait_lgkm0();
-            } else if (next < tiles) {
+                if (WEIGHTS && all) scale_weights<false>(s, scales + kOwnTile, bits);
+                else if (WEIGHTS) scale_weights<true>(s, scales + kOwnTile, bits);
+            } else if (next < end) {
                 wait_vmcnt<NP>();
             } else {
                 wait_vmcnt<0>();
@@ -705,16 +785,16 @@ __device__ __forceinline__ void short_part(cargs& a, Shared<DP, FMT>& sh, const 
             w.read_values(vals, 0, z[0]);
             w.values(vals, s, z);
             wait_lgkm0();
-            if (!CODES && next < tiles) ask_v(next);
+            if (!CODES && next < end) ask_v(next);
         }
     }
     // join the waves
     cargs& e = fresh();
     constexpr uint32_t NF = DP / 8u;
     __syncthreads();
-    float2* const ml = reinterpret_cast<float2*>(sh.kaddr);
+    float2* const ml = reinterpret_cast<float2*>(sh.addr);
     f32x4* const sums = reinterpret_cast<f32x4*>(sh.ring);
-    const uint32_t tiles = (k1 - k0 + kOwnTile - 1u) / kOwnTile, working = tiles < kWaves ? tiles : kWaves;
+    const uint32_t working = tiles < kWaves ? tiles : kWaves;
     const float total = w.total();
     if (lane < 32u) ml[wave * 32u + lane] = make_float2(w.m, total);
     __syncthreads();
@@ -752,7 +832,7 @@ __device__ __forceinline__ void short_part(cargs& a, Shared<DP, FMT>& sh, const 
 template <typename T, uint32_t DP, int FMT, bool TALL>
 __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_attn_cache(const CacheArgs) {
     cargs& a = kernel_args();
-    __shared__ __attribute__((aligned(1024))) Shared<DP, FMT> sh;
+    __shared__ __attribute__((aligned(1024))) std::conditional_t<TALL, Shared<DP, FMT>, ShortShared<DP, FMT>> sh;
     // Workgroups go to the 8 XCDs in turn.  The heads of one (sequence, block,
     // part) meet in one XCD: where they lie side by side in a token's row, one
     // head alone would keep few of the L2's channels busy.  A sequence's last

@@ -168,6 +168,7 @@ static tmap_status attend(const tmap_t* q, const tmap_t* k_pool, const tmap_t* v
     a.row_pages = pt->row_pages;
     a.pages = pt->pages;
     a.slots = pt->slots;
+    a.slot_shift = (pt->slots & (pt->slots - 1u)) == 0 ? (uint32_t)__builtin_ctz(pt->slots) : 32u;
     // Scores are kept in powers of two.  A negative scale turns the queries
     // around and a scale of 0 makes them 0, so that the factor is above 0 and
     // masked scores stay at -inf.
