@@ -1,6 +1,12 @@
 // kernel_kv8.hip -- pools of 8-bit codes: their geometry, and tokens read back.
 //
-// A lane takes 16 codes of a head and its scale, and writes 16 values.
+// A lane takes 16 codes of a head and its scale, and writes 16 values, two such at
+// a time.  Bound by HBM, of whose rate gathered heads of 128 bytes and a line for
+// each page's scales reach 84 %: 65536 tokens of 2 x 8 x 128 e4m3 to bf16 (407 MB)
+// take 93 us, 4.4 TB/s.  Tokens of a workgroup and items in flight of a lane were
+// measured there: 8 and 4 97 us, 16 and 4 99, 4 and 4 93, 2 and 2 99; 8 codes a
+// lane, whose stores lie side by side, 115 (twice the address arithmetic); each XCD
+// a run of neighbouring tokens 98.
 #include <hip/hip_runtime.h>
 
 #include <cstring>
@@ -10,7 +16,7 @@
 namespace att {
 
 constexpr uint32_t kReadThreads = 256;
-constexpr uint32_t kReadTokens = 8;           // tokens of a workgroup
+constexpr uint32_t kReadTokens = 4;           // tokens of a workgroup
 
 struct ReadSeg {
     uint64_t src, dst;
@@ -26,8 +32,7 @@ struct ReadArgs {
     uint64_t pitch;
     uint32_t* err;
     uint32_t table_rows, row_pages, pages, slots;
-    uint32_t tokens, dim, heads, chunks;      // chunks: of 16 codes in a head
-    uint32_t magic_chunks, magic_heads;
+    uint32_t tokens, dim, heads, magic_heads;
     uint32_t e4m3;
 };
 
@@ -37,28 +42,33 @@ __device__ __forceinline__ uint32_t quotient(uint32_t n, uint32_t d, uint32_t ma
     return q * d > n ? q - 1u : q;
 }
 
-// 16 codes times their scale.
-__device__ __forceinline__ void values_of(u32x4 code, float scale, bool e4m3, float (&y)[16]) {
+// N codes, four a word, times their scale.
+template <uint32_t N>
+__device__ __forceinline__ void values_of(const uint32_t (&code)[N / 4], float scale, bool e4m3, float (&y)[N]) {
 #pragma unroll
-    for (uint32_t w = 0; w < 4; ++w) {
+    for (uint32_t w = 0; w < N / 4; ++w) {
+        uint32_t c = code[w];
+        asm("" : "+v"(c));                    // a whole word, not four loads of a byte
         if (e4m3) {
-            const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int32_t)code[w], false);
-            const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8((int32_t)code[w], true);
+            const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int32_t)c, false);
+            const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8((int32_t)c, true);
             y[4 * w] = lo[0] * scale;
             y[4 * w + 1] = lo[1] * scale;
             y[4 * w + 2] = hi[0] * scale;
             y[4 * w + 3] = hi[1] * scale;
         } else {
 #pragma unroll
-            for (uint32_t i = 0; i < 4; ++i) y[4 * w + i] = (float)(int8_t)(code[w] >> (8u * i)) * scale;
+            for (uint32_t i = 0; i < 4; ++i) y[4 * w + i] = (float)(int8_t)(c >> (8u * i)) * scale;
         }
     }
 }
 
 template <typename T>
 __global__ __launch_bounds__(kReadThreads) void k_kv8_read(const ReadArgs a) {
+    constexpr uint32_t N = 16;                // codes of an item
     __shared__ int2 where[kReadTokens];       // page (-1: none) and slot
-    const uint32_t tid = threadIdx.x, items = kReadTokens * 2u * a.heads * a.chunks;
+    const uint32_t tid = threadIdx.x, chunks = a.dim / N, step = kReadThreads / chunks;
+    const uint32_t x0 = tid / chunks, c = tid - x0 * chunks, items = kReadTokens * 2u * a.heads;
     const uint32_t blocks = (a.tokens - 1u) / kReadTokens + 1u;
     for (uint32_t block = blockIdx.x; block < blocks; block += gridDim.x) {
         const uint32_t t0 = block * kReadTokens;
@@ -78,35 +88,35 @@ __global__ __launch_bounds__(kReadThreads) void k_kv8_read(const ReadArgs a) {
             where[tid] = w;
         }
         __syncthreads();
-        constexpr uint32_t U = 4;             // loads in flight per lane
-        for (uint32_t i0 = tid; i0 < items; i0 += U * kReadThreads) {
-            u32x4 code[U];
+        constexpr uint32_t U = 2;             // loads in flight per lane
+        for (uint32_t i0 = x0; x0 < step && i0 < items; i0 += U * step) {
+            uint32_t code[U][N / 4];
             uint16_t scale[U];
             gbyte* dst[U];
 #pragma unroll
             for (uint32_t n = 0; n < U; ++n) {
-                const uint32_t i = i0 + n * kReadThreads;
+                const uint32_t i = i0 + n * step;
                 dst[n] = nullptr;
                 if (i >= items) continue;
-                const uint32_t x = quotient(i, a.chunks, a.magic_chunks), c = i - x * a.chunks;
-                const uint32_t y = quotient(x, a.heads, a.magic_heads), h = x - y * a.heads;
+                const uint32_t y = quotient(i, a.heads, a.magic_heads), h = i - y * a.heads;
                 const ReadSeg& g = a.seg[y & 1u];
                 const int2 w = where[y / 2u];
                 if (w.x < 0) continue;
                 const gbyte* p = gptr(g.src) + (int64_t)w.x * g.src_page + (int64_t)h * g.src_head;
-                code[n] = *(const ATT_GLOBAL u32x4*)(p + (int64_t)w.y * g.src_slot + c * 16u);
+                const u32x4 x = *(const ATT_GLOBAL u32x4*)(p + (int64_t)w.y * g.src_slot + c * N);
+#pragma unroll
+                for (uint32_t k = 0; k < 4; ++k) code[n][k] = x[k];
                 scale[n] = *(const ATT_GLOBAL uint16_t*)(p + scale_offset((uint32_t)w.y, a.slots, a.dim, g.src_slot));
-                dst[n] = gptr(g.dst) + (int64_t)(t0 + y / 2u) * g.dst_tok + (int64_t)h * g.dst_head +
-                         c * 16u * sizeof(T);
+                dst[n] = gptr(g.dst) + (int64_t)(t0 + y / 2u) * g.dst_tok + (int64_t)h * g.dst_head + c * N * sizeof(T);
             }
 #pragma unroll
             for (uint32_t n = 0; n < U; ++n) {
                 if (!dst[n]) continue;
-                float y[16];
-                values_of(code[n], __builtin_bit_cast(float, (uint32_t)scale[n] << 16), a.e4m3, y);
-                T z[16];
+                float y[N];
+                values_of<N>(code[n], __builtin_bit_cast(float, (uint32_t)scale[n] << 16), a.e4m3, y);
+                T z[N];
 #pragma unroll
-                for (uint32_t q = 0; q < 16; ++q) z[q] = (T)y[q];
+                for (uint32_t q = 0; q < N; ++q) z[q] = (T)y[q];
 #pragma unroll
                 for (uint32_t q = 0; q < sizeof(T); ++q) {
                     u32x4 v;
@@ -162,8 +172,6 @@ extern "C" tmap_status kv8_read(int32_t format, const tmap_t* k_pool, const tmap
     a.tokens = (uint32_t)vk.dim[2];
     a.dim = (uint32_t)vk.dim[0];
     a.heads = (uint32_t)vk.dim[1];
-    a.chunks = a.dim / 16u;
-    a.magic_chunks = magic_for(a.chunks);
     a.magic_heads = magic_for(a.heads);
     a.e4m3 = format == KV_E4M3;
     st = device_error_word(&a.err);
