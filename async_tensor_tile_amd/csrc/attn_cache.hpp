@@ -42,15 +42,13 @@ struct CacheArgs {
     f32x4* part_o;
     float2* part_ml;
     uint32_t table_rows, row_pages, pages, slots;
-    uint32_t slot_shift;             // slots = 1 << slot_shift; 32: not a power of two
     uint32_t window, sinks;          // window 0: none
     uint32_t dim, q_len, group, kv, batch;
-    uint32_t rows_own;               // rows of a sequence's key / value head
-    uint32_t blocks32, blocks;       // of 32 rows, of a workgroup's
+    uint32_t blocks32, blocks;       // of a sequence's key / value head: of 32 rows, of a workgroup's
     uint32_t parts;                  // along the keys
     uint32_t tall;                   // 128 rows a workgroup
-    uint32_t inner;                  // (sequence, block, part) triples, a multiple of 8
-    uint32_t hint;
+    uint32_t first_item;             // of (block, part) pairs, where a launch does not hold them all
+    double per_group, per_slots, per_parts;   // 1 / group, 1 / slots, 1 / parts
     uint32_t direct;                 // one part: the result is written at once
     float scale;                     // |scale| * log2(e), 1 if that is 0
     uint32_t flip;                   // sign bits to turn in the queries (scale below 0)
@@ -66,6 +64,12 @@ __device__ __forceinline__ cargs& fresh() {
     return *p;
 }
 
+// n / d for n, d below 2^31 and per_d = 1 / d: (n + 1/2) / d is at least 2^-32 away
+// from a whole number, and the product off by less than 2^-20 of that.
+__device__ __forceinline__ uint32_t quotient(uint32_t n, double per_d) { return (uint32_t)(((double)n + 0.5) * per_d); }
+// The page of a row that holds a token.
+__device__ __forceinline__ uint32_t column_of(cargs& a, uint32_t token) { return quotient(token, a.per_slots); }
+
 // One sequence as the device's arrays say it is.
 struct Sequence {
     uint32_t row;        // of the table
@@ -74,16 +78,12 @@ struct Sequence {
 };
 
 __device__ __forceinline__ Sequence sequence_of(cargs& a, uint32_t b, bool record) {
-    Sequence s = {a.rows ? (uint32_t)scalar_load(a.rows, b) : b, 0u, a.q_len};
-    bool bad = false;
-    if (a.count) {
-        const uint32_t n = (uint32_t)scalar_load(a.count, b);
-        bad = n > a.q_len;
-        s.count = bad ? 0u : n;
-        if (s.count == 0u) {
-            if (bad && record && threadIdx.x == 0) record_page_error(a.err);
-            return s;
-        }
+    const uint32_t asked = a.count ? (uint32_t)scalar_load(a.count, b) : a.q_len;
+    Sequence s = {a.rows ? (uint32_t)scalar_load(a.rows, b) : b, 0u, asked <= a.q_len ? asked : 0u};
+    bool bad = asked > a.q_len;
+    if (s.count == 0u) {
+        if (bad && record && threadIdx.x == 0) record_page_error(a.err);
+        return s;
     }
     if (s.row < a.table_rows) {
         const int64_t room = (int64_t)a.slots * a.row_pages, len = scalar_load(a.lens, s.row);
@@ -235,11 +235,6 @@ __device__ __forceinline__ uint64_t seen_bits(cargs& a, const Span& x, Sees& s, 
         ++s.steps;
     }
     return bits;
-}
-
-// The page of a row that holds a token.
-__device__ __forceinline__ uint32_t column_of(cargs& a, uint32_t token) {
-    return a.slot_shift < 32u ? token >> a.slot_shift : token / a.slots;
 }
 
 // Where the keys of the list lie, thread after thread a key: its page first.
@@ -416,28 +411,40 @@ __device__ __forceinline__ uint64_t part_index(cargs& a, uint32_t b, uint32_t he
     return (((uint64_t)b * a.kv + head) * a.blocks32 + block32) * a.parts + part;
 }
 
-// Elements d .. d + 3 of row r of a sequence's head.
-template <typename T>
-__device__ __forceinline__ void store_result(cargs& a, uint32_t b, uint32_t head, uint32_t r, uint32_t d, f32x4 x) {
-    const uint32_t j = r / a.group, g = r - j * a.group;
-    gbyte* p = gptr(a.o.base) + (int64_t)b * a.o.stride[3] + (int64_t)j * a.o.stride[2] +
-               (int64_t)(head * a.group + g) * a.o.stride[1];
-    typename Vec<T>::v4 y;
-#pragma unroll
-    for (uint32_t i = 0; i < 4; ++i) y[i] = (T)x[i];
-    *(ATT_GLOBAL uint64_t*)(p + d * 2u) = __builtin_bit_cast(uint64_t, y);
-}
-
-__device__ __forceinline__ void store_lse(cargs& a, uint32_t b, uint32_t head, uint32_t r, float m, float l) {
-    const uint32_t j = r / a.group, g = r - j * a.group;
-    a.lse[((uint64_t)b * a.q_len + j) * ((uint64_t)a.kv * a.group) + head * a.group + g] =
-        l == 0.0f ? -INFINITY : m * 0.6931471805599453f + logf(l);
-}
-
 struct Job {
     uint32_t b, head, block, part;
     Sequence seq;
 };
+
+// Row r of a sequence's head: query j, and where it and its results lie.
+struct Row {
+    uint32_t j;
+    bool valid;
+    const gbyte* q;
+    gbyte* o;
+    uint64_t lse;
+};
+
+__device__ __forceinline__ Row row_of(cargs& a, const Job& job, uint32_t r, uint32_t rows) {
+    const uint32_t j = quotient(r, a.per_group), g = r - j * a.group, h = job.head * a.group;
+    const gbyte* const q = gptr(a.q.base) + ((int64_t)job.b * a.q.stride[3] + (int64_t)h * a.q.stride[1]);
+    gbyte* const o = gptr(a.o.base) + ((int64_t)job.b * a.o.stride[3] + (int64_t)h * a.o.stride[1]);
+    return {j, r < rows, q + (j * a.q.stride[2] + g * a.q.stride[1]), o + (j * a.o.stride[2] + g * a.o.stride[1]),
+            ((uint64_t)job.b * a.q_len + j) * (a.kv * a.group) + h + g};
+}
+
+// Elements d .. d + 3 of a row.
+template <typename T>
+__device__ __forceinline__ void store_result(const Row& r, uint32_t d, f32x4 x) {
+    typename Vec<T>::v4 y;
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i) y[i] = (T)x[i];
+    *(ATT_GLOBAL uint64_t*)(r.o + d * 2u) = __builtin_bit_cast(uint64_t, y);
+}
+
+__device__ __forceinline__ void store_lse(cargs& a, const Row& r, float m, float l) {
+    a.lse[r.lse] = l == 0.0f ? -INFINITY : m * 0.6931471805599453f + logf(l);
+}
 
 // ---- many rows ----------------------------------------------------------------------
 
@@ -448,17 +455,18 @@ __device__ __forceinline__ void tall_part(cargs& a, Shared<DP, FMT>& sh, const J
     const uint32_t tid = threadIdx.x, wave = uniform(tid / 64u), lane = lane_id();
     const uint32_t rows = job.seq.count * a.group, first_row = job.block * kWgRows;
     const uint32_t last_row = first_row + kWgRows < rows ? first_row + kWgRows - 1u : rows - 1u;
-    const Span x = span_of<kTile>(a, job.seq, first_row / a.group, last_row / a.group);
+    const Span x = span_of<kTile>(a, job.seq, uniform(quotient(first_row, a.per_group)),
+                                  uniform(quotient(last_row, a.per_group)));
     const uint32_t per = part_keys(x.n, a.parts, kTile);
     const uint32_t k0 = part_begin(x.n, job.part, per), k1 = part_begin(x.n, job.part + 1u, per);
     const uint32_t tiles = (k1 - k0 + kTile - 1u) / kTile;
-    const uint32_t r = first_row + wave * kRows + lane % 32u;
-    const bool valid = r < rows, busy = first_row + wave * kRows < rows;
+    const Row row = row_of(a, job, first_row + wave * kRows + lane % 32u, rows);
+    const bool busy = first_row + wave * kRows < rows;
     constexpr uint32_t SEG = kSegment / kTile;                            // tiles of a segment
     constexpr uint32_t NG = Geo<DP>::cpr / kWaves;                        // groups a wave copies of a tile's keys
     constexpr bool CODES = FMT != KV_SAME, WEIGHTS = CODES && kScaledWeights<T>;
     Wave<T, DP> w;
-    w.load(a, job.head, job.b * a.rows_own + r, valid);
+    w.load_row(a, row.q, row.valid);
     int32_t page = page_of_key<kTile>(a, x, job.seq.row, k0 + tid, k1);
     Scales scales = place_key<kTile, DP, FMT>(a, x, job.head, k0 + tid, k1, page, sh, tid);
     if (CODES) {
@@ -468,7 +476,7 @@ __device__ __forceinline__ void tall_part(cargs& a, Shared<DP, FMT>& sh, const J
     }
     if (tid < 4u) sh.odd[tid] = 0u;
     __syncthreads();
-    Sees sees = sees_of(a, x, sh.parent, r / a.group, valid);
+    Sees sees = sees_of(a, x, sh.parent, row.j, row.valid);
     // Stages of keys first, of values behind them.
     auto keys = [&](uint32_t t) { return sh.ring + (t & 1u) * Geo<DP>::tile_bytes; };
     auto vals = [&](uint32_t t) { return sh.ring + (2u + (t & 1u)) * Geo<DP>::tile_bytes; };
@@ -608,14 +616,15 @@ __device__ __forceinline__ void tall_part(cargs& a, Shared<DP, FMT>& sh, const J
     const uint32_t hh = lane / 32u;
     const float l = w.total();
     if (e.direct) {
-        if (!valid) return;
+        if (!row.valid) return;
+        const Row out = row_of(e, job, first_row + wave * kRows + lane % 32u, rows);
 #pragma unroll
         for (uint32_t i = 0; i < DP / 8u; ++i) {
             const uint32_t b = i / 4u, g = i % 4u, d = 8u * i + 4u * hh;
             const f32x4 y = {w.o[b][4u * g], w.o[b][4u * g + 1u], w.o[b][4u * g + 2u], w.o[b][4u * g + 3u]};
-            if (d < e.dim) store_result<T>(e, job.b, job.head, r, d, l == 0.0f ? (f32x4)(0.0f) : y / l);
+            if (d < e.dim) store_result<T>(out, d, l == 0.0f ? (f32x4)(0.0f) : y / l);
         }
-        if (lane < 32u && e.lse) store_lse(e, job.b, job.head, r, w.m, l);
+        if (lane < 32u && e.lse) store_lse(e, out, w.m, l);
         return;
     }
     const uint64_t at = part_index(e, job.b, job.head, job.block * kWaves + wave, job.part);
@@ -640,14 +649,12 @@ __device__ __forceinline__ void tall_part(cargs& a, Shared<DP, FMT>& sh, const J
 template <typename T, uint32_t DP, int FMT>
 __device__ __forceinline__ void short_part(cargs& a, ShortShared<DP, FMT>& sh, const Job& job) {
     const uint32_t tid = threadIdx.x, wave = uniform(tid / 64u), lane = lane_id(), n32 = lane % 32u;
-    const uint32_t rows = job.seq.count * a.group, first_row = job.block * kRows;
-    const uint32_t last_row = first_row + kRows < rows ? first_row + kRows - 1u : rows - 1u;
-    const Span x = span_of<kOwnTile>(a, job.seq, first_row / a.group, last_row / a.group);
+    const uint32_t rows = job.seq.count * a.group;
+    const Span x = span_of<kOwnTile>(a, job.seq, 0u, job.seq.count - 1u);
     const uint32_t per = part_keys(x.n, a.parts, kOwnTile);
     const uint32_t k0 = part_begin(x.n, job.part, per), k1 = part_begin(x.n, job.part + 1u, per);
     const uint32_t tiles = (k1 - k0 + kOwnTile - 1u) / kOwnTile;
-    const uint32_t r = first_row + n32;
-    const bool valid = r < rows;
+    const Row row = row_of(a, job, n32, rows);
     constexpr uint32_t NP = Geo<DP>::cpr / 2;                             // copies of a tile's keys
     constexpr bool CODES = FMT != KV_SAME, WEIGHTS = CODES && kScaledWeights<T>;
     // Pages of the list: those of the first tokens, then those from `low` on.
@@ -664,15 +671,15 @@ __device__ __forceinline__ void short_part(cargs& a, ShortShared<DP, FMT>& sh, c
         }
     };
     Wave<T, DP> w;
+    w.load_row(a, row.q, row.valid);
     auto first_page = [&](uint32_t i) {
         const int32_t t = token_of<kOwnTile>(x, i < x.context ? i : x.n - kOwnTile, x.n);   // of the drafted ones the first node
         return t < 0 ? 0u : entry_of(column_of(fresh(), (uint32_t)t), i < x.few);
     };
     uint32_t p0 = first_page(k0);
     load_pages(p0);
-    w.load(a, job.head, job.b * a.rows_own + r, valid);
     __syncthreads();
-    Sees sees = sees_of(a, x, sh.parent, r / a.group, valid);
+    Sees sees = sees_of(a, x, sh.parent, row.j, row.valid);
     uint8_t* const keys = sh.ring + wave * 2u * Geo<DP>::own_bytes;
     uint8_t* const vals = keys + Geo<DP>::own_bytes;
     const float scale = a.scale;
@@ -817,14 +824,14 @@ __device__ __forceinline__ void short_part(cargs& a, ShortShared<DP, FMT>& sh, c
     for (uint32_t f = wave; f < NF; f += kWaves) {
         f32x4 y = (f32x4)(0.0f);
         for (uint32_t i = 0; i < working; ++i) y += sums[(i * NF + f) * 64u + lane];
-        if (!valid) continue;
+        if (!row.valid) continue;
         const uint32_t d = 8u * f + 4u * (lane / 32u);
         if (!e.direct) out[f * 64u + lane] = y;
-        else if (d < e.dim) store_result<T>(e, job.b, job.head, r, d, l == 0.0f ? (f32x4)(0.0f) : y / l);
+        else if (d < e.dim) store_result<T>(row, d, l == 0.0f ? (f32x4)(0.0f) : y / l);
     }
-    if (wave == 0 && valid && lane < 32u) {
+    if (wave == 0 && row.valid && lane < 32u) {
         if (!e.direct) e.part_ml[block * 32u + lane] = make_float2(m, l);
-        else if (e.lse) store_lse(e, job.b, job.head, r, m, l);
+        else if (e.lse) store_lse(e, row, m, l);
     }
 }
 
@@ -833,32 +840,31 @@ template <typename T, uint32_t DP, int FMT, bool TALL>
 __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_attn_cache(const CacheArgs) {
     cargs& a = kernel_args();
     __shared__ __attribute__((aligned(1024))) std::conditional_t<TALL, Shared<DP, FMT>, ShortShared<DP, FMT>> sh;
-    // Workgroups go to the 8 XCDs in turn.  The heads of one (sequence, block,
-    // part) meet in one XCD: where they lie side by side in a token's row, one
-    // head alone would keep few of the L2's channels busy.  A sequence's last
-    // blocks, which see the most, go first.
     Job job;
+    uint32_t item;
+    // Workgroups go to the 8 XCDs in turn, x fastest.
     if constexpr (TALL) {
-        const uint32_t units = a.batch * a.kv, unit = blockIdx.x % units;
-        uint32_t item = blockIdx.x / units;
-        job.head = unit % a.kv;
-        job.b = unit / a.kv;
-        job.part = item % a.parts;
-        job.block = a.blocks - 1u - item / a.parts;
-        if (item >= a.blocks * a.parts) return;
+        // A unit (sequence and head) keeps to few XCDs, to one where the heads are a
+        // multiple of 8: its blocks read the same keys (8192 queries of 16384 tokens,
+        // window 4096: 593 us, with a block's heads on one XCD 658).  A sequence's
+        // last blocks, which see the most, go first.
+        item = blockIdx.z + a.first_item;
+        job.head = blockIdx.x;
+        job.b = blockIdx.y;
     } else {
-    const uint32_t i8 = blockIdx.x % 8u, y = blockIdx.x / 8u;
-    job.head = y % a.kv;
-    uint32_t item = y / a.kv * 8u + i8;
-    if (item >= a.inner) return;
-    job.part = item % a.parts;
-    item /= a.parts;
-    job.b = item % a.batch;
-    job.block = a.blocks - 1u - item / a.batch;
+        // The heads of one (sequence, part) meet in one XCD: where they lie side by
+        // side in a token's row, one head alone would keep few of the L2's channels
+        // busy.
+        item = (blockIdx.z * gridDim.y + blockIdx.y) * 8u + blockIdx.x % 8u;
+        job.head = blockIdx.x / 8u;
+        if (item >= a.batch * a.parts) return;
     }
+    const uint32_t rest = a.parts == 1u ? item : uniform(quotient(item, a.per_parts));
+    job.part = item - rest * a.parts;
+    if constexpr (TALL) job.block = a.blocks - 1u - rest;
+    else job.b = rest, job.block = 0;
     job.seq = sequence_of(a, job.b, job.head == 0 && job.part == 0 && job.block == 0);
-    const uint32_t rows = job.seq.count * a.group;
-    if (job.block * (TALL ? kWgRows : kRows) >= rows) return;
+    if (job.block * (TALL ? kWgRows : kRows) >= job.seq.count * a.group) return;
     if (a.parent) {
         for (uint32_t n = threadIdx.x; n < job.seq.count; n += kThreads) {
             const int32_t p = a.parent[(uint64_t)job.b * a.q_len + n];
@@ -879,6 +885,6 @@ static inline uint32_t padded_dim(uint32_t dim) {
 
 // The products' launch; defined where it is instantiated.
 template <typename T, int FMT>
-void launch_attn_cache(const CacheArgs& a, uint32_t groups, hipStream_t stream);
+void launch_attn_cache(const CacheArgs& a, hipStream_t stream);
 
 }  // namespace att

@@ -7,19 +7,31 @@
 namespace att {
 
 template <typename T, int FMT, uint32_t DP>
-static void launch_dim(const CacheArgs& a, uint32_t groups, hipStream_t stream) {
-    if (a.tall) hipLaunchKernelGGL((k_attn_cache<T, DP, FMT, true>), dim3(groups), dim3(kThreads), 0, stream, a);
-    else hipLaunchKernelGGL((k_attn_cache<T, DP, FMT, false>), dim3(groups), dim3(kThreads), 0, stream, a);
+static void launch_dim(const CacheArgs& a, hipStream_t stream) {
+    constexpr uint32_t most = 65535;                                       // a grid's y and z
+    if (!a.tall) {
+        const uint32_t eights = (a.batch * a.parts + 7u) / 8u, y = eights < most ? eights : most;
+        hipLaunchKernelGGL((k_attn_cache<T, DP, FMT, false>), dim3(8u * a.kv, y, (eights + y - 1u) / y), dim3(kThreads), 0,
+                           stream, a);
+        return;
+    }
+    const uint32_t items = a.blocks * a.parts;
+    CacheArgs part = a;
+    for (; part.first_item < items; part.first_item += most) {
+        const uint32_t left = items - part.first_item;
+        hipLaunchKernelGGL((k_attn_cache<T, DP, FMT, true>), dim3(a.kv, a.batch, left < most ? left : most), dim3(kThreads),
+                           0, stream, part);
+    }
 }
 
 template <typename T, int FMT>
-void launch_attn_cache(const CacheArgs& a, uint32_t groups, hipStream_t stream) {
+void launch_attn_cache(const CacheArgs& a, hipStream_t stream) {
     switch (padded_dim(a.dim)) {
-    case 64: return launch_dim<T, FMT, 64>(a, groups, stream);
-    case 96: return launch_dim<T, FMT, 96>(a, groups, stream);
-    case 128: return launch_dim<T, FMT, 128>(a, groups, stream);
-    case 192: return launch_dim<T, FMT, 192>(a, groups, stream);
-    default: return launch_dim<T, FMT, 256>(a, groups, stream);
+    case 64: return launch_dim<T, FMT, 64>(a, stream);
+    case 96: return launch_dim<T, FMT, 96>(a, stream);
+    case 128: return launch_dim<T, FMT, 128>(a, stream);
+    case 192: return launch_dim<T, FMT, 192>(a, stream);
+    default: return launch_dim<T, FMT, 256>(a, stream);
     }
 }
 

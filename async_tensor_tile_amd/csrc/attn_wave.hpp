@@ -168,10 +168,15 @@ struct Wave {
     // The lane's query (row r of the head's rows; none past `rows`).
     template <class Args>
     __device__ __forceinline__ void load(const Args& a, uint32_t head, uint32_t r, bool valid) {
-        const uint32_t lane = lane_id();
         const uint32_t b = r / a.rows_own, in = r - b * a.rows_own, j = in / a.group, g = in - j * a.group;
-        const gbyte* p = gptr(a.q.base) + (int64_t)b * a.q.stride[3] + (int64_t)j * a.q.stride[2] +
-                         (int64_t)(head * a.group + g) * a.q.stride[1];
+        load_row(a, gptr(a.q.base) + (int64_t)b * a.q.stride[3] + (int64_t)j * a.q.stride[2] +
+                        (int64_t)(head * a.group + g) * a.q.stride[1], valid);
+    }
+
+    // The lane's query at p.
+    template <class Args>
+    __device__ __forceinline__ void load_row(const Args& a, const gbyte* p, bool valid) {
+        const uint32_t lane = lane_id();
 #pragma unroll
         for (uint32_t k = 0; k < NK; ++k) {
             const uint32_t d = k * 16u + (lane / 32u) * 8u;

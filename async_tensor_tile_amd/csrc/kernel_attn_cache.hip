@@ -19,13 +19,14 @@ __global__ __launch_bounds__(kThreads) void k_attn_cache_join(const CacheArgs) {
     const uint32_t block = blockIdx.x % a.blocks32, unit = blockIdx.x / a.blocks32, head = unit % a.kv, b = unit / a.kv;
     const uint32_t f = blockIdx.y * kWaves + threadIdx.x / 64u, d = 8u * f + 4u * hh;
     if (8u * f >= a.dim) return;
-    const uint32_t rows = sequence_of(a, b, false).count * a.group, r = block * kRows + n32;
+    const Job job = {b, head, 0u, 0u, sequence_of(a, b, false)};
+    const uint32_t rows = job.seq.count * a.group;
     if (block * kRows >= rows) return;
     const uint64_t first = part_index(a, b, head, block, 0);
-    const bool valid = r < rows;
+    const Row row = row_of(a, job, block * kRows + n32, rows);
     f32x4 acc = (f32x4)(0.0f);
     float m = -INFINITY, l = 0.0f;
-    if (valid) {
+    if (row.valid) {
         for (uint32_t i0 = 0; i0 < a.parts; i0 += U) {
             float2 ml[U];
             f32x4 x[U];
@@ -52,8 +53,8 @@ __global__ __launch_bounds__(kThreads) void k_attn_cache_join(const CacheArgs) {
                 acc += x[u] * w;
             }
         }
-        if (d < a.dim) store_result<T>(a, b, head, r, d, l == 0.0f ? (f32x4)(0.0f) : acc / l);
-        if (f == 0 && hh == 0 && a.lse) store_lse(a, b, head, r, m, l);
+        if (d < a.dim) store_result<T>(row, d, l == 0.0f ? (f32x4)(0.0f) : acc / l);
+        if (f == 0 && hh == 0 && a.lse) store_lse(a, row, m, l);
     }
 }
 
@@ -70,7 +71,7 @@ static uint64_t ceil_div(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
 // How the work is cut: fills the fields of `a` that follow from the shapes, the
 // window and the hint alone and returns the workspace's bytes, 0 if there are
 // more rows than 31 bits count or more workgroups than a launch holds.
-static uint64_t plan(CacheArgs* a, uint32_t hint, uint64_t* groups_out) {
+static uint64_t plan(CacheArgs* a, uint32_t hint) {
     constexpr uint64_t cus = 256;
     const uint32_t dp = padded_dim((uint32_t)a->q.dim[0]);
     const uint64_t room = dp <= 128 ? 2 * cus : cus;                       // workgroups that run at once
@@ -81,7 +82,7 @@ static uint64_t plan(CacheArgs* a, uint32_t hint, uint64_t* groups_out) {
     a->group = (uint32_t)a->q.dim[1] / a->kv;
     const uint64_t rows = (uint64_t)a->q_len * a->group;
     if (rows * a->batch > 0x7FFFFFFFull) return 0;
-    a->rows_own = (uint32_t)rows;
+    a->per_group = 1.0 / a->group;
     a->tall = rows > kRows;
     a->blocks = (uint32_t)ceil_div(rows, a->tall ? kWgRows : kRows);
     a->blocks32 = a->tall ? a->blocks * kWaves : a->blocks;
@@ -92,13 +93,11 @@ static uint64_t plan(CacheArgs* a, uint32_t hint, uint64_t* groups_out) {
     const uint64_t jobs = (uint64_t)a->batch * a->kv * a->blocks;
     const uint64_t most = keys <= 512 ? 1 : ceil_div(keys, 256), want = room / jobs;
     a->parts = (uint32_t)(want < 1 ? 1 : want < most ? want : most);
+    a->per_parts = 1.0 / a->parts;
     a->direct = a->parts == 1;
-    const uint64_t inner = ceil_div((uint64_t)a->batch * a->blocks * a->parts, 8) * 8, groups = inner * a->kv;
     constexpr uint64_t most_groups = max_groups(kThreads);                 // of the products' launch, of the join's
     const uint64_t blocks = (uint64_t)a->batch * a->kv * a->blocks32;
-    if (groups > most_groups || blocks > most_groups) return 0;
-    a->inner = (uint32_t)((uint64_t)a->batch * a->blocks * a->parts);
-    *groups_out = groups;
+    if (jobs * a->parts > most_groups || blocks > most_groups) return 0;
     const uint64_t parts = a->direct ? 0 : blocks * a->parts;
     a->part_ml = reinterpret_cast<float2*>(parts * dp * 32 * 4);           // behind the sums
     return parts * (dp * 32 * 4 + 32 * 8) + 16;
@@ -111,10 +110,10 @@ static void join(const CacheArgs& a, hipStream_t stream) {
 }
 
 template <typename T>
-static tmap_status launch(const CacheArgs& a, int32_t format, uint32_t groups, hipStream_t stream, const char* name) {
-    if (format == KV_SAME) launch_attn_cache<T, KV_SAME>(a, groups, stream);
-    else if (format == KV_INT8) launch_attn_cache<T, KV_INT8>(a, groups, stream);
-    else launch_attn_cache<T, KV_E4M3>(a, groups, stream);
+static tmap_status launch(const CacheArgs& a, int32_t format, hipStream_t stream, const char* name) {
+    if (format == KV_SAME) launch_attn_cache<T, KV_SAME>(a, stream);
+    else if (format == KV_INT8) launch_attn_cache<T, KV_INT8>(a, stream);
+    else launch_attn_cache<T, KV_E4M3>(a, stream);
     const tmap_status st = check_launch(name);
     if (st || a.direct) return st;
     switch (padded_dim(a.dim)) {
@@ -153,8 +152,7 @@ static tmap_status attend(const tmap_t* q, const tmap_t* k_pool, const tmap_t* v
     if (reinterpret_cast<uintptr_t>(d_ws) % 16 != 0) return TMAP_ERR_ALIGN;
     a.window = window;
     a.sinks = window ? sinks : 0;
-    uint64_t groups = 0;
-    const uint64_t need = plan(&a, len_hint, &groups);
+    const uint64_t need = plan(&a, len_hint);
     if (need == 0 || ws_bytes < need) return TMAP_ERR_UNSUPPORTED;
     a.part_o = static_cast<f32x4*>(d_ws);
     a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(d_ws) + reinterpret_cast<uintptr_t>(a.part_ml));
@@ -168,7 +166,7 @@ static tmap_status attend(const tmap_t* q, const tmap_t* k_pool, const tmap_t* v
     a.row_pages = pt->row_pages;
     a.pages = pt->pages;
     a.slots = pt->slots;
-    a.slot_shift = (pt->slots & (pt->slots - 1u)) == 0 ? (uint32_t)__builtin_ctz(pt->slots) : 32u;
+    a.per_slots = 1.0 / pt->slots;
     // Scores are kept in powers of two.  A negative scale turns the queries
     // around and a scale of 0 makes them 0, so that the factor is above 0 and
     // masked scores stay at -inf.
@@ -178,8 +176,8 @@ static tmap_status attend(const tmap_t* q, const tmap_t* k_pool, const tmap_t* v
     a.lse = d_lse;
     st = device_error_word(&a.err);
     if (st) return st;
-    if (tq == TMAP_F16) return launch<_Float16>(a, format, (uint32_t)groups, as_stream(stream), name);
-    return launch<__bf16>(a, format, (uint32_t)groups, as_stream(stream), name);
+    if (tq == TMAP_F16) return launch<_Float16>(a, format, as_stream(stream), name);
+    return launch<__bf16>(a, format, as_stream(stream), name);
 }
 
 }  // namespace att
@@ -194,8 +192,7 @@ extern "C" uint64_t attn_cache_workspace(const tmap_t* q, const tmap_t* k_pool, 
     if (view_of(q, 4, &a.q, &tq) || view_of(k_pool, 4, &a.k, &tk) || !shapes_fit(a.q, a.k)) return 0;
     a.window = window;
     a.sinks = window ? sinks : 0;
-    uint64_t groups;
-    return plan(&a, len_hint, &groups);
+    return plan(&a, len_hint);
 }
 
 extern "C" tmap_status attn_window(const tmap_t* q, const tmap_t* k_pool, const tmap_t* v_pool, int32_t format,

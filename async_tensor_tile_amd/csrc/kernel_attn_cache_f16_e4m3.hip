@@ -2,5 +2,5 @@
 #include "attn_cache_launch.hpp"
 
 namespace att {
-template void launch_attn_cache<_Float16, KV_E4M3>(const CacheArgs& a, uint32_t groups, hipStream_t stream);
+template void launch_attn_cache<_Float16, KV_E4M3>(const CacheArgs& a, hipStream_t stream);
 }
