@@ -482,8 +482,15 @@ __device__ __forceinline__ void tall_part(cargs& a, Shared<DP, FMT>& sh, const J
     auto vals = [&](uint32_t t) { return sh.ring + (2u + (t & 1u)) * Geo<DP>::tile_bytes; };
     auto there = [&](uint32_t t) { return uniform64(sh.there[t % (2u * SEG)]); };
     auto in = [&](uint32_t t) { return t % (2u * SEG) * kTile; };         // where a tile's keys are placed
-    const RowCopy<DP, kWaves, false> kcopy{wave, a.dim};
-    const RowCopy<DP, kWaves, true> vcopy{wave, a.dim};
+    const uint32_t dim = a.dim;
+    auto copy_k = [&](const uint64_t* addr, const uint8_t* to) {
+        if (dim == DP) RowCopy<DP, kWaves, false, true>{wave, DP}.template all<NG>(addr, to);
+        else RowCopy<DP, kWaves, false>{wave, dim}.template all<NG>(addr, to);
+    };
+    auto copy_v = [&](const uint64_t* addr, const uint8_t* to) {
+        if (dim == DP) RowCopy<DP, kWaves, true, true>{wave, DP}.template all<NG>(addr, to);
+        else RowCopy<DP, kWaves, true>{wave, dim}.template all<NG>(addr, to);
+    };
     CodeCopy<T, DP, FMT == KV_SAME ? KV_INT8 : FMT, kTile, kThreads, false> kcode;
     CodeCopy<T, DP, FMT == KV_SAME ? KV_INT8 : FMT, kTile, kThreads, true> vcode;
     // What is on its way has arrived, for every wave, and every wave is done
@@ -511,7 +518,6 @@ __device__ __forceinline__ void tall_part(cargs& a, Shared<DP, FMT>& sh, const J
             page = page_of_key<kTile>(fresh(), x, job.seq.row, k0 + (t / SEG + AHEAD) * kSegment + tid, k1);
         if (tid == 0) sh.odd[(t + 1u) % 3u] = 0u;
     };
-    const uint32_t dim = a.dim;
     if (CODES) {
         kcode.load(tid, dim, sh.kaddr + in(0));
         vcode.load(tid, dim, sh.vaddr + in(0));
@@ -522,9 +528,9 @@ __device__ __forceinline__ void tall_part(cargs& a, Shared<DP, FMT>& sh, const J
         kcode.load(tid, dim, sh.kaddr + in(2));
         vcode.load(tid, dim, sh.vaddr + in(1));
     } else if (tiles) {
-        kcopy.template all<NG>(sh.kaddr + in(0), keys(0));
-        kcopy.template all<NG>(sh.kaddr + in(1), keys(1));
-        vcopy.template all<NG>(sh.vaddr + in(0), vals(0));
+        copy_k(sh.kaddr + in(0), keys(0));
+        copy_k(sh.kaddr + in(1), keys(1));
+        copy_v(sh.vaddr + in(0), vals(0));
     }
     meet();
     // Behind the last tile, keys that are not there are copied and multiplied:
@@ -536,8 +542,8 @@ __device__ __forceinline__ void tall_part(cargs& a, Shared<DP, FMT>& sh, const J
             kcode.load(tid, dim, sh.kaddr + in(t + 3u));
             vcode.load(tid, dim, sh.vaddr + in(t + 2u));
         } else {
-            kcopy.template all<NG>(sh.kaddr + in(t + 2u), keys(t));
-            vcopy.template all<NG>(sh.vaddr + in(t + 1u), vals(t + 1u));
+            copy_k(sh.kaddr + in(t + 2u), keys(t));
+            copy_v(sh.vaddr + in(t + 1u), vals(t + 1u));
         }
     };
     const float scale = a.scale;
@@ -573,7 +579,7 @@ __device__ __forceinline__ void tall_part(cargs& a, Shared<DP, FMT>& sh, const J
         begin(t);
         fill(t);
         if (!busy) return;
-        top = w.template advance<CODES, WEIGHTS>(scale, keys(t + 1u), vals(t), top, y, next, sh.kscale + in(t + 1u),
+        top = w.template advance<CODES, WEIGHTS, true>(scale, keys(t + 1u), vals(t), top, y, next, sh.kscale + in(t + 1u),
                                                  sh.vscale + in(t));
         finish(t + 1u, next, true);
     };
@@ -709,19 +715,19 @@ __device__ __forceinline__ void short_part(cargs& a, ShortShared<DP, FMT>& sh, c
         scale_at = CODES && ok ? at + (uint64_t)scale_offset(slot, slots, dim, (int64_t)slot_bytes) : 0u;
         return (uint32_t)__ballot(ok);
     };
-    const RowCopy<DP, 1, false> kcopy{0, dim};
-    const RowCopy<DP, 1, true> vcopy{0, dim};
     CodeCopy<T, DP, FMT == KV_SAME ? KV_INT8 : FMT, kOwnTile, 64, false> kcode;
     CodeCopy<T, DP, FMT == KV_SAME ? KV_INT8 : FMT, kOwnTile, 64, true> vcode;
     auto ask_k = [&](uint32_t t) {
         const uint64_t* addr = sh.addr[wave][(t / kWaves) & 1u];
         if (CODES) kcode.load(lane, dim, addr);
-        else kcopy.template all<NP>(addr, keys);
+        else if (dim == DP) RowCopy<DP, 1, false, true>{0, DP}.template all<NP>(addr, keys);
+        else RowCopy<DP, 1, false>{0, dim}.template all<NP>(addr, keys);
     };
     auto ask_v = [&](uint32_t t) {
         const uint64_t* addr = sh.addr[wave][(t / kWaves) & 1u] + kOwnTile;
         if (CODES) vcode.load(lane, dim, addr);
-        else vcopy.template all<NP>(addr, vals);
+        else if (dim == DP) RowCopy<DP, 1, true, true>{0, DP}.template all<NP>(addr, vals);
+        else RowCopy<DP, 1, true>{0, dim}.template all<NP>(addr, vals);
     };
     // Tiles in runs that one set of pages is enough for: n keys touch n / slots + 3
     // at most (the first, the last, and a cut between the first tokens and the rest).

@@ -308,8 +308,9 @@ struct Wave {
     // cores and the other units work at the same time within a wave.
     // Returns the largest of the next scores.  KEYS, VALUES: the next scores are
     // multiplied by scales of their keys, this tile's weights (but not their sum)
-    // by scales of theirs.
-    template <bool KEYS = false, bool VALUES = false>
+    // by scales of theirs.  FREE: the compiler may move instructions from one product
+    // to another.
+    template <bool KEYS = false, bool VALUES = false, bool FREE = false>
     __device__ __forceinline__ float advance(float scale, const uint8_t* keys, const uint8_t* vals, float top,
                                              f32x16 (&s)[2], f32x16 (&next)[2], const float* key_scales = nullptr,
                                              const float* value_scales = nullptr) {
@@ -378,7 +379,7 @@ struct Wave {
                 if constexpr (j == 0) best = next[0][0];
                 else best = fmaxf(best, next[j / 16u][j % 16u]);
             });
-            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (!FREE) __builtin_amdgcn_sched_barrier(0);
         });
         l += sum[0] + sum[1];
         return max_halves(best) * scale;
@@ -489,8 +490,8 @@ struct Wave {
 
 // Copy n of N of a wave's share of a tile: groups first, first + STEP, ... of
 // 64 chunks each.  Chunk i = 64 * group + lane is row i / cpr; the row's
-// address says where it lies.
-template <uint32_t DP, uint32_t STEP, bool VALUES>
+// address says where it lies.  FULL: the row has DP elements.
+template <uint32_t DP, uint32_t STEP, bool VALUES, bool FULL = false>
 struct RowCopy {
     uint32_t first, dim;
     // Rows from one of the wave's groups to the next; where that is a whole
@@ -506,6 +507,7 @@ struct RowCopy {
         uint32_t row;
         const uint32_t c = chunk(n, row);
         const uint64_t at = addr[row] + c * 16u;
+        if constexpr (FULL) return at;
         const uint64_t in = (uint64_t)((int64_t)(int32_t)(c * 8u - dim) >> 32);   // all ones below dim, without a branch
         return (at & in) | (zero_row() & ~in);
     }

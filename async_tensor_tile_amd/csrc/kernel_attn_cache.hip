@@ -91,16 +91,32 @@ static uint64_t plan(CacheArgs* a, uint32_t hint) {
     uint64_t keys = hint;
     if (a->window && (uint64_t)a->window + a->sinks + span < keys) keys = (uint64_t)a->window + a->sinks + span;
     const uint64_t jobs = (uint64_t)a->batch * a->kv * a->blocks;
-    const uint64_t most = keys <= 512 ? 1 : ceil_div(keys, 256), want = room / jobs;
-    a->parts = (uint32_t)(want < 1 ? 1 : want < most ? want : most);
+    // Parts of 256 keys and above, of 128 while they leave compute units without one
+    // (2 trees of 13 nodes of 700 tokens: 14.3 us, in parts of 256 15.7; 1 x 60 nodes of
+    // 4000 tokens 27.9 and 23.9).  Few keys in one part: no second launch (512 keys of 64
+    // elements 10.4 us, 12.3 in two parts; 128 rows with 400 keys 21.7 and 16.4).
+    uint64_t parts = 1;
+    if (keys > (a->tall ? 256u : 512u)) {
+        const auto least = [](uint64_t x, uint64_t y) { return x < y ? x : y; };
+        const auto larger = [](uint64_t x, uint64_t y) { return x < y ? y : x; };
+        parts = larger(least(ceil_div(keys, 256), room / jobs), least(ceil_div(keys, 128), cus / jobs));
+        parts = larger(parts, 1);
+        // Rounds of workgroups that are mostly full (40 sequences of 8192 tokens, 8 heads:
+        // 228 us in one part, 198 in three).
+        const auto full = [&](uint64_t n) { return (double)(jobs * n) / (double)(ceil_div(jobs * n, room) * room); };
+        if (!a->tall && keys >= 2048)
+            for (uint64_t n = parts + 1, end = parts + 3; n <= end; ++n)
+                if (full(n) > 1.15 * full(parts)) parts = n;
+    }
+    a->parts = (uint32_t)parts;
     a->per_parts = 1.0 / a->parts;
     a->direct = a->parts == 1;
     constexpr uint64_t most_groups = max_groups(kThreads);                 // of the products' launch, of the join's
     const uint64_t blocks = (uint64_t)a->batch * a->kv * a->blocks32;
     if (jobs * a->parts > most_groups || blocks > most_groups) return 0;
-    const uint64_t parts = a->direct ? 0 : blocks * a->parts;
-    a->part_ml = reinterpret_cast<float2*>(parts * dp * 32 * 4);           // behind the sums
-    return parts * (dp * 32 * 4 + 32 * 8) + 16;
+    const uint64_t pieces = a->direct ? 0 : blocks * a->parts;
+    a->part_ml = reinterpret_cast<float2*>(pieces * dp * 32 * 4);          // behind the sums
+    return pieces * (dp * 32 * 4 + 32 * 8) + 16;
 }
 
 template <typename T, uint32_t DP>
