@@ -8,7 +8,7 @@
 // (a tree) the drafted ones, whose tiles stand in descending order so that a
 // row's way up its ancestors is walked once.  Few rows (a token a sequence): 32
 // in a workgroup, whose waves take tiles of 32 keys in turn.  Many (a prompt):
-// 128, 32 a wave, over shared tiles of 64 keys.  Where that leaves the GPU
+// 32 a wave, over shared tiles of 64 keys.  Where that leaves the GPU
 // unfilled the list is cut into parts, joined by a second launch.
 //
 // A tile that every row sees whole is not masked.  In the others each lane masks
@@ -46,7 +46,7 @@ struct CacheArgs {
     uint32_t dim, q_len, group, kv, batch;
     uint32_t blocks32, blocks;       // of a sequence's key / value head: of 32 rows, of a workgroup's
     uint32_t parts;                  // along the keys
-    uint32_t tall;                   // 128 rows a workgroup
+    uint32_t tall;                   // 32 rows a wave, else a workgroup
     uint32_t first_item;             // of (block, part) pairs, where a launch does not hold them all
     double per_group, per_slots, per_parts;   // 1 / group, 1 / slots, 1 / parts
     uint32_t direct;                 // one part: the result is written at once
@@ -54,6 +54,11 @@ struct CacheArgs {
     uint32_t flip;                   // sign bits to turn in the queries (scale below 0)
     uint32_t zero;                   // the scale is 0
 };
+
+// Waves of a workgroup with many rows.  Codes are turned into elements by all of
+// them, so eight waves on one tile halve that work; above dim 128 a wave needs the
+// registers of two.
+constexpr uint32_t tall_waves(bool codes, uint32_t dp) { return codes && dp <= 128 ? 8u : 4u; }
 
 typedef __attribute__((address_space(4))) const CacheArgs cargs;
 __device__ __forceinline__ cargs& kernel_args() { return *(cargs*)__builtin_amdgcn_kernarg_segment_ptr(); }
@@ -448,13 +453,14 @@ __device__ __forceinline__ void store_lse(cargs& a, const Row& r, float m, float
 
 // ---- many rows ----------------------------------------------------------------------
 
-// Four waves of 32 rows over shared tiles of 64 keys.  Two stages: while a tile
+// Waves of 32 rows over shared tiles of 64 keys.  Two stages: while a tile
 // is used the next is on its way; a barrier a tile.
 template <typename T, uint32_t DP, int FMT>
 __device__ __forceinline__ void tall_part(cargs& a, Shared<DP, FMT>& sh, const Job& job) {
+    constexpr uint32_t WAVES = tall_waves(FMT != KV_SAME, DP), THREADS = 64u * WAVES, ROWS = 32u * WAVES;
     const uint32_t tid = threadIdx.x, wave = uniform(tid / 64u), lane = lane_id();
-    const uint32_t rows = job.seq.count * a.group, first_row = job.block * kWgRows;
-    const uint32_t last_row = first_row + kWgRows < rows ? first_row + kWgRows - 1u : rows - 1u;
+    const uint32_t rows = job.seq.count * a.group, first_row = job.block * ROWS;
+    const uint32_t last_row = first_row + ROWS < rows ? first_row + ROWS - 1u : rows - 1u;
     const Span x = span_of<kTile>(a, job.seq, uniform(quotient(first_row, a.per_group)),
                                   uniform(quotient(last_row, a.per_group)));
     const uint32_t per = part_keys(x.n, a.parts, kTile);
@@ -463,13 +469,19 @@ __device__ __forceinline__ void tall_part(cargs& a, Shared<DP, FMT>& sh, const J
     const Row row = row_of(a, job, first_row + wave * kRows + lane % 32u, rows);
     const bool busy = first_row + wave * kRows < rows;
     constexpr uint32_t SEG = kSegment / kTile;                            // tiles of a segment
-    constexpr uint32_t NG = Geo<DP>::cpr / kWaves;                        // groups a wave copies of a tile's keys
+    constexpr uint32_t NG = Geo<DP>::cpr / WAVES;                         // groups a wave copies of a tile's keys
+    // The threads that place the keys of a segment, one each.
+    const bool places = THREADS == kSegment || tid < kSegment;
     constexpr bool CODES = FMT != KV_SAME, WEIGHTS = CODES && kScaledWeights<T>;
     Wave<T, DP> w;
     w.load_row(a, row.q, row.valid);
-    int32_t page = page_of_key<kTile>(a, x, job.seq.row, k0 + tid, k1);
-    Scales scales = place_key<kTile, DP, FMT>(a, x, job.head, k0 + tid, k1, page, sh, tid);
-    if (CODES) {
+    int32_t page = -1;
+    Scales scales = {0, 0};
+    if (places) {
+        page = page_of_key<kTile>(a, x, job.seq.row, k0 + tid, k1);
+        scales = place_key<kTile, DP, FMT>(a, x, job.head, k0 + tid, k1, page, sh, tid);
+    }
+    if (CODES && places) {
         sh.kscale[tid] = __builtin_bit_cast(float, scale_bits(scales.k));
         sh.vscale[tid] = __builtin_bit_cast(float, scale_bits(scales.v));
         page = page_of_key<kTile>(a, x, job.seq.row, k0 + kSegment + tid, k1);
@@ -484,15 +496,15 @@ __device__ __forceinline__ void tall_part(cargs& a, Shared<DP, FMT>& sh, const J
     auto in = [&](uint32_t t) { return t % (2u * SEG) * kTile; };         // where a tile's keys are placed
     const uint32_t dim = a.dim;
     auto copy_k = [&](const uint64_t* addr, const uint8_t* to) {
-        if (dim == DP) RowCopy<DP, kWaves, false, true>{wave, DP}.template all<NG>(addr, to);
-        else RowCopy<DP, kWaves, false>{wave, dim}.template all<NG>(addr, to);
+        if (dim == DP) RowCopy<DP, WAVES, false, true>{wave, DP}.template all<NG>(addr, to);
+        else RowCopy<DP, WAVES, false>{wave, dim}.template all<NG>(addr, to);
     };
     auto copy_v = [&](const uint64_t* addr, const uint8_t* to) {
-        if (dim == DP) RowCopy<DP, kWaves, true, true>{wave, DP}.template all<NG>(addr, to);
-        else RowCopy<DP, kWaves, true>{wave, dim}.template all<NG>(addr, to);
+        if (dim == DP) RowCopy<DP, WAVES, true, true>{wave, DP}.template all<NG>(addr, to);
+        else RowCopy<DP, WAVES, true>{wave, dim}.template all<NG>(addr, to);
     };
-    CodeCopy<T, DP, FMT == KV_SAME ? KV_INT8 : FMT, kTile, kThreads, false> kcode;
-    CodeCopy<T, DP, FMT == KV_SAME ? KV_INT8 : FMT, kTile, kThreads, true> vcode;
+    CodeCopy<T, DP, FMT == KV_SAME ? KV_INT8 : FMT, kTile, THREADS, false> kcode;
+    CodeCopy<T, DP, FMT == KV_SAME ? KV_INT8 : FMT, kTile, THREADS, true> vcode;
     // What is on its way has arrived, for every wave, and every wave is done
     // with the stages that are filled next.
     auto meet = [&] {
@@ -505,16 +517,16 @@ __device__ __forceinline__ void tall_part(cargs& a, Shared<DP, FMT>& sh, const J
     constexpr uint32_t PLACE = CODES ? 0u : 1u, FETCH = CODES ? SEG - 1u : 0u, AHEAD = CODES ? 2u : 1u;
     auto begin = [&](uint32_t t) {
         meet();
-        if (t % SEG == PLACE) {
+        if (t % SEG == PLACE && places) {
             const uint32_t s = t / SEG + 1u, at = (s & 1u) * kSegment + tid;
             scales = place_key<kTile, DP, FMT>(fresh(), x, job.head, k0 + s * kSegment + tid, k1, page, sh, at);
         }
-        if (CODES && t % SEG == 1u) {
+        if (CODES && t % SEG == 1u && places) {
             const uint32_t at = ((t / SEG + 1u) & 1u) * kSegment + tid;
             sh.kscale[at] = __builtin_bit_cast(float, scale_bits(scales.k));
             sh.vscale[at] = __builtin_bit_cast(float, scale_bits(scales.v));
         }
-        if (t % SEG == FETCH)
+        if (t % SEG == FETCH && places)
             page = page_of_key<kTile>(fresh(), x, job.seq.row, k0 + (t / SEG + AHEAD) * kSegment + tid, k1);
         if (tid == 0) sh.odd[(t + 1u) % 3u] = 0u;
     };
@@ -563,7 +575,7 @@ __device__ __forceinline__ void tall_part(cargs& a, Shared<DP, FMT>& sh, const J
     // whole are added to the rows that see them, and are 0 for the product.
     auto odd_values = [&](uint32_t t, const f32x16 (&p)[2]) {
         uint8_t* const v = vals(t);
-        const bool odd = Wave<T, DP>::template odd_share<false>(v, wave, kWaves, kTile);
+        const bool odd = Wave<T, DP>::template odd_share<false>(v, wave, WAVES, kTile);
         if (odd && lane == 0) sh.odd[t % 3u] = 1u;
         wait_lgkm0();
         wg_barrier();
@@ -571,7 +583,7 @@ __device__ __forceinline__ void tall_part(cargs& a, Shared<DP, FMT>& sh, const J
         if (busy) w.template add_odd<2>(v, p, seen);
         wait_lgkm0();
         wg_barrier();
-        Wave<T, DP>::template odd_share<true>(v, wave, kWaves, kTile);
+        Wave<T, DP>::template odd_share<true>(v, wave, WAVES, kTile);
         wait_lgkm0();
         wg_barrier();
     };
@@ -633,7 +645,7 @@ __device__ __forceinline__ void tall_part(cargs& a, Shared<DP, FMT>& sh, const J
         if (lane < 32u && e.lse) store_lse(e, out, w.m, l);
         return;
     }
-    const uint64_t at = part_index(e, job.b, job.head, job.block * kWaves + wave, job.part);
+    const uint64_t at = part_index(e, job.b, job.head, job.block * WAVES + wave, job.part);
     f32x4* out = part_at<DP>(e, at);
 #pragma unroll
     for (uint32_t b = 0; b < DP / 32u; ++b)
@@ -841,9 +853,11 @@ __device__ __forceinline__ void short_part(cargs& a, ShortShared<DP, FMT>& sh, c
     }
 }
 
-// TALL: 128 rows a workgroup, else 32.
+// TALL: 32 rows a wave, else 32 a workgroup.
 template <typename T, uint32_t DP, int FMT, bool TALL>
-__global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_attn_cache(const CacheArgs) {
+__global__ __launch_bounds__(TALL ? 64 * tall_waves(FMT != KV_SAME, DP) : kThreads, DP <= 128 ? 2 : 1) void k_attn_cache(
+    const CacheArgs) {
+    constexpr uint32_t THREADS = TALL ? 64u * tall_waves(FMT != KV_SAME, DP) : kThreads;
     cargs& a = kernel_args();
     __shared__ __attribute__((aligned(1024))) std::conditional_t<TALL, Shared<DP, FMT>, ShortShared<DP, FMT>> sh;
     Job job;
@@ -870,9 +884,9 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_attn_cache(cons
     if constexpr (TALL) job.block = a.blocks - 1u - rest;
     else job.b = rest, job.block = 0;
     job.seq = sequence_of(a, job.b, job.head == 0 && job.part == 0 && job.block == 0);
-    if (job.block * (TALL ? kWgRows : kRows) >= job.seq.count * a.group) return;
+    if (job.block * (TALL ? THREADS / 2u : kRows) >= job.seq.count * a.group) return;
     if (a.parent) {
-        for (uint32_t n = threadIdx.x; n < job.seq.count; n += kThreads) {
+        for (uint32_t n = threadIdx.x; n < job.seq.count; n += THREADS) {
             const int32_t p = a.parent[(uint64_t)job.b * a.q_len + n];
             const bool ok = p >= -1 && p < (int32_t)n;
             if (!ok) record_page_error(a.err);

@@ -19,8 +19,8 @@ static void launch_dim(const CacheArgs& a, hipStream_t stream) {
     CacheArgs part = a;
     for (; part.first_item < items; part.first_item += most) {
         const uint32_t left = items - part.first_item;
-        hipLaunchKernelGGL((k_attn_cache<T, DP, FMT, true>), dim3(a.kv, a.batch, left < most ? left : most), dim3(kThreads),
-                           0, stream, part);
+        hipLaunchKernelGGL((k_attn_cache<T, DP, FMT, true>), dim3(a.kv, a.batch, left < most ? left : most),
+                           dim3(64u * tall_waves(FMT != KV_SAME, DP)), 0, stream, part);
     }
 }
 

@@ -71,10 +71,9 @@ static uint64_t ceil_div(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
 // How the work is cut: fills the fields of `a` that follow from the shapes, the
 // window and the hint alone and returns the workspace's bytes, 0 if there are
 // more rows than 31 bits count or more workgroups than a launch holds.
-static uint64_t plan(CacheArgs* a, uint32_t hint) {
+static uint64_t plan(CacheArgs* a, uint32_t hint, bool codes) {
     constexpr uint64_t cus = 256;
     const uint32_t dp = padded_dim((uint32_t)a->q.dim[0]);
-    const uint64_t room = dp <= 128 ? 2 * cus : cus;                       // workgroups that run at once
     a->dim = (uint32_t)a->q.dim[0];
     a->q_len = (uint32_t)a->q.dim[2];
     a->batch = (uint32_t)a->q.dim[3];
@@ -84,10 +83,12 @@ static uint64_t plan(CacheArgs* a, uint32_t hint) {
     if (rows * a->batch > 0x7FFFFFFFull) return 0;
     a->per_group = 1.0 / a->group;
     a->tall = rows > kRows;
-    a->blocks = (uint32_t)ceil_div(rows, a->tall ? kWgRows : kRows);
-    a->blocks32 = a->tall ? a->blocks * kWaves : a->blocks;
+    const uint32_t waves = a->tall ? tall_waves(codes, dp) : 1u;
+    const uint64_t room = dp <= 128 && waves <= 4 ? 2 * cus : cus;         // workgroups that run at once
+    a->blocks32 = (uint32_t)ceil_div(rows, kRows * waves) * waves;
+    a->blocks = a->blocks32 / waves;
     // keys of a block of rows: those of the window, or all
-    const uint64_t span = ceil_div(a->tall ? kWgRows : kRows, a->group) + 1;
+    const uint64_t span = ceil_div(kRows * waves, a->group) + 1;
     uint64_t keys = hint;
     if (a->window && (uint64_t)a->window + a->sinks + span < keys) keys = (uint64_t)a->window + a->sinks + span;
     const uint64_t jobs = (uint64_t)a->batch * a->kv * a->blocks;
@@ -168,7 +169,7 @@ static tmap_status attend(const tmap_t* q, const tmap_t* k_pool, const tmap_t* v
     if (reinterpret_cast<uintptr_t>(d_ws) % 16 != 0) return TMAP_ERR_ALIGN;
     a.window = window;
     a.sinks = window ? sinks : 0;
-    const uint64_t need = plan(&a, len_hint);
+    const uint64_t need = plan(&a, len_hint, format != KV_SAME);
     if (need == 0 || ws_bytes < need) return TMAP_ERR_UNSUPPORTED;
     a.part_o = static_cast<f32x4*>(d_ws);
     a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(d_ws) + reinterpret_cast<uintptr_t>(a.part_ml));
@@ -208,7 +209,7 @@ extern "C" uint64_t attn_cache_workspace(const tmap_t* q, const tmap_t* k_pool, 
     if (view_of(q, 4, &a.q, &tq) || view_of(k_pool, 4, &a.k, &tk) || !shapes_fit(a.q, a.k)) return 0;
     a.window = window;
     a.sinks = window ? sinks : 0;
-    return plan(&a, len_hint);
+    return plan(&a, len_hint, tk == TMAP_U8);
 }
 
 extern "C" tmap_status attn_window(const tmap_t* q, const tmap_t* k_pool, const tmap_t* v_pool, int32_t format,
