@@ -46,19 +46,14 @@ struct CacheArgs {
     uint32_t dim, q_len, group, kv, batch;
     uint32_t blocks32, blocks;       // of a sequence's key / value head: of 32 rows, of a workgroup's
     uint32_t parts;                  // along the keys
-    uint32_t tall;                   // 32 rows a wave, else a workgroup
+    uint32_t waves;                  // of a workgroup with 32 rows each; 0: few rows, 32 in all
     uint32_t first_item;             // of (block, part) pairs, where a launch does not hold them all
-    double per_group, per_slots, per_parts;   // 1 / group, 1 / slots, 1 / parts
+    double per_group, per_slots, per_parts, per_block, per_kv;   // 1 / group, / slots, / parts, / blocks32, / kv
     uint32_t direct;                 // one part: the result is written at once
     float scale;                     // |scale| * log2(e), 1 if that is 0
     uint32_t flip;                   // sign bits to turn in the queries (scale below 0)
     uint32_t zero;                   // the scale is 0
 };
-
-// Waves of a workgroup with many rows.  Codes are turned into elements by all of
-// them, so eight waves on one tile halve that work; above dim 128 a wave needs the
-// registers of two.
-constexpr uint32_t tall_waves(bool codes, uint32_t dp) { return codes && dp <= 128 ? 8u : 4u; }
 
 typedef __attribute__((address_space(4))) const CacheArgs cargs;
 __device__ __forceinline__ cargs& kernel_args() { return *(cargs*)__builtin_amdgcn_kernarg_segment_ptr(); }
@@ -82,9 +77,15 @@ struct Sequence {
     uint32_t count;      // queries; 0 where there are none, or something is out of range
 };
 
+__device__ __forceinline__ uint32_t asked_of(cargs& a, uint32_t b) {
+    return a.count ? (uint32_t)scalar_load(a.count, b) : a.q_len;
+}
+__device__ __forceinline__ uint32_t count_of(cargs& a, uint32_t asked) { return asked <= a.q_len ? asked : 0u; }
+
+// `record`: what is out of range is recorded.
 __device__ __forceinline__ Sequence sequence_of(cargs& a, uint32_t b, bool record) {
-    const uint32_t asked = a.count ? (uint32_t)scalar_load(a.count, b) : a.q_len;
-    Sequence s = {a.rows ? (uint32_t)scalar_load(a.rows, b) : b, 0u, asked <= a.q_len ? asked : 0u};
+    const uint32_t asked = asked_of(a, b);
+    Sequence s = {a.rows ? (uint32_t)scalar_load(a.rows, b) : b, 0u, count_of(a, asked)};
     bool bad = asked > a.q_len;
     if (s.count == 0u) {
         if (bad && record && threadIdx.x == 0) record_page_error(a.err);
@@ -455,9 +456,9 @@ __device__ __forceinline__ void store_lse(cargs& a, const Row& r, float m, float
 
 // Waves of 32 rows over shared tiles of 64 keys.  Two stages: while a tile
 // is used the next is on its way; a barrier a tile.
-template <typename T, uint32_t DP, int FMT>
+template <typename T, uint32_t DP, int FMT, uint32_t WAVES>
 __device__ __forceinline__ void tall_part(cargs& a, Shared<DP, FMT>& sh, const Job& job) {
-    constexpr uint32_t WAVES = tall_waves(FMT != KV_SAME, DP), THREADS = 64u * WAVES, ROWS = 32u * WAVES;
+    constexpr uint32_t THREADS = 64u * WAVES, ROWS = 32u * WAVES;
     const uint32_t tid = threadIdx.x, wave = uniform(tid / 64u), lane = lane_id();
     const uint32_t rows = job.seq.count * a.group, first_row = job.block * ROWS;
     const uint32_t last_row = first_row + ROWS < rows ? first_row + ROWS - 1u : rows - 1u;
@@ -470,6 +471,7 @@ __device__ __forceinline__ void tall_part(cargs& a, Shared<DP, FMT>& sh, const J
     const bool busy = first_row + wave * kRows < rows;
     constexpr uint32_t SEG = kSegment / kTile;                            // tiles of a segment
     constexpr uint32_t NG = Geo<DP>::cpr / WAVES;                         // groups a wave copies of a tile's keys
+    static_assert(FMT != KV_SAME || Geo<DP>::cpr % WAVES == 0, "every wave copies as many");
     // The threads that place the keys of a segment, one each.
     const bool places = THREADS == kSegment || tid < kSegment;
     constexpr bool CODES = FMT != KV_SAME, WEIGHTS = CODES && kScaledWeights<T>;
@@ -600,14 +602,18 @@ __device__ __forceinline__ void tall_part(cargs& a, Shared<DP, FMT>& sh, const J
         if (CODES) scale_scores(s[0], sh.kscale + in(0));
         finish(0, s[0], false);
     }
-    // Tiles of both kinds in loops of their own: in one loop their registers do not fit beside each other.
+    // Tiles of both kinds in loops of their own: in one loop their registers do not
+    // fit beside each other.  Above dim 128 those of a tile between two others do not
+    // either (2048 queries of 32768 tokens, dim 256: 7570 us, one after the other 4510).
+    constexpr bool BETWEEN = DP <= 128;
     for (uint32_t t = 0; t < tiles;) {
-        for (; t < tiles && !seen_by_all<kTile>(x, k0 + t * kTile); ++t) {
+        for (; t < tiles && !(BETWEEN && seen_by_all<kTile>(x, k0 + t * kTile)); ++t) {
             begin(t);
             fill(t);
             if (busy) w.weights(scale, s[0]);
             if (WEIGHTS && busy) scale_weights<true>(s[0], sh.vscale + in(t), seen);
-            if (!WEIGHTS || FMT != KV_INT8) odd_values(t, s[0]);           // an int8 code is a number
+            if ((!WEIGHTS || FMT != KV_INT8) && (BETWEEN || !seen_by_all<kTile>(x, k0 + t * kTile)))
+                odd_values(t, s[0]);                                       // an int8 code is a number
             if (!busy) continue;
             typename Wave<T, DP>::Piece z[2][DP / 32];
             w.read_values(vals(t), 0, z[0]);
@@ -616,6 +622,7 @@ __device__ __forceinline__ void tall_part(cargs& a, Shared<DP, FMT>& sh, const J
             if (CODES) scale_scores(s[0], sh.kscale + in(t + 1u));
             finish(t + 1u, s[0], false);
         }
+        if constexpr (!BETWEEN) break;
         uint32_t n = 0;
         while (t + n < tiles && seen_by_all<kTile>(x, k0 + (t + n) * kTile)) ++n;
         for (; n > 1u; n -= 2u, t += 2u) {
@@ -853,11 +860,11 @@ __device__ __forceinline__ void short_part(cargs& a, ShortShared<DP, FMT>& sh, c
     }
 }
 
-// TALL: 32 rows a wave, else 32 a workgroup.
-template <typename T, uint32_t DP, int FMT, bool TALL>
-__global__ __launch_bounds__(TALL ? 64 * tall_waves(FMT != KV_SAME, DP) : kThreads, DP <= 128 ? 2 : 1) void k_attn_cache(
-    const CacheArgs) {
-    constexpr uint32_t THREADS = TALL ? 64u * tall_waves(FMT != KV_SAME, DP) : kThreads;
+// WAVES of 32 rows each; 0: few rows, 32 in all, and four waves on them.
+template <typename T, uint32_t DP, int FMT, uint32_t WAVES>
+__global__ __launch_bounds__(WAVES ? 64 * WAVES : kThreads, DP <= 128 ? 2 : 1) void k_attn_cache(const CacheArgs) {
+    constexpr bool TALL = WAVES != 0;
+    constexpr uint32_t THREADS = TALL ? 64u * WAVES : kThreads;
     cargs& a = kernel_args();
     __shared__ __attribute__((aligned(1024))) std::conditional_t<TALL, Shared<DP, FMT>, ShortShared<DP, FMT>> sh;
     Job job;
@@ -893,7 +900,7 @@ __global__ __launch_bounds__(TALL ? 64 * tall_waves(FMT != KV_SAME, DP) : kThrea
             sh.parent[n] = ok ? (uint16_t)p : (uint16_t)0xFFFFu;
         }
     }
-    if constexpr (TALL) tall_part<T, DP, FMT>(a, sh, job);
+    if constexpr (TALL) tall_part<T, DP, FMT, WAVES>(a, sh, job);
     else short_part<T, DP, FMT>(a, sh, job);
 }
 

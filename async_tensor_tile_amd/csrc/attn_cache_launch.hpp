@@ -6,21 +6,32 @@
 
 namespace att {
 
-template <typename T, int FMT, uint32_t DP>
-static void launch_dim(const CacheArgs& a, hipStream_t stream) {
-    constexpr uint32_t most = 65535;                                       // a grid's y and z
-    if (!a.tall) {
-        const uint32_t eights = (a.batch * a.parts + 7u) / 8u, y = eights < most ? eights : most;
-        hipLaunchKernelGGL((k_attn_cache<T, DP, FMT, false>), dim3(8u * a.kv, y, (eights + y - 1u) / y), dim3(kThreads), 0,
-                           stream, a);
-        return;
-    }
+constexpr uint32_t kMostGrid = 65535;                                      // a grid's y and z
+
+template <typename T, int FMT, uint32_t DP, uint32_t WAVES>
+static void launch_tall(const CacheArgs& a, hipStream_t stream) {
     const uint32_t items = a.blocks * a.parts;
     CacheArgs part = a;
-    for (; part.first_item < items; part.first_item += most) {
+    for (; part.first_item < items; part.first_item += kMostGrid) {
         const uint32_t left = items - part.first_item;
-        hipLaunchKernelGGL((k_attn_cache<T, DP, FMT, true>), dim3(a.kv, a.batch, left < most ? left : most),
-                           dim3(64u * tall_waves(FMT != KV_SAME, DP)), 0, stream, part);
+        hipLaunchKernelGGL((k_attn_cache<T, DP, FMT, WAVES>), dim3(a.kv, a.batch, left < kMostGrid ? left : kMostGrid),
+                           dim3(64u * WAVES), 0, stream, part);
+    }
+}
+
+template <typename T, int FMT, uint32_t DP>
+static void launch_dim(const CacheArgs& a, hipStream_t stream) {
+    if (a.waves == 0) {
+        const uint32_t eights = (a.batch * a.parts + 7u) / 8u, y = eights < kMostGrid ? eights : kMostGrid;
+        hipLaunchKernelGGL((k_attn_cache<T, DP, FMT, 0>), dim3(8u * a.kv, y, (eights + y - 1u) / y), dim3(kThreads), 0,
+                           stream, a);
+    } else if constexpr (DP > 128 || (DP == 96 && FMT == KV_SAME)) {
+        launch_tall<T, FMT, DP, 4>(a, stream);
+    } else if constexpr (FMT != KV_SAME) {
+        launch_tall<T, FMT, DP, 8>(a, stream);
+    } else {
+        if (a.waves == 8) launch_tall<T, FMT, DP, 8>(a, stream);
+        else launch_tall<T, FMT, DP, 4>(a, stream);
     }
 }
 

@@ -16,11 +16,12 @@ __global__ __launch_bounds__(kThreads) void k_attn_cache_join(const CacheArgs) {
     cargs& a = kernel_args();
     constexpr uint32_t U = 16;                                            // parts in flight
     const uint32_t lane = lane_id(), n32 = lane % 32u, hh = lane / 32u;
-    const uint32_t block = blockIdx.x % a.blocks32, unit = blockIdx.x / a.blocks32, head = unit % a.kv, b = unit / a.kv;
+    const uint32_t unit = uniform(quotient(blockIdx.x, a.per_block)), block = blockIdx.x - unit * a.blocks32;
+    const uint32_t b = uniform(quotient(unit, a.per_kv)), head = unit - b * a.kv;
     const uint32_t f = blockIdx.y * kWaves + threadIdx.x / 64u, d = 8u * f + 4u * hh;
     if (8u * f >= a.dim) return;
-    const Job job = {b, head, 0u, 0u, sequence_of(a, b, false)};
-    const uint32_t rows = job.seq.count * a.group;
+    const Job job = {b, head, 0u, 0u, {}};
+    const uint32_t rows = count_of(a, asked_of(a, b)) * a.group;
     if (block * kRows >= rows) return;
     const uint64_t first = part_index(a, b, head, block, 0);
     const Row row = row_of(a, job, block * kRows + n32, rows);
@@ -82,22 +83,30 @@ static uint64_t plan(CacheArgs* a, uint32_t hint, bool codes) {
     const uint64_t rows = (uint64_t)a->q_len * a->group;
     if (rows * a->batch > 0x7FFFFFFFull) return 0;
     a->per_group = 1.0 / a->group;
-    a->tall = rows > kRows;
-    const uint32_t waves = a->tall ? tall_waves(codes, dp) : 1u;
+    // Waves of a workgroup with many rows.  Eight share a tile's copies, and the work
+    // of turning codes into elements (2048 queries of 32768 tokens: 987 us, with four
+    // waves 1055; int8 1626 and 1973), but mask more where they see few keys (8192
+    // queries, window 128: 98 and 88 us, window 1024 200 and 197) and wait for each
+    // other where half of them have no rows (16 trees of 120 rows: 75 and 69 us).
+    // Above dim 128 a wave needs the registers of two; the twelve groups of a tile's copies
+    // at dim 96 are no whole number for each of eight.
+    const auto keys_of = [&](uint64_t block) -> uint64_t {                // keys of a block of rows: of the window, or all
+        const uint64_t all = (uint64_t)a->window + a->sinks + ceil_div(block, a->group) + 1;
+        return a->window && all < hint ? all : hint;
+    };
+    a->waves = rows <= kRows ? 0u : dp > 128 ? 4u : codes || (dp != 96 && rows > 4 * kRows && keys_of(8 * kRows) >= 2048) ? 8u : 4u;
+    const uint32_t waves = a->waves ? a->waves : 1u;
+    const uint64_t keys = keys_of(kRows * waves);
     const uint64_t room = dp <= 128 && waves <= 4 ? 2 * cus : cus;         // workgroups that run at once
     a->blocks32 = (uint32_t)ceil_div(rows, kRows * waves) * waves;
     a->blocks = a->blocks32 / waves;
-    // keys of a block of rows: those of the window, or all
-    const uint64_t span = ceil_div(kRows * waves, a->group) + 1;
-    uint64_t keys = hint;
-    if (a->window && (uint64_t)a->window + a->sinks + span < keys) keys = (uint64_t)a->window + a->sinks + span;
     const uint64_t jobs = (uint64_t)a->batch * a->kv * a->blocks;
     // Parts of 256 keys and above, of 128 while they leave compute units without one
     // (2 trees of 13 nodes of 700 tokens: 14.3 us, in parts of 256 15.7; 1 x 60 nodes of
     // 4000 tokens 27.9 and 23.9).  Few keys in one part: no second launch (512 keys of 64
     // elements 10.4 us, 12.3 in two parts; 128 rows with 400 keys 21.7 and 16.4).
     uint64_t parts = 1;
-    if (keys > (a->tall ? 256u : 512u)) {
+    if (keys > (a->waves ? 256u : 512u)) {
         const auto least = [](uint64_t x, uint64_t y) { return x < y ? x : y; };
         const auto larger = [](uint64_t x, uint64_t y) { return x < y ? y : x; };
         parts = larger(least(ceil_div(keys, 256), room / jobs), least(ceil_div(keys, 128), cus / jobs));
@@ -105,12 +114,14 @@ static uint64_t plan(CacheArgs* a, uint32_t hint, bool codes) {
         // Rounds of workgroups that are mostly full (40 sequences of 8192 tokens, 8 heads:
         // 228 us in one part, 198 in three).
         const auto full = [&](uint64_t n) { return (double)(jobs * n) / (double)(ceil_div(jobs * n, room) * room); };
-        if (!a->tall && keys >= 2048)
+        if (!a->waves && keys >= 2048)
             for (uint64_t n = parts + 1, end = parts + 3; n <= end; ++n)
                 if (full(n) > 1.15 * full(parts)) parts = n;
     }
     a->parts = (uint32_t)parts;
     a->per_parts = 1.0 / a->parts;
+    a->per_block = 1.0 / a->blocks32;
+    a->per_kv = 1.0 / a->kv;
     a->direct = a->parts == 1;
     constexpr uint64_t most_groups = max_groups(kThreads);                 // of the products' launch, of the join's
     const uint64_t blocks = (uint64_t)a->batch * a->kv * a->blocks32;
