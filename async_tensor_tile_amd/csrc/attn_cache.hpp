@@ -674,12 +674,14 @@ __device__ __forceinline__ void tall_part(cargs& a, Shared<DP, FMT>& sh, const J
 template <typename T, uint32_t DP, int FMT>
 __device__ __forceinline__ void short_part(cargs& a, ShortShared<DP, FMT>& sh, const Job& job) {
     const uint32_t tid = threadIdx.x, wave = uniform(tid / 64u), lane = lane_id(), n32 = lane % 32u;
-    const uint32_t rows = job.seq.count * a.group;
-    const Span x = span_of<kOwnTile>(a, job.seq, 0u, job.seq.count - 1u);
+    const uint32_t rows = job.seq.count * a.group, first_row = job.block * kRows;
+    const uint32_t last_row = first_row + kRows < rows ? first_row + kRows - 1u : rows - 1u;
+    const Span x = span_of<kOwnTile>(a, job.seq, uniform(quotient(first_row, a.per_group)),
+                                     uniform(quotient(last_row, a.per_group)));
     const uint32_t per = part_keys(x.n, a.parts, kOwnTile);
     const uint32_t k0 = part_begin(x.n, job.part, per), k1 = part_begin(x.n, job.part + 1u, per);
     const uint32_t tiles = (k1 - k0 + kOwnTile - 1u) / kOwnTile;
-    const Row row = row_of(a, job, n32, rows);
+    const Row row = row_of(a, job, first_row + n32, rows);
     constexpr uint32_t NP = Geo<DP>::cpr / 2;                             // copies of a tile's keys
     constexpr bool CODES = FMT != KV_SAME, WEIGHTS = CODES && kScaledWeights<T>;
     // Pages of the list: those of the first tokens, then those from `low` on.
@@ -884,12 +886,15 @@ __global__ __launch_bounds__(WAVES ? 64 * WAVES : kThreads, DP <= 128 ? 2 : 1) v
         // busy.
         item = (blockIdx.z * gridDim.y + blockIdx.y) * 8u + blockIdx.x % 8u;
         job.head = blockIdx.x / 8u;
-        if (item >= a.batch * a.parts) return;
+        if (item >= a.batch * a.blocks * a.parts) return;
     }
-    const uint32_t rest = a.parts == 1u ? item : uniform(quotient(item, a.per_parts));
+    uint32_t rest = a.parts == 1u ? item : uniform(quotient(item, a.per_parts));
     job.part = item - rest * a.parts;
-    if constexpr (TALL) job.block = a.blocks - 1u - rest;
-    else job.b = rest, job.block = 0;
+    if constexpr (!TALL) {
+        job.b = a.blocks == 1u ? rest : uniform(quotient(rest, a.per_block));   // blocks of 32 rows
+        rest -= job.b * a.blocks;
+    }
+    job.block = a.blocks - 1u - rest;
     job.seq = sequence_of(a, job.b, job.head == 0 && job.part == 0 && job.block == 0);
     if (job.block * (TALL ? THREADS / 2u : kRows) >= job.seq.count * a.group) return;
     if (a.parent) {

@@ -22,7 +22,7 @@ static void launch_tall(const CacheArgs& a, hipStream_t stream) {
 template <typename T, int FMT, uint32_t DP>
 static void launch_dim(const CacheArgs& a, hipStream_t stream) {
     if (a.waves == 0) {
-        const uint32_t eights = (a.batch * a.parts + 7u) / 8u, y = eights < kMostGrid ? eights : kMostGrid;
+        const uint32_t eights = (a.batch * a.blocks * a.parts + 7u) / 8u, y = eights < kMostGrid ? eights : kMostGrid;
         hipLaunchKernelGGL((k_attn_cache<T, DP, FMT, 0>), dim3(8u * a.kv, y, (eights + y - 1u) / y), dim3(kThreads), 0,
                            stream, a);
     } else if constexpr (DP > 128 || (DP == 96 && FMT == KV_SAME)) {

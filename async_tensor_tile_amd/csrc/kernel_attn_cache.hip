@@ -83,18 +83,25 @@ static uint64_t plan(CacheArgs* a, uint32_t hint, bool codes) {
     const uint64_t rows = (uint64_t)a->q_len * a->group;
     if (rows * a->batch > 0x7FFFFFFFull) return 0;
     a->per_group = 1.0 / a->group;
+    const auto keys_of = [&](uint64_t block) -> uint64_t {                // keys of a block of rows: of the window, or all
+        const uint64_t all = (uint64_t)a->window + a->sinks + ceil_div(block, a->group) + 1;
+        return a->window && all < hint ? all : hint;
+    };
+    // Blocks of 32 rows, each with all of its keys, while all of them run at once and
+    // their keys are few: the start is shorter (2 trees of 13 nodes x 4 heads of 700
+    // tokens: 12.3 us, with shared tiles 14.1; 8 of 32 nodes of 2000 42 and 32, e4m3 35
+    // and 47; 2048 queries of 2048 tokens, window 128: 59 and 24).
+    const uint64_t shorts = (uint64_t)a->batch * a->kv * ceil_div(rows, kRows);
+    const bool few = rows <= kRows || (shorts <= 2 * cus && shorts * keys_of(kRows) <= (codes ? 1u << 19 : 1u << 18));
     // Waves of a workgroup with many rows.  Eight share a tile's copies, and the work
-    // of turning codes into elements (2048 queries of 32768 tokens: 987 us, with four
+    // of turning codes into elements (2048 queries of 32768 tokens: 972 us, with four
     // waves 1055; int8 1626 and 1973), but mask more where they see few keys (8192
     // queries, window 128: 98 and 88 us, window 1024 200 and 197) and wait for each
     // other where half of them have no rows (16 trees of 120 rows: 75 and 69 us).
     // Above dim 128 a wave needs the registers of two; the twelve groups of a tile's copies
     // at dim 96 are no whole number for each of eight.
-    const auto keys_of = [&](uint64_t block) -> uint64_t {                // keys of a block of rows: of the window, or all
-        const uint64_t all = (uint64_t)a->window + a->sinks + ceil_div(block, a->group) + 1;
-        return a->window && all < hint ? all : hint;
-    };
-    a->waves = rows <= kRows ? 0u : dp > 128 ? 4u : codes || (dp != 96 && rows > 4 * kRows && keys_of(8 * kRows) >= 2048) ? 8u : 4u;
+    const bool many = codes || (dp != 96 && rows > 4 * kRows && keys_of(8 * kRows) >= 2048);
+    a->waves = few ? 0u : dp <= 128 && many ? 8u : 4u;
     const uint32_t waves = a->waves ? a->waves : 1u;
     const uint64_t keys = keys_of(kRows * waves);
     const uint64_t room = dp <= 128 && waves <= 4 ? 2 * cus : cus;         // workgroups that run at once
