@@ -228,3 +228,90 @@ def test_a_chain_is_causal():
         a = s.check(window, sinks)
         b = s.check(window, sinks, parents_of(g, 2, 40, "chain"))
         assert np.abs(a[0] - b[0]).max() < 2e-3 and np.abs(a[1] - b[1]).max() < 1e-5
+
+
+# ---- shared tiles: many rows whose work is cut as for long sequences, or of many sequences ----
+
+FAR = 1 << 20
+
+LONG = [  # dtype, fmt, lens, counts, q_len, heads, kv, dim, slots, heads_first, gap
+    ("bf16", "same", [200], None, 200, 4, 1, 64, 16, False, 0),
+    ("f16", "same", [300, 70, 5, 0], [33, 33, 5, 1], 33, 2, 2, 128, 16, False, 8),
+    ("bf16", "same", [1500, 600], [257, 300], 300, 2, 2, 128, 48, True, 0),
+    ("bf16", "same", [1000, 64], None, 65, 3, 3, 96, 33, False, 0),
+    ("f16", "same", [700, 200], None, 64, 6, 2, 72, 16, True, 0),
+    ("bf16", "same", [513, 100], [70, 100], 100, 4, 2, 192, 16, False, 0),
+    ("f16", "same", [450], None, 129, 2, 1, 256, 8, False, 0),
+    ("f16", "same", [130], None, 130, 5, 5, 40, 1, False, 0),
+    ("bf16", "int8", [777, 200], [300, 133], 300, 5, 1, 80, 48, True, 0),
+    ("f16", "e4m3", [1300, 64, 65], None, 100, 8, 2, 128, 16, False, 16),
+    ("f16", "int8", [900, 66], [80, 66], 80, 4, 4, 64, 16, False, 0),
+    ("bf16", "e4m3", [600], None, 90, 2, 1, 192, 16, True, 0),
+    ("f16", "e4m3", [333], None, 140, 1, 1, 96, 1, False, 0),
+    ("bf16", "int8", [600, 0, 3], [128, 5, 128], 128, 2, 1, 256, 16, False, 0),
+    ("bf16", "e4m3", [700, 33], [40, 33], 40, 1, 1, 112, 100, False, 0),
+]
+
+
+@pytest.mark.parametrize("case", range(len(LONG)))
+def test_long(case):
+    dtype, fmt, lens, counts, q_len, heads, kv, dim, slots, first, gap = LONG[case]
+    s = Setup(gen(700 + case), dtype, fmt, lens, counts, q_len, heads, kv, dim, slots, first, gap)
+    s.check(hint=FAR)
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (300, 0), (2500, 7), (40, 3)])
+@pytest.mark.parametrize("case", range(0, len(LONG), 2))
+def test_long_tree(case, window, sinks):
+    dtype, fmt, lens, counts, n, heads, kv, dim, slots, first, gap = LONG[case]
+    g = gen(720 + case)
+    counts = [min(a, b) for a, b in zip(lens, counts or [n] * len(lens))]
+    s = Setup(g, dtype, fmt, lens, counts, n, heads, kv, dim, slots, first, gap)
+    s.check(window, sinks, parents_of(g, len(lens), n, "near"), hint=FAR)
+
+
+MANY = [  # dtype, fmt, batch, length, q_len, heads, kv, dim, slots, heads_first, window, sinks
+    ("bf16", "same", 14, 260, 160, 8, 8, 64, 16, False, 0, 0),
+    ("f16", "same", 17, 400, 130, 8, 8, 128, 16, True, 60, 4),
+    ("bf16", "same", 13, 210, 70, 16, 8, 96, 48, False, 64, 64),
+    ("f16", "same", 20, 700, 100, 8, 4, 128, 7, False, 500, 1),
+    ("bf16", "same", 40, 190, 65, 5, 5, 192, 16, True, 33, 0),
+    ("f16", "int8", 18, 300, 130, 8, 8, 64, 16, False, 100, 3),
+    ("bf16", "e4m3", 18, 500, 129, 8, 8, 128, 33, True, 90, 90),
+    ("bf16", "int8", 15, 280, 100, 12, 6, 80, 16, False, 0, 0),
+    ("f16", "e4m3", 40, 150, 65, 5, 5, 256, 16, False, 20, 2),
+]
+
+
+@pytest.mark.parametrize("case", range(len(MANY)))
+def test_many_sequences(case):
+    """More blocks of 32 rows than run at once."""
+    dtype, fmt, batch, length, q_len, heads, kv, dim, slots, first, window, sinks = MANY[case]
+    g = gen(740 + case)
+    lens = [max(0, length - 13 * b) if b % 5 else length for b in range(batch)]
+    counts = [0 if b == 3 else max(1, q_len - 11 * (b % 7)) for b in range(batch)]
+    s = Setup(g, dtype, fmt, lens, counts, q_len, heads, kv, dim, slots, first)
+    s.check(window, sinks)
+    counts = [min(a, b) for a, b in zip(lens, counts)]
+    s = Setup(g, dtype, fmt, lens, counts, q_len, heads, kv, dim, slots, first)
+    s.check(window, sinks, parents_of(g, batch, q_len, "far"))
+
+
+@pytest.mark.parametrize("slots", [1, 2, 16])
+@pytest.mark.parametrize("fmt", ["same", "int8"])
+def test_more_pages_than_are_looked_up_at_once(fmt, slots):
+    """One part of more keys than a thousand pages hold, drafted tokens among them."""
+    g = gen(760 + slots)
+    n = 1020 * slots + 700
+    lens = [n] * 3 + [n - 500] * 2
+    for parents, q_len in ((None, 2), (parents_of(g, 5, 8, "near"), 8), (parents_of(g, 5, 30, "near"), 30)):
+        s = Setup(g, "f16", fmt, lens, None, q_len, 1, 1, 64, slots)
+        s.check(0, 0, parents, hint=100)
+        s.check(n - 200, 5, parents, hint=100)
+
+
+def test_a_long_tree_of_small_pages():
+    g = gen(770)
+    s = Setup(g, "bf16", "same", [3000], None, 1000, 1, 1, 64, 1)
+    s.check(0, 0, parents_of(g, 1, 1000, "near"), hint=100)
+    s.check(0, 0, parents_of(g, 1, 1000, "chain"), hint=FAR)

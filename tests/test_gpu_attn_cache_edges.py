@@ -44,6 +44,8 @@ def seen_by(s, b, parents, window, sinks):
     return ok.tree_sees(s.seq_lens[b], [int(p) for p in parents[b][:n]], window, sinks)
 
 
+FAR = 1 << 20       # a hint that cuts the work as for long sequences: shared tiles, many parts
+
 SHAPES = [  # dtype, fmt, lens, counts, q_len, heads, kv, dim, slots, heads_first, window, sinks, kind
     ("bf16", "same", [90, 300], None, 1, 8, 2, 128, 16, False, 50, 3, None),
     ("f16", "same", [90, 300], None, 6, 8, 2, 64, 7, True, 50, 3, None),
@@ -56,9 +58,10 @@ SHAPES = [  # dtype, fmt, lens, counts, q_len, heads, kv, dim, slots, heads_firs
 ]
 
 
+@pytest.mark.parametrize("hint", [None, FAR])
 @pytest.mark.parametrize("what", [float("nan"), float("inf"), float("-inf")])
 @pytest.mark.parametrize("case", range(len(SHAPES)))
-def test_what_is_not_seen_does_not_count(case, what):
+def test_what_is_not_seen_does_not_count(case, what, hint):
     """Slots behind the lengths, pages of no row and tokens that no query sees hold infinities and NaN; then so does a
     token that some queries see: the others' results stay as they were, bit for bit."""
     dtype, fmt, lens, counts, q_len, heads, kv, dim, slots, first, window, sinks, kind = SHAPES[case]
@@ -66,7 +69,7 @@ def test_what_is_not_seen_does_not_count(case, what):
     s = Setup(g, dtype, fmt, lens, counts, q_len, heads, kv, dim, slots, first)
     parents = None if kind is None else parents_of(g, len(lens), q_len, kind)
     d_parents = None if parents is None else ints(parents)
-    clean = s.run(window, sinks, d_parents)
+    clean = s.run(window, sinks, d_parents, hint=hint)
     held = np.zeros((s.pages, slots), bool)
     sees = [seen_by(s, b, parents, window, sinks) for b in range(len(lens))]
     for b, r in enumerate(s.rows):
@@ -82,7 +85,7 @@ def test_what_is_not_seen_does_not_count(case, what):
                 at = 2 * slot
                 x[:, slots + at // dim, at % dim:at % dim + 2] = torch.tensor([what]).bfloat16().view(torch.uint8).cuda()
                 x[:, slot] = 0x7F
-    got = s.run(window, sinks, d_parents)
+    got = s.run(window, sinks, d_parents, hint=hint)
     assert all(np.array_equal(a, c) for a, c in zip(got, clean))
     if q_len == 1:
         return
@@ -91,7 +94,7 @@ def test_what_is_not_seen_does_not_count(case, what):
     tokens = [int(t[len(t) // 2]) for t in some]
     for b, t in enumerate(tokens):
         spoil(s, t, b, what, keys=False)
-    got = s.run(window, sinks, d_parents)
+    got = s.run(window, sinks, d_parents, hint=hint)
     for b, t in enumerate(tokens):
         n, see = sees[b].shape[0], sees[b][:, t]
         assert np.array_equal(got[0][b, :n][~see], clean[0][b, :n][~see])
@@ -101,25 +104,26 @@ def test_what_is_not_seen_does_not_count(case, what):
             assert (got[0][b, :n][see] == what).all()
     for b, t in enumerate(tokens):
         spoil(s, t, b, float("nan"), values=False)
-    got = s.run(window, sinks, d_parents)
+    got = s.run(window, sinks, d_parents, hint=hint)
     for b, t in enumerate(tokens):
         n, see = sees[b].shape[0], sees[b][:, t]
         for a, c in zip(got, clean):
             assert np.array_equal(a[b, :n][~see], c[b, :n][~see]) and np.isnan(a[b, :n][see]).all()
 
 
+@pytest.mark.parametrize("hint", [None, FAR])
 @pytest.mark.parametrize("what", [float("nan"), float("inf")])
 @pytest.mark.parametrize("q_len", [5, 100])
-def test_single_odd_elements(q_len, what):
+def test_single_odd_elements(q_len, what, hint):
     """One element of one value: the others of the row stay as they were."""
     g = gen(620)
     s = Setup(g, "bf16", "same", [300], None, q_len, 4, 2, 128, 16)
-    clean = s.run(64, 2)
+    clean = s.run(64, 2, hint=hint)
     see = ok.causal_sees(300, q_len, 64, 2)
     t = int(np.argwhere(see.any(0) & ~see.all(0))[3, 0])
     page, slot = int(s.table[s.rows[0], t // 16]), t % 16
     s.v[page, slot, 1, 77] = what
-    got = s.run(64, 2)
+    got = s.run(64, 2, hint=hint)
     at = np.zeros(clean[0].shape, bool)
     at[0, see[:, t], 2:, 77] = True                                      # of the heads that share the second one
     assert np.array_equal(got[0][~at], clean[0][~at]) and np.array_equal(got[1], clean[1])
@@ -127,12 +131,14 @@ def test_single_odd_elements(q_len, what):
 
 
 @pytest.mark.parametrize("scale", [-0.3, 0.0, 1e-30, 6.0])
+@pytest.mark.parametrize("hint", [None, FAR])
 @pytest.mark.parametrize("q_len", [2, 90])
-def test_scales(q_len, scale):
+def test_scales(q_len, scale, hint):
     s = Setup(gen(630), "f16", "same", [200, 90, 3], None, q_len, 4, 2, 64, 16)
-    s.check(40, 3, scale=scale)
+    s.check(40, 3, scale=scale, hint=hint)
+    s.check(0, 0, scale=scale, hint=hint)
     s = Setup(gen(631), "bf16", "int8", [200, 90], None, q_len, 4, 2, 64, 16)
-    s.check(40, 3, parents_of(gen(1), 2, q_len, "near"), scale=scale)
+    s.check(0, 0, parents_of(gen(1), 2, q_len, "near"), scale=scale, hint=hint)
 
 
 @pytest.mark.parametrize("window,sinks", [(2 ** 32 - 1, 5), (1 << 31, 2 ** 32 - 1), (5, 2 ** 32 - 1), (300, 1 << 31)])
@@ -161,16 +167,17 @@ def recorded():
     assert e.value.name == "ERR_PAGE"
 
 
+@pytest.mark.parametrize("hint", [None, FAR])
 @pytest.mark.parametrize("q_len", [2, 80])
-def test_out_of_range(q_len):
+def test_out_of_range(q_len, hint):
     """Rows, counts, lengths and pages out of range are recorded; the other sequences' results stay as they were."""
     s = Setup(gen(640), "bf16", "same", [90, 100, 200, 120, 130], [2] * 5, q_len, 4, 2, 64, 16)
-    clean = s.run(0, 0)
+    clean = s.run(0, 0, hint=hint)
     s.o.fill_(-3.0), s.lse.fill_(-3.0)
     s.d_rows[0] = 7                                                      # there are seven rows
     s.count[1] = q_len + 1
     s.count[3] = -1
-    got = s.run(0, 0)
+    got = s.run(0, 0, hint=hint)
     recorded()
     assert (got[0][0, :2] == 0).all() and np.isneginf(got[1][0, :2]).all()
     assert (got[0][[1, 3]] == -3.0).all() and (got[1][[1, 3]] == -3.0).all()
@@ -181,7 +188,7 @@ def test_out_of_range(q_len):
     s.lens[s.rows[1]] = 1 << 30
     s.lens[s.rows[2]] = -5
     s.table[s.rows[4], 2] = s.pages                                      # tokens 32 .. 47 are left out
-    got = s.run(0, 0)
+    got = s.run(0, 0, hint=hint)
     recorded()
     assert (got[0][2, :2] == 0).all() and np.isneginf(got[1][2, :2]).all()
     for a, c in zip(got, clean):
@@ -189,36 +196,38 @@ def test_out_of_range(q_len):
     assert np.isfinite(got[0][4, :2]).all() and not np.array_equal(got[0][4, :2], clean[0][4, :2])
 
 
+@pytest.mark.parametrize("hint", [None, FAR])
 @pytest.mark.parametrize("n", [9, 100])
-def test_trees_out_of_range(n):
+def test_trees_out_of_range(n, hint):
     g = gen(641)
     s = Setup(g, "f16", "same", [150, 200, 120], [n] * 3, n, 2, 1, 64, 16)
     parents = parents_of(g, 3, n, "near")
     good = parents.copy()
     good[0, 3], good[1, 5] = -1, -1
-    want = s.run(0, 0, ints(good))
+    want = s.run(0, 0, ints(good), hint=hint)
     bad = parents.copy()
     bad[0, 3], bad[1, 5] = 3, -2                                         # itself, and no node
-    got = s.run(0, 0, ints(bad))
+    got = s.run(0, 0, ints(bad), hint=hint)
     recorded()
     assert all(np.array_equal(a, b) for a, b in zip(got, want))
     bad[0, 3], bad[1, 5] = 2 ** 31 - 1, -2 ** 31
-    got = s.run(0, 0, ints(bad))
+    got = s.run(0, 0, ints(bad), hint=hint)
     recorded()
     assert all(np.array_equal(a, b) for a, b in zip(got, want))
     s.lens[s.rows[2]] = n - 1                                            # a row shorter than its tree
-    got = s.run(0, 0, ints(good))
+    got = s.run(0, 0, ints(good), hint=hint)
     recorded()
     assert (got[0][2] == 0).all() and np.isneginf(got[1][2]).all()
     assert np.array_equal(got[0][:2], want[0][:2])
 
 
+@pytest.mark.parametrize("q_len,hint", [(3, None), (70, FAR)])
 @pytest.mark.parametrize("fmt", ["same", "e4m3"])
-def test_offsets_beyond_32_bits(fmt):
+def test_offsets_beyond_32_bits(fmt, q_len, hint):
     """Pages that lie more than 4 GiB behind the pool's start."""
     g = gen(650)
-    s = Setup(g, "bf16", fmt, [100, 60], None, 3, 2, 1, 128, 16)
-    clean = s.run(40, 4)
+    s = Setup(g, "bf16", fmt, [100, 70], None, q_len, 2, 1, 128, 16)
+    clean = s.run(0, 0, hint=hint)
     page_bytes = s.k[0].numel() * s.k.element_size()
     pages = (9 << 29) // page_bytes + s.pages
     for name in "kv":
@@ -228,7 +237,7 @@ def test_offsets_beyond_32_bits(fmt):
         setattr(s, name, big)
     s.table.copy_(torch.where(s.table >= 0, s.table + (pages - s.pages), s.table))
     s.pt = att.page_table(s.table, s.lens, None, pages, s.slots)
-    got = s.run(40, 4)
+    got = s.run(0, 0, hint=hint)
     assert all(np.array_equal(a, b) for a, b in zip(got, clean))
 
 
@@ -302,16 +311,17 @@ def test_two_streams_at_once():
         assert np.array_equal(f64(s.o), w[0]) and np.array_equal(f64(s.lse), w[1])
 
 
-def test_results_do_not_depend_on_the_batch():
+@pytest.mark.parametrize("window,sinks,hint", [(300, 2, 300), (0, 0, FAR)])
+def test_results_do_not_depend_on_the_batch(window, sinks, hint):
     """A sequence's result is the same alone and beside others, run after run."""
     g = gen(662)
     s = Setup(g, "bf16", "same", [900, 50, 400], [100, 20, 64], 100, 4, 2, 128, 16)
-    first = s.run(300, 2, hint=300)
+    first = s.run(window, sinks, hint=hint)
     for _ in range(3):
-        again = s.run(300, 2, hint=300)
+        again = s.run(window, sinks, hint=hint)
         assert all(np.array_equal(a, b) for a, b in zip(first, again))
     s.count[0] = 0
     s.o.fill_(-3.0), s.lse.fill_(-3.0)
-    got = s.run(300, 2, hint=300)
+    got = s.run(window, sinks, hint=hint)
     assert (got[0][0] == -3.0).all()
     assert all(np.array_equal(a[1:], b[1:]) for a, b in zip(got, first))
