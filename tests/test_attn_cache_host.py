@@ -10,18 +10,21 @@ from test_kv8_host import codes
 from test_kvcache_host import BASE, pool, queries, refused, table
 
 
-def window(q=queries(), kp=pool(), vp=None, fmt="same", pt=table(), rows=0, count=0, window=0, sinks=0, hint=64,
-           scale=0.1, o=None, lse=0, ws=BASE, n=None):
-    vp = kp if vp is None else vp
-    o = queries() if o is None else o
+NONE = object()          # an argument that is left out: a module loads no library
+
+
+def window(q=NONE, kp=NONE, vp=None, fmt="same", pt=None, rows=0, count=0, window=0, sinks=0, hint=64, scale=0.1, o=None,
+           lse=0, ws=BASE, n=None):
+    q, kp = queries() if q is NONE else q, pool() if kp is NONE else kp
+    vp, pt, o = kp if vp is None else vp, pt or table(), queries() if o is None else o
     if n is None:
         n = max(16, att.attn_cache_workspace(q, kp, window, sinks, hint)) if q and kp else 16
     return lambda: att.attn_window(q, kp, vp, fmt, pt, rows, count, window, sinks, hint, scale, o, lse, ws, 0, n)
 
 
-def tree(q=queries(q_len=5), kp=pool(), fmt="same", pt=table(), parent=BASE, hint=64, o=None, ws=BASE, n=1 << 40):
-    o = q if o is None else o
-    return lambda: att.attn_tree(q, kp, kp, fmt, pt, 0, 0, parent, 0, 0, hint, 0.1, o, 0, ws, 0, n)
+def tree(q=None, kp=None, fmt="same", pt=None, parent=BASE, hint=64, ws=BASE, n=1 << 40):
+    q, kp, pt = q or queries(q_len=5), kp or pool(), pt or table()
+    return lambda: att.attn_tree(q, kp, kp, fmt, pt, 0, 0, parent, 0, 0, hint, 0.1, q, 0, ws, 0, n)
 
 
 def test_window_refusals():
