@@ -595,90 +595,140 @@ typedef TokensOf<kFewPools> FewTokens;
 constexpr uint32_t kKeepThreads = 128;
 constexpr uint32_t kKeepTokens = 128;     // tokens whose places are worked out together
 
+// Entry i as the device's arrays say it is.
+struct KeepEntry {
+    uint32_t row;
+    int64_t first, count, len;
+    const int32_t* entries;      // the row's pages
+    const int32_t* kept;
+    bool good;
+};
+
+__device__ __forceinline__ KeepEntry keep_entry(const Table& t, const int32_t* rows, const int32_t* from,
+                                                const int32_t* keep, uint32_t width, const int32_t* count, uint32_t i,
+                                                bool record, uint32_t* err) {
+    KeepEntry e;
+    e.row = (uint32_t)rows[i];
+    e.first = from[i];
+    e.count = count[i];
+    e.len = -1;
+    const int64_t room = (int64_t)t.slots * t.row_pages;
+    if (e.row < t.rows) e.len = t.lens[e.row];
+    const bool there = e.len >= 0 && e.len <= room;
+    if (!there && record) record_page_error(err);
+    e.good = there && e.first >= 0 && e.first <= e.len && e.count >= 0 && e.count <= (int64_t)width;
+    e.entries = t.table + (uint64_t)e.row * t.pitch;
+    e.kept = keep + (uint64_t)i * width;
+    return e;
+}
+
+// Whether kept token j ascends, is there, and moves between pages that may be used.
+__device__ __forceinline__ bool may_move(const Table& t, const KeepEntry& e, uint32_t j, uint32_t* err) {
+    const int64_t k = e.kept[j], before = j ? e.kept[j - 1] : -1;
+    if (k <= before || e.first + k >= e.len) return false;
+    if (k == (int64_t)j) return true;
+    const int32_t a = e.entries[(uint32_t)(e.first + k) / t.slots], b = e.entries[(uint32_t)(e.first + j) / t.slots];
+    if ((uint32_t)a >= t.pages || (uint32_t)b >= t.pages) {
+        record_page_error(err);
+        return false;
+    }
+    return t.refs[b] <= 1;
+}
+
+// Where a kept token comes from and goes to in a pool.  src < 0: it stays.
+struct Move {
+    int64_t src, dst, src_scale, dst_scale;
+};
+
+template <uint32_t N>
+__device__ __forceinline__ Move move_of(const Table& t, const TokensOf<N>& p, const KeepEntry& e, uint32_t j) {
+    Move m = {-1, -1, -1, -1};
+    const uint32_t k = (uint32_t)e.kept[j];
+    if (k == j) return m;
+    const uint32_t from_at = (uint32_t)e.first + k, to_at = (uint32_t)e.first + j;
+    const uint32_t from_slot = from_at % t.slots, to_slot = to_at % t.slots;
+    const int64_t a = e.entries[from_at / t.slots] * p.page, b = e.entries[to_at / t.slots] * p.page;
+    m.src = a + (int64_t)from_slot * p.slot;
+    m.dst = b + (int64_t)to_slot * p.slot;
+    if (p.codes) {
+        m.src_scale = a + scale_offset(from_slot, t.slots, p.dim, p.slot);
+        m.dst_scale = b + scale_offset(to_slot, t.slots, p.dim, p.slot);
+    }
+    return m;
+}
+
+// Pieces of a token: the 16-byte chunks of each head, then each head's scale.
+template <uint32_t N>
+__device__ __forceinline__ uint32_t pieces_of(const TokensOf<N>& p) {
+    return p.heads * ((p.bytes + 15u) / 16u) + (p.codes ? p.heads : 0u);
+}
+
+// Piece u of n tokens, in their order.  Kept tokens ascend, so token j comes from
+// index j or above: a thread that moves its piece of each in turn, a few loads
+// ahead, never reads what it wrote.
+template <uint32_t N>
+__device__ __forceinline__ void move_piece(const TokensOf<N>& p, gbyte* pool, uint32_t u, const Move* moves, uint32_t n) {
+    const uint32_t chunks = (p.bytes + 15u) / 16u, data = p.heads * chunks;
+    const bool scale = u >= data;
+    const uint32_t h = scale ? u - data : u / chunks, c = scale ? 0u : u - h * chunks;
+    const int64_t off = (int64_t)h * p.head + c * 16u;
+    const uint32_t left = scale ? 2u : p.bytes - c * 16u < 16u ? p.bytes - c * 16u : 16u;
+    constexpr uint32_t U = 8;                                           // loads in flight
+    for (uint32_t j = 0; j < n; j += U) {
+        u32x4 v[U];
+        uint16_t s[U];
+#pragma unroll
+        for (uint32_t x = 0; x < U; ++x) {
+            if (j + x >= n || moves[j + x].src < 0) continue;
+            if (scale) s[x] = *(const ATT_GLOBAL uint16_t*)(pool + moves[j + x].src_scale + off);
+            else if (left == 16u) v[x] = *(const ATT_GLOBAL u32x4*)(pool + moves[j + x].src + off);
+        }
+#pragma unroll
+        for (uint32_t x = 0; x < U; ++x) {
+            if (j + x >= n || moves[j + x].src < 0) continue;
+            if (scale) *(ATT_GLOBAL uint16_t*)(pool + moves[j + x].dst_scale + off) = s[x];
+            else if (left == 16u) *(ATT_GLOBAL u32x4*)(pool + moves[j + x].dst + off) = v[x];
+            else for (uint32_t e = 0; e < left; ++e) pool[moves[j + x].dst + off + e] = pool[moves[j + x].src + off + e];
+        }
+    }
+}
+
+// A row ends at token `end`, and gives back the pages between that and its old end.
+__device__ __forceinline__ void end_row(const Table& t, uint32_t row, uint32_t len, uint32_t end, uint32_t lane,
+                                        uint32_t* err) {
+    const uint32_t c0 = (end + t.slots - 1u) / t.slots, c1 = (len + t.slots - 1u) / t.slots;
+    int32_t* const entries = t.table + (uint64_t)row * t.pitch;
+    for (uint32_t c = c0 + lane; c < c1; c += 64u) {
+        const int32_t page = entries[c];
+        entries[c] = -1;
+        if ((uint32_t)page < t.pages) atomicSub(&t.refs[page], 1);
+        else record_page_error(err);
+    }
+    if (lane == 0) t.lens[row] = (int32_t)end;
+}
+
 // Entry i and one pool: the checks, the same in every workgroup of the entry and
-// all on what no workgroup of this launch changes, then the moves.  Kept tokens
-// ascend, so token j comes from index j or above: a thread that moves its piece
-// of each token in their order, a few loads ahead, never reads what it wrote.
+// all on what no workgroup of this launch changes, then the moves.
 template <uint32_t N>
 __global__ __launch_bounds__(kKeepThreads) void k_page_keep(const Table t, const TokensOf<N> p, const int32_t* rows,
                                                             const int32_t* from, const int32_t* keep, uint32_t width,
                                                             const int32_t* count, int32_t* ok, uint32_t* err) {
-    __shared__ int64_t src[kKeepTokens], dst[kKeepTokens];              // of the tokens; -1: stays where it is
-    __shared__ int64_t src_scale[kKeepTokens], dst_scale[kKeepTokens];
+    __shared__ Move moves[kKeepTokens];
     const uint32_t tid = threadIdx.x, i = blockIdx.x;
-    const uint32_t row = (uint32_t)rows[i];
-    const int64_t first = from[i], n = count[i], room = (int64_t)t.slots * t.row_pages;
-    const int32_t* kept = keep + (uint64_t)i * width;
-    int64_t len = -1;
-    if (row < t.rows) len = t.lens[row];
-    if ((len < 0 || len > room) && tid == 0 && blockIdx.y == 0) record_page_error(err);
-    bool good = len >= 0 && len <= room && first >= 0 && first <= len && n >= 0 && n <= (int64_t)width;
-    const int32_t* entries = t.table + (uint64_t)row * t.pitch;
-    if (good) {
-        for (uint32_t j = tid; j < (uint32_t)n; j += kKeepThreads) {
-            const int64_t k = kept[j], before = j ? kept[j - 1] : -1;
-            if (k <= before || first + k >= len) {
-                good = false;
-                break;
-            }
-            if (k == (int64_t)j) continue;
-            const int32_t a = entries[(uint32_t)(first + k) / t.slots], b = entries[(uint32_t)(first + j) / t.slots];
-            if ((uint32_t)a >= t.pages || (uint32_t)b >= t.pages) {
-                record_page_error(err);
-                good = false;
-            } else if (t.refs[b] > 1) {
-                good = false;
-            }
-        }
-    }
+    const KeepEntry e = keep_entry(t, rows, from, keep, width, count, i, tid == 0 && blockIdx.y == 0, err);
+    bool good = e.good;
+    if (good)
+        for (uint32_t j = tid; j < (uint32_t)e.count && good; j += kKeepThreads) good = may_move(t, e, j, err);
     good = __syncthreads_and(good);
     if (blockIdx.y == 0 && tid == 0) ok[i] = good;
     if (!good || p.npool == 0) return;
-    gbyte* const pool = gptr(p.base[blockIdx.y]);
-    const uint32_t chunks = (p.bytes + 15u) / 16u, pieces = p.heads * chunks, units = pieces + (p.codes ? p.heads : 0u);
-    for (uint32_t j0 = 0; j0 < (uint32_t)n; j0 += kKeepTokens) {
-        const uint32_t m = (uint32_t)n - j0 < kKeepTokens ? (uint32_t)n - j0 : kKeepTokens;
+    const uint32_t units = pieces_of(p);
+    for (uint32_t j0 = 0; j0 < (uint32_t)e.count; j0 += kKeepTokens) {
+        const uint32_t m = (uint32_t)e.count - j0 < kKeepTokens ? (uint32_t)e.count - j0 : kKeepTokens;
         if (j0) __syncthreads();                                        // the places before are used
-        if (tid < m) {
-            const uint32_t j = j0 + tid, k = (uint32_t)kept[j];
-            src[tid] = dst[tid] = -1;
-            if (k != j) {
-                const uint32_t from_at = (uint32_t)first + k, to_at = (uint32_t)first + j;
-                const uint32_t from_slot = from_at % t.slots, to_slot = to_at % t.slots;
-                const int64_t a = entries[from_at / t.slots] * p.page, b = entries[to_at / t.slots] * p.page;
-                src[tid] = a + (int64_t)from_slot * p.slot;
-                dst[tid] = b + (int64_t)to_slot * p.slot;
-                if (p.codes) {
-                    src_scale[tid] = a + scale_offset(from_slot, t.slots, p.dim, p.slot);
-                    dst_scale[tid] = b + scale_offset(to_slot, t.slots, p.dim, p.slot);
-                }
-            }
-        }
+        if (tid < m) moves[tid] = move_of(t, p, e, j0 + tid);
         __syncthreads();
-        for (uint32_t u = tid; u < units; u += kKeepThreads) {
-            const bool scale = u >= pieces;
-            const uint32_t h = scale ? u - pieces : u / chunks, c = scale ? 0u : u - h * chunks;
-            const int64_t off = (int64_t)h * p.head + c * 16u;
-            const uint32_t left = scale ? 2u : p.bytes - c * 16u < 16u ? p.bytes - c * 16u : 16u;
-            constexpr uint32_t U = 8;                                   // loads in flight
-            for (uint32_t j = 0; j < m; j += U) {
-                u32x4 v[U];
-                uint16_t s[U];
-#pragma unroll
-                for (uint32_t x = 0; x < U; ++x) {
-                    if (j + x >= m || src[j + x] < 0) continue;
-                    if (scale) s[x] = *(const ATT_GLOBAL uint16_t*)(pool + src_scale[j + x] + off);
-                    else if (left == 16u) v[x] = *(const ATT_GLOBAL u32x4*)(pool + src[j + x] + off);
-                }
-#pragma unroll
-                for (uint32_t x = 0; x < U; ++x) {
-                    if (j + x >= m || src[j + x] < 0) continue;
-                    if (scale) *(ATT_GLOBAL uint16_t*)(pool + dst_scale[j + x] + off) = s[x];
-                    else if (left == 16u) *(ATT_GLOBAL u32x4*)(pool + dst[j + x] + off) = v[x];
-                    else for (uint32_t e = 0; e < left; ++e) pool[dst[j + x] + off + e] = pool[src[j + x] + off + e];
-                }
-            }
-        }
+        for (uint32_t u = tid; u < units; u += kKeepThreads) move_piece(p, gptr(p.base[blockIdx.y]), u, moves, m);
     }
 }
 
@@ -687,16 +737,45 @@ __global__ __launch_bounds__(64) void k_page_end(const Table t, const int32_t* r
                                                  const int32_t* count, const int32_t* ok, uint32_t* err) {
     const uint32_t i = blockIdx.x;
     if (!ok[i]) return;
-    const uint32_t row = (uint32_t)rows[i], len = (uint32_t)t.lens[row], end = (uint32_t)from[i] + (uint32_t)count[i];
-    const uint32_t c0 = (end + t.slots - 1u) / t.slots, c1 = (len + t.slots - 1u) / t.slots;
-    int32_t* const entries = t.table + (uint64_t)row * t.pitch;
-    for (uint32_t c = c0 + threadIdx.x; c < c1; c += 64u) {
-        const int32_t page = entries[c];
-        entries[c] = -1;
-        if ((uint32_t)page < t.pages) atomicSub(&t.refs[page], 1);
-        else record_page_error(err);
+    const uint32_t row = (uint32_t)rows[i];
+    end_row(t, row, (uint32_t)t.lens[row], (uint32_t)from[i] + (uint32_t)count[i], threadIdx.x, err);
+}
+
+// A few entries and little data by one workgroup, in one launch: all checks, all
+// moves, then the ends.
+constexpr uint32_t kOneKeepThreads = 512;
+constexpr uint32_t kOneKeepTokens = 512;  // kept indices of all entries together
+template <uint32_t N>
+__global__ __launch_bounds__(kOneKeepThreads) void k_page_keep_one(const Table t, const TokensOf<N> p, const int32_t* rows,
+                                                                   const int32_t* from, const int32_t* keep,
+                                                                   uint32_t width, const int32_t* count, uint32_t n,
+                                                                   int32_t* ok, uint32_t* err) {
+    __shared__ Move moves[kOneKeepTokens];
+    __shared__ int32_t tokens[kOneKeepThreads / 64u];                   // that an entry moves, -1: not served
+    const uint32_t tid = threadIdx.x, lane = lane_id(), i = tid / 64u;  // a wave an entry
+    KeepEntry e;
+    bool good = false;
+    if (i < n) {
+        e = keep_entry(t, rows, from, keep, width, count, i, lane == 0, err);
+        good = e.good;
+        if (good)
+            for (uint32_t j = lane; j < (uint32_t)e.count && good; j += 64u) good = may_move(t, e, j, err);
+        good = __all(good);
+        if (good && p.npool)
+            for (uint32_t j = lane; j < (uint32_t)e.count; j += 64u) moves[i * width + j] = move_of(t, p, e, j);
+        if (lane == 0) {
+            ok[i] = good;
+            tokens[i] = good ? (int32_t)e.count : -1;
+        }
     }
-    if (threadIdx.x == 0) t.lens[row] = (int32_t)end;
+    __syncthreads();
+    const uint32_t units = pieces_of(p), all = n * p.npool * units;
+    for (uint32_t x = tid; x < all; x += kOneKeepThreads) {
+        const uint32_t y = x / units, entry = y / p.npool;
+        if (tokens[entry] > 0)
+            move_piece(p, gptr(p.base[y - entry * p.npool]), x - y * units, moves + entry * width, (uint32_t)tokens[entry]);
+    }
+    if (good) end_row(t, e.row, (uint32_t)e.len, (uint32_t)(e.first + e.count), lane, err);
 }
 
 // ---- host ------------------------------------------------------------------------
@@ -1011,6 +1090,15 @@ extern "C" tmap_status page_keep(const page_table_t* pt, const tmap_t* pools, ui
     if (st) return st;
     const hipStream_t s = as_stream(stream);
     const Table t = table_of(pt);
+    // Little to move: one launch (page_extend and page_keep of 8 entries of 8 tokens, 4
+    // pools of 8 heads: 15.4 us in a row, 17.1 in two launches; 1 entry, 16 pools: 13.9, 17.2).
+    const uint64_t pieces = npool ? (uint64_t)npool * (p.heads * ((p.bytes + 15ull) / 16) + (p.codes ? p.heads : 0)) : 0;
+    if (n <= kOneKeepThreads / 64 && (uint64_t)n * width <= kOneKeepTokens && n * pieces <= 4 * kOneKeepThreads &&
+        npool <= kFewPools) {
+        hipLaunchKernelGGL(k_page_keep_one, dim3(1), dim3(kOneKeepThreads), 0, s, t, few_tokens, d_rows, d_from, d_keep,
+                           width, d_count, n, d_ok, err);
+        return check_launch("page_keep");
+    }
     constexpr uint32_t most = max_groups(kKeepThreads);
     for (uint32_t i = 0, m = 0; i < n; i += m) {
         m = n - i < most ? n - i : most;
