@@ -533,14 +533,16 @@ __device__ __forceinline__ void tall_part(cargs& a, Shared<DP, FMT>& sh, const J
         if (tid == 0) sh.odd[(t + 1u) % 3u] = 0u;
     };
     if (CODES) {
-        kcode.load(tid, dim, sh.kaddr + in(0));
-        vcode.load(tid, dim, sh.vaddr + in(0));
-        kcode.template store<false>(tid, nullptr, keys(0));
-        vcode.template store<!WEIGHTS>(tid, sh.vscale + in(0), vals(0));
-        kcode.load(tid, dim, sh.kaddr + in(1));
-        kcode.template store<false>(tid, nullptr, keys(1));
+        auto kfirst = kcode, ksecond = kcode;                             // all on their way together
+        auto vfirst = vcode;
+        kfirst.load(tid, dim, sh.kaddr + in(0));
+        vfirst.load(tid, dim, sh.vaddr + in(0));
+        ksecond.load(tid, dim, sh.kaddr + in(1));
         kcode.load(tid, dim, sh.kaddr + in(2));
         vcode.load(tid, dim, sh.vaddr + in(1));
+        kfirst.template store<false>(tid, nullptr, keys(0));
+        vfirst.template store<!WEIGHTS>(tid, sh.vscale + in(0), vals(0));
+        ksecond.template store<false>(tid, nullptr, keys(1));
     } else if (tiles) {
         copy_k(sh.kaddr + in(0), keys(0));
         copy_k(sh.kaddr + in(1), keys(1));
