@@ -111,9 +111,10 @@ static uint64_t plan(CacheArgs* a, uint32_t hint, bool codes) {
     // Parts of 256 keys and above, of 128 while they leave compute units without one
     // (2 trees of 13 nodes of 700 tokens: 14.3 us, in parts of 256 15.7; 1 x 60 nodes of
     // 4000 tokens 27.9 and 23.9).  Few keys in one part: no second launch (512 keys of 64
-    // elements 10.4 us, 12.3 in two parts; 128 rows with 400 keys 21.7 and 16.4).
+    // elements 10.4 us, 12.3 in two parts; 128 rows with 400 keys 21.7 and 16.4; 777
+    // queries, window 300, 40 heads: 20.5 in one part, 27.6 in two).
     uint64_t parts = 1;
-    if (keys > (a->waves ? 256u : 512u)) {
+    if (keys > (!a->waves ? 512u : a->window && jobs * a->waves > 256 ? 1024u : 256u)) {
         const auto least = [](uint64_t x, uint64_t y) { return x < y ? x : y; };
         const auto larger = [](uint64_t x, uint64_t y) { return x < y ? y : x; };
         parts = larger(least(ceil_div(keys, 256), room / jobs), least(ceil_div(keys, 128), cus / jobs));
