@@ -17,8 +17,10 @@
 //
 // Codes.  Keys go to the matrix cores as they are (a code is exact in 16 bits)
 // and the fp32 scores are multiplied by the keys' scales.  So do values for bf16,
-// whose scales multiply the fp32 weights before their rounding; for f16 a value is
-// its code times its scale, rounded, as a 16-bit cache would hold it.
+// whose scales multiply the fp32 weights before their rounding.  f16 has no room for
+// a weight times any scale: there the power of two in the scale goes to the code,
+// exactly, and the rest of it to the weight.  Either way a weight is rounded once
+// and a value not at all.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -167,7 +169,8 @@ struct Shared {                       // of many rows
     uint64_t vaddr[2 * kSegment];
     uint64_t there[2 * kSegment / 64];
     float kscale[FMT == KV_SAME ? 4 : 2 * kSegment];
-    float vscale[FMT == KV_SAME ? 4 : 2 * kSegment];
+    float vscale[FMT == KV_SAME ? 4 : 2 * kSegment];   // for the weights
+    uint16_t vpower[FMT == KV_SAME ? 4 : 2 * kSegment];   // for the codes, as bf16
     uint32_t odd[4];                  // whether a tile's values hold infinities or NaN
     uint16_t parent[kMaxNodes];       // of each node, 0xFFFF: the context
 };
@@ -179,6 +182,7 @@ struct ShortShared {                  // of few rows
     uint8_t ring[Geo<DP>::ring_bytes];
     uint64_t addr[kWaves][2][2 * kOwnTile];   // of a wave's tiles: the keys' rows in the pools, the values'
     float scale[kWaves][2][FMT == KV_SAME ? 4 : 2 * kOwnTile];
+    uint16_t vpower[kWaves][2][FMT == KV_SAME ? 4 : kOwnTile];
     int32_t page[kPages];
     uint16_t parent[kMaxNodes];
 };
@@ -251,9 +255,9 @@ __device__ __forceinline__ int32_t page_of_key(cargs& a, const Span& x, uint32_t
     return *(const ATT_GLOBAL int32_t*)(gptr(a.table) + ((uint64_t)row * a.pitch + column_of(a, (uint32_t)t)) * 4u);
 }
 
-// Then its addresses, and where its scales lie.
+// Then its addresses, and its scales are asked for.
 struct Scales {
-    uint64_t k, v;                    // 0: no such key
+    uint16_t k, v;                    // as bf16, 0 where there is no such key
 };
 template <uint32_t TILE, uint32_t DP, int FMT>
 __device__ __forceinline__ Scales place_key(cargs& a, const Span& x, uint32_t head, uint32_t i, uint32_t end,
@@ -270,19 +274,29 @@ __device__ __forceinline__ Scales place_key(cargs& a, const Span& x, uint32_t he
     if (at % 64u == 0) sh.there[at / 64u] = mask;
     Scales s = {0, 0};
     if (FMT != KV_SAME && ok) {
-        s.k = kh + (uint64_t)scale_offset(slot, a.slots, a.dim, a.k.stride[1]);
-        s.v = vh + (uint64_t)scale_offset(slot, a.slots, a.dim, a.v.stride[1]);
+        s.k = *(const ATT_GLOBAL uint16_t*)(kh + (uint64_t)scale_offset(slot, a.slots, a.dim, a.k.stride[1]));
+        s.v = *(const ATT_GLOBAL uint16_t*)(vh + (uint64_t)scale_offset(slot, a.slots, a.dim, a.v.stride[1]));
     }
     return s;
 }
 
-__device__ __forceinline__ uint32_t scale_bits(uint64_t at) {
-    return at ? (uint32_t)*(const ATT_GLOBAL uint16_t*)at << 16 : 0u;
+__device__ __forceinline__ float scale_value(uint16_t bits) { return __builtin_bit_cast(float, (uint32_t)bits << 16); }
+
+// A scale as the weights' share times the codes' share.  SPLIT: of a normal one the
+// codes get the sign and the power of two, the weights 1 .. 2; 0, infinities and NaN
+// go to the codes whole.  Else the weights get all of it.
+template <bool SPLIT>
+__device__ __forceinline__ void split_scale(uint16_t bits, float* weights, uint16_t* codes) {
+    const uint32_t power = bits & 0x7F80u;
+    const bool normal = power != 0u && power != 0x7F80u;
+    *weights = !SPLIT ? scale_value(bits) : normal ? scale_value((uint16_t)((bits & 0x007Fu) | 0x3F80u)) : 1.0f;
+    if (SPLIT) *codes = normal ? (uint16_t)(bits & 0xFF80u) : bits;
 }
 
 // ---- codes ------------------------------------------------------------------------
 
-// 16 codes as elements: two chunks of 8.  SCALED: times a scale, rounded once.
+// 16 codes as elements: two chunks of 8.  SCALED: times a power of two, which rounds
+// only what is below the type's normal numbers, as a 16-bit cache's elements are.
 template <typename T, int FMT, bool SCALED>
 __device__ __forceinline__ void elements_of(u32x4 code, float scale, typename Vec<T>::v8 (&y)[2]) {
     constexpr bool F16 = std::is_same<T, _Float16>::value;
@@ -352,15 +366,15 @@ struct CodeCopy {
         if (dim == DP) each(std::true_type{});
         else each(std::false_type{});
     }
-    // scales: of the rows, for values that take theirs here.
+    // powers: of the rows, for values that take theirs here.
     template <bool SCALED>
-    __device__ __forceinline__ void store(uint32_t thread, const float* scales, uint8_t* tile) const {
+    __device__ __forceinline__ void store(uint32_t thread, const uint16_t* powers, uint8_t* tile) const {
 #pragma unroll
         for (uint32_t n = 0; n < N; ++n) {
             const uint32_t i = n * THREADS + thread, row = i / cpr, c = i - row * cpr;
             if (!whole && i >= ROWS * cpr) break;
             typename Vec<T>::v8 y[2];
-            elements_of<T, FMT, SCALED>(raw[n], SCALED ? scales[row] : 1.0f, y);
+            elements_of<T, FMT, SCALED>(raw[n], SCALED ? scale_value(powers[row]) : 1.0f, y);
             const uint32_t key = VALUES ? Geo<DP>::key_v(row) : Geo<DP>::key_k(row);
             uint8_t* at = tile + row * (DP * 2u);
             *reinterpret_cast<typename Vec<T>::v8*>(at + ((2u * c) ^ key) * 16u) = y[0];
@@ -371,9 +385,12 @@ struct CodeCopy {
 
 // Where the values' scales go.  bf16 holds a weight times any of them: the codes
 // go to the product as they are.  f16 does not (a weight of 2^-10 times a scale of
-// 2^-17), so there a value is its code times its scale, rounded.
+// 2^-17): split.  (2048 queries of 32768 int8 tokens 1240 us; with values that are
+// their code times their scale, rounded, 1230, and the result is off by 1.7 times its
+// last rounding, not 1.4.  Weights in units of the largest scale: 1277, a token each of
+// 64 sequences, window 8192, 258 for 241.)
 template <typename T>
-constexpr bool kScaledWeights = std::is_same<T, __bf16>::value;
+constexpr bool kSplitScales = !std::is_same<T, __bf16>::value;
 
 // Weights times their values' scales; a key that the row does not see (MASKED: a
 // bit of `sees` each) has no weight, whatever its scale.
@@ -474,8 +491,8 @@ __device__ __forceinline__ void tall_part(cargs& a, Shared<DP, FMT>& sh, const J
     static_assert(FMT != KV_SAME || Geo<DP>::cpr % WAVES == 0, "every wave copies as many");
     // The threads that place the keys of a segment, one each.
     const bool places = THREADS == kSegment || tid < kSegment;
-    constexpr bool CODES = FMT != KV_SAME, WEIGHTS = CODES && kScaledWeights<T>;
-    Wave<T, DP> w;
+    constexpr bool CODES = FMT != KV_SAME, SPLIT = CODES && kSplitScales<T>;
+    Wave<T, DP, CODES> w;
     w.load_row(a, row.q, row.valid);
     int32_t page = -1;
     Scales scales = {0, 0};
@@ -484,8 +501,8 @@ __device__ __forceinline__ void tall_part(cargs& a, Shared<DP, FMT>& sh, const J
         scales = place_key<kTile, DP, FMT>(a, x, job.head, k0 + tid, k1, page, sh, tid);
     }
     if (CODES && places) {
-        sh.kscale[tid] = __builtin_bit_cast(float, scale_bits(scales.k));
-        sh.vscale[tid] = __builtin_bit_cast(float, scale_bits(scales.v));
+        sh.kscale[tid] = scale_value(scales.k);
+        split_scale<SPLIT>(scales.v, &sh.vscale[tid], &sh.vpower[tid]);
         page = page_of_key<kTile>(a, x, job.seq.row, k0 + kSegment + tid, k1);
     }
     if (tid < 4u) sh.odd[tid] = 0u;
@@ -514,7 +531,7 @@ __device__ __forceinline__ void tall_part(cargs& a, Shared<DP, FMT>& sh, const J
         wait_lgkm0();
         wg_barrier();
     };
-    // Addresses of the next segment's keys: pages a step ahead, scales a step behind.
+    // Addresses of the next segment's keys: pages a step ahead.
     // Codes are asked for a tile earlier, so they are placed a step earlier.
     constexpr uint32_t PLACE = CODES ? 0u : 1u, FETCH = CODES ? SEG - 1u : 0u, AHEAD = CODES ? 2u : 1u;
     auto begin = [&](uint32_t t) {
@@ -525,8 +542,8 @@ __device__ __forceinline__ void tall_part(cargs& a, Shared<DP, FMT>& sh, const J
         }
         if (CODES && t % SEG == 1u && places) {
             const uint32_t at = ((t / SEG + 1u) & 1u) * kSegment + tid;
-            sh.kscale[at] = __builtin_bit_cast(float, scale_bits(scales.k));
-            sh.vscale[at] = __builtin_bit_cast(float, scale_bits(scales.v));
+            sh.kscale[at] = scale_value(scales.k);
+            split_scale<SPLIT>(scales.v, &sh.vscale[at], &sh.vpower[at]);
         }
         if (t % SEG == FETCH && places)
             page = page_of_key<kTile>(fresh(), x, job.seq.row, k0 + (t / SEG + AHEAD) * kSegment + tid, k1);
@@ -541,7 +558,7 @@ __device__ __forceinline__ void tall_part(cargs& a, Shared<DP, FMT>& sh, const J
         kcode.load(tid, dim, sh.kaddr + in(2));
         vcode.load(tid, dim, sh.vaddr + in(1));
         kfirst.template store<false>(tid, nullptr, keys(0));
-        vfirst.template store<!WEIGHTS>(tid, sh.vscale + in(0), vals(0));
+        vfirst.template store<SPLIT>(tid, sh.vpower + in(0), vals(0));
         ksecond.template store<false>(tid, nullptr, keys(1));
     } else if (tiles) {
         copy_k(sh.kaddr + in(0), keys(0));
@@ -554,7 +571,7 @@ __device__ __forceinline__ void tall_part(cargs& a, Shared<DP, FMT>& sh, const J
     auto fill = [&](uint32_t t) {
         if (CODES) {
             kcode.template store<false>(tid, nullptr, keys(t));
-            vcode.template store<!WEIGHTS>(tid, sh.vscale + in(t + 1u), vals(t + 1u));
+            vcode.template store<SPLIT>(tid, sh.vpower + in(t + 1u), vals(t + 1u));
             kcode.load(tid, dim, sh.kaddr + in(t + 3u));
             vcode.load(tid, dim, sh.vaddr + in(t + 2u));
         } else {
@@ -579,7 +596,7 @@ __device__ __forceinline__ void tall_part(cargs& a, Shared<DP, FMT>& sh, const J
     // whole are added to the rows that see them, and are 0 for the product.
     auto odd_values = [&](uint32_t t, const f32x16 (&p)[2]) {
         uint8_t* const v = vals(t);
-        const bool odd = Wave<T, DP>::template odd_share<false>(v, wave, WAVES, kTile);
+        const bool odd = Wave<T, DP, CODES>::template odd_share<false>(v, wave, WAVES, kTile);
         if (odd && lane == 0) sh.odd[t % 3u] = 1u;
         wait_lgkm0();
         wg_barrier();
@@ -587,7 +604,7 @@ __device__ __forceinline__ void tall_part(cargs& a, Shared<DP, FMT>& sh, const J
         if (busy) w.template add_odd<2>(v, p, seen);
         wait_lgkm0();
         wg_barrier();
-        Wave<T, DP>::template odd_share<true>(v, wave, WAVES, kTile);
+        Wave<T, DP, CODES>::template odd_share<true>(v, wave, WAVES, kTile);
         wait_lgkm0();
         wg_barrier();
     };
@@ -595,7 +612,7 @@ __device__ __forceinline__ void tall_part(cargs& a, Shared<DP, FMT>& sh, const J
         begin(t);
         fill(t);
         if (!busy) return;
-        top = w.template advance<CODES, WEIGHTS, true>(scale, keys(t + 1u), vals(t), top, y, next, sh.kscale + in(t + 1u),
+        top = w.template advance<CODES, CODES, true>(scale, keys(t + 1u), vals(t), top, y, next, sh.kscale + in(t + 1u),
                                                  sh.vscale + in(t));
         finish(t + 1u, next, true);
     };
@@ -613,11 +630,11 @@ __device__ __forceinline__ void tall_part(cargs& a, Shared<DP, FMT>& sh, const J
             begin(t);
             fill(t);
             if (busy) w.weights(scale, s[0]);
-            if (WEIGHTS && busy) scale_weights<true>(s[0], sh.vscale + in(t), seen);
-            if ((!WEIGHTS || FMT != KV_INT8) && (BETWEEN || !seen_by_all<kTile>(x, k0 + t * kTile)))
-                odd_values(t, s[0]);                                       // an int8 code is a number
+            if (CODES && busy) scale_weights<!SPLIT>(s[0], sh.vscale + in(t), seen);
+            if ((SPLIT || FMT != KV_INT8) && (BETWEEN || !seen_by_all<kTile>(x, k0 + t * kTile)))
+                odd_values(t, s[0]);                                       // an int8 code by itself is a number
             if (!busy) continue;
-            typename Wave<T, DP>::Piece z[2][DP / 32];
+            typename Wave<T, DP, CODES>::Piece z[2][DP / 32];
             w.read_values(vals(t), 0, z[0]);
             w.values(vals(t), s[0], z);
             w.scores(keys(t + 1u), s[0]);
@@ -685,7 +702,7 @@ __device__ __forceinline__ void short_part(cargs& a, ShortShared<DP, FMT>& sh, c
     const uint32_t tiles = (k1 - k0 + kOwnTile - 1u) / kOwnTile;
     const Row row = row_of(a, job, first_row + n32, rows);
     constexpr uint32_t NP = Geo<DP>::cpr / 2;                             // copies of a tile's keys
-    constexpr bool CODES = FMT != KV_SAME, WEIGHTS = CODES && kScaledWeights<T>;
+    constexpr bool CODES = FMT != KV_SAME, SPLIT = CODES && kSplitScales<T>;
     // Pages of the list: those of the first tokens, then those from `low` on.
     const uint32_t few_pages = x.few ? column_of(a, x.few - 1u) + 1u : 0u, low_page = column_of(a, x.low);
     auto entry_of = [&](uint32_t column, bool few) { return few ? column : column - low_page + few_pages; };
@@ -738,6 +755,13 @@ __device__ __forceinline__ void short_part(cargs& a, ShortShared<DP, FMT>& sh, c
         scale_at = CODES && ok ? at + (uint64_t)scale_offset(slot, slots, dim, (int64_t)slot_bytes) : 0u;
         return (uint32_t)__ballot(ok);
     };
+    // Waited for here: codes asked for behind a scale that is still on its way come
+    // later (64 x 1 of 32768 e4m3 tokens, window 8192: 251 us, waited for 229).
+    auto own_scale = [&] {
+        uint32_t bits = scale_at ? *(const ATT_GLOBAL uint16_t*)scale_at : 0u;
+        asm volatile("" : "+v"(bits));
+        return (uint16_t)bits;
+    };
     CodeCopy<T, DP, FMT == KV_SAME ? KV_INT8 : FMT, kOwnTile, 64, false> kcode;
     CodeCopy<T, DP, FMT == KV_SAME ? KV_INT8 : FMT, kOwnTile, 64, true> vcode;
     auto ask_k = [&](uint32_t t) {
@@ -765,10 +789,10 @@ __device__ __forceinline__ void short_part(cargs& a, ShortShared<DP, FMT>& sh, c
         }
         const uint32_t end = tiles - t0 < run ? tiles : t0 + run;
         uint32_t there = 0;
-        uint32_t bits16 = 0;                                              // of the lane's scale
+        uint16_t bits16 = 0;                                              // of the lane's scale
         if (t0 + wave < end) {
             there = place(t0 + wave);
-            if (CODES) bits16 = scale_bits(scale_at);
+            if (CODES) bits16 = own_scale();
             wait_lgkm0();
             ask_k(t0 + wave);
             ask_v(t0 + wave);
@@ -776,15 +800,17 @@ __device__ __forceinline__ void short_part(cargs& a, ShortShared<DP, FMT>& sh, c
         for (uint32_t t = t0 + wave; t < end; t += kWaves) {
             const uint32_t next = t + kWaves, k = k0 + t * kOwnTile, now = there;
             float* const scales = sh.scale[wave][(t / kWaves) & 1u];
+            uint16_t* const powers = sh.vpower[wave][(t / kWaves) & 1u];
             if (CODES) {
-                scales[lane] = __builtin_bit_cast(float, bits16);
+                if (lane < kOwnTile) scales[lane] = scale_value(bits16);
+                else split_scale<SPLIT>(bits16, &scales[lane], &powers[lane - kOwnTile]);
                 wait_lgkm0();
                 kcode.template store<false>(lane, nullptr, keys);
-                vcode.template store<!WEIGHTS>(lane, scales + kOwnTile, vals);
+                vcode.template store<SPLIT>(lane, powers, vals);
             }
             if (next < end) {
                 there = place(next);
-                if (CODES) bits16 = scale_bits(scale_at);
+                if (CODES) bits16 = own_scale();
             }
             wait_lgkm0();
             if (!CODES) {
@@ -804,14 +830,14 @@ __device__ __forceinline__ void short_part(cargs& a, ShortShared<DP, FMT>& sh, c
             if (!all || now != ~0u) w.mask(s, bits);
             w.weights(scale, s);
             if (CODES) {
-                if (WEIGHTS && all) scale_weights<false>(s, scales + kOwnTile, bits);
-                else if (WEIGHTS) scale_weights<true>(s, scales + kOwnTile, bits);
+                if (SPLIT || all) scale_weights<false>(s, scales + kOwnTile, bits);
+                else scale_weights<true>(s, scales + kOwnTile, bits);
             } else if (next < end) {
                 wait_vmcnt<NP>();
             } else {
                 wait_vmcnt<0>();
             }
-            if ((!WEIGHTS || FMT != KV_INT8) && !all && Wave<T, DP>::template odd_share<false>(vals, 0, 1, kOwnTile)) {
+            if ((SPLIT || FMT != KV_INT8) && !all && Wave<T, DP>::template odd_share<false>(vals, 0, 1, kOwnTile)) {
                 w.template add_odd<1>(vals, s, bits);
                 wait_lgkm0();
                 Wave<T, DP>::template odd_share<true>(vals, 0, 1, kOwnTile);

@@ -140,7 +140,11 @@ __device__ __forceinline__ uint64_t zero_row() { return (uint64_t)(uintptr_t)g_z
 
 // A wave's 32 queries and what it has summed for them.  Lane l: query l % 32,
 // half l / 32 of each group of 8 keys (scores) or 8 elements (result).
-template <typename T, uint32_t DP>
+// AGAIN: offsets within a tile are worked out for each tile.  Kept from tile to tile,
+// beside codes on their way, they do not fit into the registers, and one that comes
+// back from memory waits for the codes too (2048 queries of 32768 e4m3 tokens: 1247 us,
+// this 1165).
+template <typename T, uint32_t DP, bool AGAIN = false>
 struct Wave {
     typedef typename Vec<T>::v8 v8;
     typedef typename Vec<T>::v4 v4;
@@ -193,14 +197,15 @@ struct Wave {
     template <uint32_t NB>
     __device__ __forceinline__ void scores(const uint8_t* keys, f32x16 (&s)[NB]) const {
         constexpr uint32_t AHEAD = 2;
-        const uint32_t lane = lane_id(), row = lane % 32u, key = Geo<DP>::key_k(row);
+        const uint32_t lane = lane_id(), row = lane % 32u;
         const uint8_t* at = keys + row * (DP * 2u);
+        uint32_t chunk = (lane / 32u ^ Geo<DP>::key_k(row)) * 16u;
+        if (AGAIN) asm volatile("" : "+v"(chunk));
         v8 x[AHEAD + 1][NB];
         auto read = [&](uint32_t k) {
-            const uint32_t c = (2u * k + lane / 32u) ^ key;
 #pragma unroll
             for (uint32_t n = 0; n < NB; ++n)
-                x[k % (AHEAD + 1)][n] = *reinterpret_cast<const v8*>(at + n * 32u * (DP * 2u) + c * 16u);
+                x[k % (AHEAD + 1)][n] = *reinterpret_cast<const v8*>(at + n * 32u * (DP * 2u) + (32u * k ^ chunk));
         };
 #pragma unroll
         for (uint32_t k = 0; k < AHEAD; ++k) read(k);
@@ -276,11 +281,13 @@ struct Wave {
     __device__ __forceinline__ static void read_values(const uint8_t* vals, uint32_t step, Piece (&x)[NO]) {
         const uint32_t lane = lane_id(), i = lane % 16u;
         const uint32_t row = 4u * (lane / 32u) + i / 4u;                  // of 4 x 16-element pieces
-        const uint32_t c0 = 2u * ((lane / 16u) & 1u) + (i % 4u) / 2u, key = Geo<DP>::key_v(row);
+        const uint32_t c0 = 2u * ((lane / 16u) & 1u) + (i % 4u) / 2u;
         const uint8_t* at = vals + (step * 16u + row) * (DP * 2u) + 8u * (i & 1u);
+        uint32_t chunk = (c0 ^ Geo<DP>::key_v(row)) * 16u;
+        if (AGAIN) asm volatile("" : "+v"(chunk));
 #pragma unroll
         for (uint32_t b = 0; b < NO; ++b) {
-            const uint8_t* v = at + ((4u * b + c0) ^ key) * 16u;
+            const uint8_t* v = at + (64u * b ^ chunk);
             x[b].h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)v);
             x[b].h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(v + 8u * DP * 2u));
         }
@@ -316,22 +323,24 @@ struct Wave {
                                              const float* value_scales = nullptr) {
         // Products of scores, of values, and how far ahead of them LDS is read.  Beside
         // scales and codes on their way, what is read five ahead does not fit into the
-        // registers (2048 queries of 32768 e4m3 tokens: 1695 us, three ahead 1505, two 1240).
+        // registers (2048 queries of 32768 e4m3 tokens: 1695 us, three ahead 1505, two 1247).
         constexpr uint32_t NS = 2 * NK, NP = 4 * NO, AHEAD = KEYS ? 2 : 5;
-        const uint32_t lane = lane_id(), row = lane % 32u, key = Geo<DP>::key_k(row);
-        const uint8_t* kat = keys + row * (DP * 2u);
+        const uint32_t lane = lane_id(), row = lane % 32u;
         const uint32_t i16 = lane % 16u, vrow = 4u * (lane / 32u) + i16 / 4u;
-        const uint32_t c0 = 2u * ((lane / 16u) & 1u) + (i16 % 4u) / 2u, vkey = Geo<DP>::key_v(vrow);
+        const uint32_t c0 = 2u * ((lane / 16u) & 1u) + (i16 % 4u) / 2u;
+        const uint8_t* kat = keys + row * (DP * 2u);
         const uint8_t* vat = vals + vrow * (DP * 2u) + 8u * (i16 & 1u);
+        uint32_t kchunk = (lane / 32u ^ Geo<DP>::key_k(row)) * 16u, vchunk = (c0 ^ Geo<DP>::key_v(vrow)) * 16u;
+        if (AGAIN) asm volatile("" : "+v"(kchunk), "+v"(vchunk));
         Piece x[AHEAD + 1];
         auto read = [&](uint32_t i) {                                     // what product i takes from LDS
             Piece& y = x[i % (AHEAD + 1u)];
             if (i < NS) {
                 const uint32_t k = i / 2u, n = i % 2u;
-                y.v = *reinterpret_cast<const v8*>(kat + n * 32u * (DP * 2u) + ((2u * k + lane / 32u) ^ key) * 16u);
+                y.v = *reinterpret_cast<const v8*>(kat + n * 32u * (DP * 2u) + (32u * k ^ kchunk));
             } else if (i < NS + NP) {
                 const uint32_t t = (i - NS) / NO, b = (i - NS) % NO;
-                const uint8_t* v = vat + t * 16u * (DP * 2u) + ((4u * b + c0) ^ vkey) * 16u;
+                const uint8_t* v = vat + t * 16u * (DP * 2u) + (64u * b ^ vchunk);
                 y.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)v);
                 y.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(v + 8u * DP * 2u));
             }
