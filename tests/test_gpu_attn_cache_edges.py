@@ -141,6 +141,45 @@ def test_scales(q_len, scale, hint):
     s.check(0, 0, parents_of(gen(1), 2, q_len, "near"), scale=scale, hint=hint)
 
 
+def set_value_scales(s, scale):
+    """Scales [pages, kv, slots] of a pool of values."""
+    p = s.v if s.heads_first else s.v.transpose(1, 2)
+    rows = p.shape[2] - s.slots
+    tail = torch.zeros((*p.shape[:2], rows * s.dim), dtype=torch.uint8)
+    tail[..., :2 * s.slots] = scale.bfloat16().contiguous().view(torch.uint8)
+    p[:, :, s.slots:] = tail.view(*p.shape[:2], rows, s.dim).cuda()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("q_len,hint", [(1, None), (90, FAR)])
+def test_value_scales_of_all_sizes(q_len, hint, fmt, dtype):
+    """From far below the smallest number of f16 to its largest values, beside each other, some with a sign."""
+    g = gen(660)
+    s = Setup(g, dtype, fmt, [300, 90], None, q_len, 4, 2, 64, 16)
+    top = 8.0 if fmt == "int8" else 6.0
+    power = torch.rand((s.pages, 2, 16), generator=g) * (top + 45) - 45
+    set_value_scales(s, torch.exp2(power) * (1 - 2 * (torch.rand(power.shape, generator=g) < 0.2).float()))
+    s.check(0, 0, hint=hint)
+    set_value_scales(s, torch.exp2(power - 20))
+    s.check(40, 3, hint=hint)
+
+
+@pytest.mark.parametrize("heads", [2, 64])
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_values_beyond_f16(fmt, heads):
+    """A value that f16 does not hold is an infinity, and a code 0 times its scale is 0."""
+    s = Setup(gen(670), "f16", fmt, [1], None, 1, heads, 1, 128, 16)
+    s.v[:, :s.slots, :, ::5] = 0
+    for scale in (2.0 ** 20, 1.5 * 2.0 ** 40, 2.0 ** 120):
+        set_value_scales(s, torch.full((s.pages, 1, 16), scale))
+        value = s.tokens(s.v, 0)[0, 0]
+        with np.errstate(over="ignore"):
+            want = value.astype(np.float16).astype(np.float64)
+        assert (value == 0).any() and np.isinf(want).any()
+        assert np.array_equal(s.run()[0][0, 0], np.tile(want, (heads, 1)))
+
+
 @pytest.mark.parametrize("window,sinks", [(2 ** 32 - 1, 5), (1 << 31, 2 ** 32 - 1), (5, 2 ** 32 - 1), (300, 1 << 31)])
 @pytest.mark.parametrize("q_len", [1, 70])
 def test_windows_and_sinks_beyond_everything(q_len, window, sinks):
