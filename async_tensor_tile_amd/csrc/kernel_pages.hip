@@ -693,18 +693,18 @@ __device__ __forceinline__ void move_piece(const TokensOf<N>& p, gbyte* pool, ui
     }
 }
 
-// A row ends at token `end`, and gives back the pages between that and its old end.
+// A row ends at token `end`, and gives back the pages between that and its old end;
+// each once, and the shorter end stays, also where a row is listed twice.
 __device__ __forceinline__ void end_row(const Table& t, uint32_t row, uint32_t len, uint32_t end, uint32_t lane,
                                         uint32_t* err) {
     const uint32_t c0 = (end + t.slots - 1u) / t.slots, c1 = (len + t.slots - 1u) / t.slots;
     int32_t* const entries = t.table + (uint64_t)row * t.pitch;
     for (uint32_t c = c0 + lane; c < c1; c += 64u) {
-        const int32_t page = entries[c];
-        entries[c] = -1;
+        const int32_t page = atomicExch(&entries[c], -1);
         if ((uint32_t)page < t.pages) atomicSub(&t.refs[page], 1);
         else record_page_error(err);
     }
-    if (lane == 0) t.lens[row] = (int32_t)end;
+    if (lane == 0) atomicMin(&t.lens[row], (int32_t)end);
 }
 
 // Entry i and one pool: the checks, the same in every workgroup of the entry and

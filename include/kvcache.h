@@ -194,8 +194,8 @@ tmap_status page_compact(const page_table_t* from, const page_table_t* to, const
  * The d_count[i] <= width kept indices ascend from 0 or above and end below the
  * row's length (none: the row is cut to d_from[i]).  d_ok[i] = 1, or 0 for an
  * entry that is left as it was: where that does not hold, or where a page that
- * would be written is shared (count above 1).  Rows are distinct.  pools may be
- * NULL with npool == 0: the tables alone.  Errors: NULL, RANK, UNSUPPORTED
+ * would be written is shared (count above 1).  Rows are distinct (of one that is
+ * listed twice every page is given back once).  pools may be NULL with npool == 0: the tables alone.  Errors: NULL, RANK, UNSUPPORTED
  * (table, pools), HIP.  n == 0 is a no-op. */
 tmap_status page_keep(const page_table_t* pt, const tmap_t* pools, uint32_t npool, const int32_t* d_rows,
                       const int32_t* d_from, const int32_t* d_keep, uint32_t width, const int32_t* d_count, uint32_t n,
@@ -251,12 +251,13 @@ uint64_t attn_cache_workspace(const tmap_t* q, const tmap_t* k_pool, uint32_t wi
  * attn_shared_prefix; a query that sees nothing gets o = 0 and lse = -inf, and
  * what a query does not see does not reach it, whatever it holds.  The pools are
  * of the queries' type (KV_SAME) or hold codes; a key is c * s, and so is a value
- * (f16: rounded to the type).  len_hint is the length that the work is
- * split for (any value is right).  A count or row out of range is recorded: no
+ * (f16: one beyond the type's numbers is an infinity, one below its normal
+ * numbers is rounded to a step of theirs).  len_hint is the length that the work
+ * is split for (any value is right).  A count or row out of range is recorded: no
  * query is there, or none sees a token.  Errors as attn_shared_prefix, and
- * UNSUPPORTED for pools that are not of the format (more than 2^24 - 1
- * workgroups: about one for each sequence, key / value head and 128 of its
- * queries). */
+ * UNSUPPORTED for pools that are not of the format and for more than 2^31 - 1
+ * pairs of a query and a head of its group, or 2^24 - 1 workgroups (one at most
+ * for each sequence, key / value head and 32 such pairs, or 512 in all). */
 tmap_status attn_window(const tmap_t* q, const tmap_t* k_pool, const tmap_t* v_pool, int32_t format,
                         const page_table_t* pt, const int32_t* d_rows, const int32_t* d_count, uint32_t window,
                         uint32_t sinks, uint32_t len_hint, float scale, const tmap_t* o, float* d_lse, void* d_ws,

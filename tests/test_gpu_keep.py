@@ -217,3 +217,28 @@ def test_keep_in_a_graph():
         torch.cuda.synchronize()
         assert grown.tolist() == [1] * n and good.tolist() == [1] * n
         s.same_as(want)
+
+
+@pytest.mark.parametrize("entries", [3, 20])
+def test_a_row_listed_twice(entries):
+    """What is kept is not said, but every page is given back once and the row's length is that of its pages."""
+    g = gen(330 + entries)
+    s = State(g, 24, 6, 4, 2, 24)
+    lens = np.full(24, 22, np.int32)
+    table, refs = np.arange(144, dtype=np.int32).reshape(24, 6), np.ones(146, np.int32)
+    refs[144:] = 0
+    s.lens.copy_(ints(lens)), s.table.copy_(ints(table)), s.refs.copy_(ints(refs))
+    rows = np.repeat(np.arange(entries), 2)
+    first = s.rng.integers(0, 20, 2 * entries)
+    count = s.rng.integers(0, 3, 2 * entries)
+    good = run(s, rows, first, np.tile([0, 2], (2 * entries, 1)), np.minimum(count, 22 - first))
+    ends, held = s.lens.cpu().numpy(), s.table.cpu().numpy()
+    for r in range(24):
+        n = -(-int(ends[r]) // 4)
+        assert (held[r, :n] >= 0).all() and (held[r, n:] == -1).all()
+    assert all(x in (0, 1) for x in good) and (ends[:entries] <= 22).all() and (ends[entries:] == 22).all()
+    assert np.array_equal(np.bincount(held[held >= 0], minlength=146), s.refs.cpu().numpy())
+    try:                                                                 # an entry that found a page given back may say so
+        att.tile_device_status(stream())
+    except att.TmapError as e:
+        assert e.name == "ERR_PAGE"
