@@ -499,6 +499,9 @@ def page_keep(pt: page_table_t, pools, d_rows, d_from, d_keep, d_count, n: int, 
         if len(shape) != 2 or shape[0] < n:
             raise ValueError(f"d_keep has to hold {n} rows")
         width = int(shape[1])
+    for name, x in (("d_rows", d_rows), ("d_from", d_from), ("d_count", d_count), ("d_ok", d_ok)):
+        if hasattr(x, "numel") and x.numel() < n:
+            raise ValueError(f"{name} has to hold {n} values")
     _check(lib().page_keep(_ref(pt), arr, k, _ints(d_rows, "d_rows"), _ints(d_from, "d_from"), _ints(d_keep, "d_keep"),
                            int(width), _ints(d_count, "d_count"), int(n), _ints(d_ok, "d_ok"), _addr(stream)),
            "page_keep")

@@ -17,6 +17,9 @@
 // 5.2 TB/s) take 13.7 us in pairs side by side, 16.5 in halves of the whole head,
 // 17.9 to 18.8 with part of the head turned (lanes with two chunks of a pair beside
 // lanes with one of the rest), 21.3 to 21.8 element by element.
+//
+// The step to pools of codes: 8191 tokens, 32 + 2 x 8 heads of 128 f16 elements to
+// int8 (185 MB), 38.2 us, 4.8 TB/s; 64 tokens' kernel 8.1.
 #include <hip/hip_runtime.h>
 
 #include <cmath>

@@ -82,6 +82,15 @@ def test_index_types():
         att.page_keep(table(), None, BASE, BASE, torch.zeros(16, dtype=torch.int32), BASE, 4, BASE)
 
 
+@pytest.mark.parametrize("short", ["d_rows", "d_from", "d_count", "d_ok"])
+def test_keep_takes_a_value_for_each_entry(short):
+    torch = pytest.importorskip("torch")
+    rows, first, count, good = (torch.zeros(3 if name == short else 4, dtype=torch.int32)
+                                for name in ("d_rows", "d_from", "d_count", "d_ok"))
+    with pytest.raises(ValueError, match=short):
+        att.page_keep(table(), None, rows, first, torch.zeros((4, 4), dtype=torch.int32), count, 4, good)
+
+
 def test_keep_refusals():
     def call(pt=table(), pools=pool(), rows=BASE, first=BASE, keep=BASE, count=BASE, n=4, good=BASE, width=4):
         return lambda: att.page_keep(pt, pools, rows, first, keep, count, n, good, width=width)
