@@ -6,10 +6,10 @@ step (bf16 2^-8, fp16 2^-11, fp32 2^-24, relative).  A score is a sum of dim
 products in fp32 (codes and keys of 16 bits are exact in them), times a key's
 scale and the call's: off by at most (dim + 8) * 2^-24 times the sum of their
 absolute values, which shifts a weight by as much again, relatively, and the
-exponential adds 2^-21.  Each weight is rounded to the type for the product with
-the values, and so is a value that a code stands for; n of those are added in
-fp32, and the quotient is rounded to the type.  Weights and values below the
-smallest normal number of f16 are off by at most 2^-25."""
+exponential adds 2^-21.  Each weight, times its value's scale or a part of it, is
+rounded to the type for the product with the values or their codes; n of those
+are added in fp32, and the quotient is rounded to the type.  Weights and values
+below the smallest normal number of f16 are off by at most 2^-25."""
 import math
 
 import numpy as np
@@ -128,7 +128,7 @@ class Setup:
             want, lse, weight, size, seen = ok.attend(q[b, :n], k, v, sees, scale)
             shift = (self.dim + 8) * 2.0 ** -24 * size + 2.0 ** -21
             m = seen[..., None]
-            limit = weight * (step * (1 if self.fmt == "same" else 2) + 2 * shift[..., None] + (m + 32) * 2.0 ** -24)
+            limit = weight * (step + 2 * shift[..., None] + (m + 32) * 2.0 ** -24)
             tiny = 2.0 ** -25 if self.dtype == "f16" else 1e-37
             limit += step * np.abs(want) + (m + 1) * tiny * (8 if self.fmt == "same" else 16)
             off = np.abs(got[b, :n] - want)
