@@ -167,8 +167,10 @@ template <typename T, uint32_t DP>
 static void join(const CacheArgs& a, hipStream_t stream) {
     const uint32_t blocks = a.batch * a.kv * a.blocks32;
     // More parts than a wave has in flight: a workgroup's waves share them (a token of
-    // 32768, 64 parts: both launches 48.5 us, so 39.6).
-    if (a.parts > 16)
+    // 32768, 64 parts: both launches 48.5 us, so 39.6), or few blocks that leave the GPU
+    // empty (a token of 4096 each of 4 rows 21.6 and 20.1; 2 trees of 60 nodes of 16000, 128
+    // blocks, 54.8 and 56.6; 12 rows of 8192, 96 blocks, 71.5 and 72.6).
+    if (a.parts > 16 || (a.parts > 4 && blocks <= 64))
         hipLaunchKernelGGL((k_attn_cache_join<T, DP, true>), dim3(blocks, (a.dim + 7u) / 8u), dim3(kThreads), 0, stream, a);
     else
         hipLaunchKernelGGL((k_attn_cache_join<T, DP, false>), dim3(blocks, (a.dim + 31u) / 32u), dim3(kThreads), 0, stream,
