@@ -625,9 +625,11 @@ __device__ __forceinline__ KeepEntry keep_entry(const Table& t, const int32_t* r
 }
 
 // Whether kept token j ascends, is there, and moves between pages that may be used.
+// Indices that ascend from 0 are at least their place in the list: one below it has
+// no place in the table, also where its neighbour is lower still.
 __device__ __forceinline__ bool may_move(const Table& t, const KeepEntry& e, uint32_t j, uint32_t* err) {
     const int64_t k = e.kept[j], before = j ? e.kept[j - 1] : -1;
-    if (k <= before || e.first + k >= e.len) return false;
+    if (k < (int64_t)j || k <= before || e.first + k >= e.len) return false;
     if (k == (int64_t)j) return true;
     const int32_t a = e.entries[(uint32_t)(e.first + k) / t.slots], b = e.entries[(uint32_t)(e.first + j) / t.slots];
     if ((uint32_t)a >= t.pages || (uint32_t)b >= t.pages) {
