@@ -697,16 +697,24 @@ __device__ __forceinline__ void move_piece(const TokensOf<N>& p, gbyte* pool, ui
     }
 }
 
+// Pages between a served entry's new end and the old one that are none are recorded,
+// by thread `i` of `n`, while the table is as the call found it: where a row is listed
+// twice, an entry that finds a page given back already has nothing to record.
+__device__ __forceinline__ void record_missing(const Table& t, const KeepEntry& e, uint32_t i, uint32_t n, uint32_t* err) {
+    const uint32_t end = (uint32_t)(e.first + e.count);
+    const uint32_t c0 = (end + t.slots - 1u) / t.slots, c1 = ((uint32_t)e.len + t.slots - 1u) / t.slots;
+    for (uint32_t c = c0 + i; c < c1; c += n)
+        if ((uint32_t)e.entries[c] >= t.pages) record_page_error(err);
+}
+
 // A row ends at token `end`, and gives back the pages between that and its old end;
 // each once, and the shorter end stays, also where a row is listed twice.
-__device__ __forceinline__ void end_row(const Table& t, uint32_t row, uint32_t len, uint32_t end, uint32_t lane,
-                                        uint32_t* err) {
+__device__ __forceinline__ void end_row(const Table& t, uint32_t row, uint32_t len, uint32_t end, uint32_t lane) {
     const uint32_t c0 = (end + t.slots - 1u) / t.slots, c1 = (len + t.slots - 1u) / t.slots;
     int32_t* const entries = t.table + (uint64_t)row * t.pitch;
     for (uint32_t c = c0 + lane; c < c1; c += 64u) {
         const int32_t page = atomicExch(&entries[c], -1);
         if ((uint32_t)page < t.pages) atomicSub(&t.refs[page], 1);
-        else record_page_error(err);
     }
     if (lane == 0) atomicMin(&t.lens[row], (int32_t)end);
 }
@@ -725,7 +733,9 @@ __global__ __launch_bounds__(kKeepThreads) void k_page_keep(const Table t, const
         for (uint32_t j = tid; j < (uint32_t)e.count && good; j += kKeepThreads) good = may_move(t, e, j, err);
     good = __syncthreads_and(good);
     if (blockIdx.y == 0 && tid == 0) ok[i] = good;
-    if (!good || p.npool == 0) return;
+    if (!good) return;
+    if (blockIdx.y == 0) record_missing(t, e, tid, kKeepThreads, err);
+    if (p.npool == 0) return;
     const uint32_t units = pieces_of(p);
     for (uint32_t j0 = 0; j0 < (uint32_t)e.count; j0 += kKeepTokens) {
         const uint32_t m = (uint32_t)e.count - j0 < kKeepTokens ? (uint32_t)e.count - j0 : kKeepTokens;
@@ -738,11 +748,11 @@ __global__ __launch_bounds__(kKeepThreads) void k_page_keep(const Table t, const
 
 // The rows of served entries end behind what they kept, one wave a row.
 __global__ __launch_bounds__(64) void k_page_end(const Table t, const int32_t* rows, const int32_t* from,
-                                                 const int32_t* count, const int32_t* ok, uint32_t* err) {
+                                                 const int32_t* count, const int32_t* ok) {
     const uint32_t i = blockIdx.x;
     if (!ok[i]) return;
     const uint32_t row = (uint32_t)rows[i];
-    end_row(t, row, (uint32_t)t.lens[row], (uint32_t)from[i] + (uint32_t)count[i], threadIdx.x, err);
+    end_row(t, row, (uint32_t)t.lens[row], (uint32_t)from[i] + (uint32_t)count[i], threadIdx.x);
 }
 
 // A few entries and little data by one workgroup, in one launch: all checks, all
@@ -765,6 +775,7 @@ __global__ __launch_bounds__(kOneKeepThreads) void k_page_keep_one(const Table t
         if (good)
             for (uint32_t j = lane; j < (uint32_t)e.count && good; j += 64u) good = may_move(t, e, j, err);
         good = __all(good);
+        if (good) record_missing(t, e, lane, 64u, err);
         if (good && p.npool)
             for (uint32_t j = lane; j < (uint32_t)e.count; j += 64u) moves[i * width + j] = move_of(t, p, e, j);
         if (lane == 0) {
@@ -779,7 +790,7 @@ __global__ __launch_bounds__(kOneKeepThreads) void k_page_keep_one(const Table t
         if (tokens[entry] > 0)
             move_piece(p, gptr(p.base[y - entry * p.npool]), x - y * units, moves + entry * width, (uint32_t)tokens[entry]);
     }
-    if (good) end_row(t, e.row, (uint32_t)e.len, (uint32_t)(e.first + e.count), lane, err);
+    if (good) end_row(t, e.row, (uint32_t)e.len, (uint32_t)(e.first + e.count), lane);
 }
 
 // ---- host ------------------------------------------------------------------------
@@ -1114,7 +1125,7 @@ extern "C" tmap_status page_keep(const page_table_t* pt, const tmap_t* pools, ui
         else
             hipLaunchKernelGGL(k_page_keep, grid, dim3(kKeepThreads), 0, s, t, p, d_rows + i, d_from + i, keep, width,
                                d_count + i, d_ok + i, err);
-        hipLaunchKernelGGL(k_page_end, dim3(m), dim3(64), 0, s, t, d_rows + i, d_from + i, d_count + i, d_ok + i, err);
+        hipLaunchKernelGGL(k_page_end, dim3(m), dim3(64), 0, s, t, d_rows + i, d_from + i, d_count + i, d_ok + i);
     }
     return check_launch("page_keep");
 }

@@ -41,3 +41,29 @@ def test_lists_below_zero(npool):
     assert run(s, np.arange(6), first, keep, [2] * 6) == expect
     s.same_as(want)
     att.tile_device_status(stream())
+
+
+@pytest.mark.parametrize("entries,npool", [(3, 2), (20, 2), (3, 17)])
+def test_rows_listed_twice_record_nothing(entries, npool):
+    """A page that the row's other entry gave back is no page out of range; run after run, whichever comes first."""
+    for k in range(20):
+        s = rows_of(24, 6, 4, 22, npool, 350 + k)
+        rows = np.repeat(np.arange(entries), 2)
+        count = np.tile([2, 0], entries)
+        good = run(s, rows, np.full(2 * entries, 3), np.tile([0, 2], (2 * entries, 1)), count)
+        assert good == [1] * (2 * entries)
+        att.tile_device_status(stream())
+
+
+@pytest.mark.parametrize("n,npool", [(2, 2), (9, 2), (2, 0), (2, 17)])
+def test_missing_pages_are_recorded(n, npool):
+    """A row whose pages behind its new end are none is served, and recorded."""
+    s = rows_of(n, 6, 4, 22, npool)
+    s.table[0, 3], s.table[1, 4] = -1, 6 * n + 2                         # no page, and one behind the last
+    want = s.model()
+    expect = want.keep(range(n), [5] * n, [[0]] * n, [1] * n)
+    assert run(s, np.arange(n), [5] * n, [[0]] * n, [1] * n) == expect == [1] * n
+    s.same_as(want)
+    with pytest.raises(att.TmapError) as e:
+        att.tile_device_status(stream())
+    assert e.value.name == "ERR_PAGE"
