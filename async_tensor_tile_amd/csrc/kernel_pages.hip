@@ -639,6 +639,15 @@ __device__ __forceinline__ bool may_move(const Table& t, const KeepEntry& e, uin
     return t.refs[b] <= 1;
 }
 
+// Whether the row may end where it would: not inside of a page that another row uses
+// too, whose tokens the row would write over as it grows again.
+__device__ __forceinline__ bool may_end(const Table& t, const KeepEntry& e) {
+    const int64_t end = e.first + e.count;
+    if (end >= e.len || (uint32_t)end % t.slots == 0u) return true;
+    const int32_t page = e.entries[(uint32_t)end / t.slots];
+    return (uint32_t)page >= t.pages || t.refs[page] <= 1;
+}
+
 // Where a kept token comes from and goes to in a pool.  src < 0: it stays.
 struct Move {
     int64_t src, dst, src_scale, dst_scale;
@@ -729,6 +738,7 @@ __global__ __launch_bounds__(kKeepThreads) void k_page_keep(const Table t, const
     const uint32_t tid = threadIdx.x, i = blockIdx.x;
     const KeepEntry e = keep_entry(t, rows, from, keep, width, count, i, tid == 0 && blockIdx.y == 0, err);
     bool good = e.good;
+    if (good && tid == kKeepThreads - 1u) good = may_end(t, e);         // of another wave than the first indices
     if (good)
         for (uint32_t j = tid; j < (uint32_t)e.count && good; j += kKeepThreads) good = may_move(t, e, j, err);
     good = __syncthreads_and(good);
@@ -772,6 +782,7 @@ __global__ __launch_bounds__(kOneKeepThreads) void k_page_keep_one(const Table t
     if (i < n) {
         e = keep_entry(t, rows, from, keep, width, count, i, lane == 0, err);
         good = e.good;
+        if (good && lane == 0) good = may_end(t, e);
         if (good)
             for (uint32_t j = lane; j < (uint32_t)e.count && good; j += 64u) good = may_move(t, e, j, err);
         good = __all(good);

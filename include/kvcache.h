@@ -193,10 +193,12 @@ tmap_status page_compact(const page_table_t* from, const page_table_t* to, const
  * of its drafted tokens.
  * The d_count[i] <= width kept indices ascend from 0 or above and end below the
  * row's length (none: the row is cut to d_from[i]).  d_ok[i] = 1, or 0 for an
- * entry that is left as it was: where that does not hold, or where a page that
- * would be written is shared (count above 1).  Rows are distinct (of one that is
- * listed twice every page is given back once).  pools may be NULL with npool == 0: the tables alone.  Errors: NULL, RANK, UNSUPPORTED
- * (table, pools), HIP.  n == 0 is a no-op. */
+ * entry that is left as it was: where that does not hold, where a page that
+ * would be written is shared (count above 1), or where the row would come to
+ * end inside of a shared page, which it would write as it grows again (fork it).
+ * Rows are distinct (of one that is listed twice every page is given back once).
+ * pools may be NULL with npool == 0: the tables alone.  Errors: NULL, RANK,
+ * UNSUPPORTED (table, pools), HIP.  n == 0 is a no-op. */
 tmap_status page_keep(const page_table_t* pt, const tmap_t* pools, uint32_t npool, const int32_t* d_rows,
                       const int32_t* d_from, const int32_t* d_keep, uint32_t width, const int32_t* d_count, uint32_t n,
                       int32_t* d_ok, void* stream);

@@ -166,6 +166,9 @@ class Pages:
             moves = [(where(f + k), where(f + j)) for j, k in enumerate(ks) if k != j] if good else []
             good = good and all(0 <= p < len(refs) for m in moves for p, _ in m)
             good = good and all(refs[p] <= 1 for _, (p, _) in moves)
+            if good and f + n < self.lens[r] and (f + n) % self.slots:    # a row does not end inside of a shared page
+                p = int(self.table[r, (f + n) // self.slots])
+                good = not (0 <= p < len(refs) and refs[p] > 1)
             ok.append(int(good))
             if not good:
                 continue

@@ -67,3 +67,47 @@ def test_missing_pages_are_recorded(n, npool):
     with pytest.raises(att.TmapError) as e:
         att.tile_device_status(stream())
     assert e.value.name == "ERR_PAGE"
+
+
+@pytest.mark.parametrize("npool", [2, 17])
+def test_rows_do_not_end_inside_of_shared_pages(npool):
+    """Two rows share their first two pages.  One that is cut inside of them would write the other's tokens as it grows
+    again: it is left as it was.  Cut at a page's end, or where it ends anyway, it is served."""
+    s = rows_of(4, 4, 4, 15, npool)
+    s.table[1, :2] = s.table[0, :2]
+    s.refs[:2], s.refs[4:6] = 2, 0
+    cuts = [([0, 1], [6, 4], [0, 0]), ([0, 1], [1, 5], [3, 2]), ([0, 1], [7, 2], [0, 1]), ([0, 1], [4, 8], [0, 0])]
+    got = []
+    for rows, first, count in cuts:
+        keep = np.tile([0, 1, 2], (2, 1))
+        want = s.model()
+        expect = want.keep(rows, first, keep, count)
+        assert run(s, rows, first, keep, count) == expect
+        s.same_as(want)
+        got.append(expect)
+    assert got == [[0, 1], [1, 0], [0, 0], [1, 0]]
+    s.refs[s.table[2, 3]] = 2                                            # an unfinished page that is shared already
+    want = s.model()
+    args = ([2, 3], [15, 13], [[0], [1]], [0, 1])
+    assert want.keep(*args) == [1, 1]
+    assert run(s, *(np.array(a) for a in args)) == [1, 1]
+    s.same_as(want)
+
+
+def test_a_fork_that_is_cut_and_grows_leaves_its_twin():
+    """A row and its fork share a full page; the fork drops its last tokens.  Whatever the call answers, growing and
+    writing the fork afterwards changes no token of the row."""
+    s = rows_of(2, 4, 4, 0)
+    ws = torch.empty(att.page_workspace(s.pt, 2), dtype=torch.uint8, device="cuda")
+    good = ints([0])
+    att.page_extend(s.pt, ints([0]), ints([8]), 1, good, ws, stream())
+    att.page_fork(s.pt, s.maps, ints([0]), ints([1]), 1, good, ws, stream())
+    held = [s.heads(p)[s.table[0, :2].long()].clone() for p in s.pools]
+    cut = run(s, [1], [6], [[0]], [0])
+    att.page_extend(s.pt, ints([1]), ints([2]), 1, good, ws, stream())
+    at = s.lens[1].item() - 1
+    for p in s.pools:                                                    # the row's new last token
+        s.heads(p)[s.table[1, at // 4].item(), :, at % 4] = 77
+    assert cut == [0]
+    assert all(torch.equal(s.heads(p)[s.table[0, :2].long()], h) for p, h in zip(s.pools, held))
+    att.tile_device_status(stream())
