@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 # ATT_DEBUG=1 in the environment selects the debug build (LDS poisoning and
@@ -335,7 +336,8 @@ def gemm_bf16_ex(A: tmap_t, B: tmap_t, d_C, M: int, N: int, K: int, ldc: int, st
 # ---- a paged key / value cache (include/kvcache.h) ----------------------------
 #
 # Positions, rows, pages and flags are int32: a tensor of another type (torch's
-# own default is int64) is refused.
+# own default is int64) is refused, and so is one with fewer values than the call
+# reads or writes.
 
 
 def _ref(m):
@@ -345,10 +347,23 @@ def _ref(m):
 _INT32 = set()      # element types that were seen to be 32-bit integers
 
 
-def _ints(x, name: str) -> int:
-    """Address of int32 values: a tensor of them, side by side, or an address."""
+def _dims(m):
+    """Dimensions of a map, innermost first, 1 beyond its rank (att/tmap_impl.hpp)."""
+    return (1,) * 5 if m is None else struct.unpack_from("=5q", m, 40)
+
+
+def _entries(n, name: str = "n") -> int:
+    """A count that the C ABI takes as uint32."""
+    n = int(n)
+    if not 0 <= n < 1 << 32:
+        raise ValueError(f"{name} has to be of 32 bits and not negative, not {n}")
+    return n
+
+
+def _ints(x, name: str, n: int = 0) -> int:
+    """Address of n int32 values or more: a tensor of them, side by side, or an address."""
     try:
-        if x.dtype in _INT32 and x.is_contiguous():
+        if x.dtype in _INT32 and x.is_contiguous() and x.numel() >= n:
             return x.data_ptr()
     except AttributeError:
         pass
@@ -357,6 +372,8 @@ def _ints(x, name: str) -> int:
             raise TypeError(f"{name} has to be int32, not {x.dtype}")
         if not x.is_contiguous():
             raise ValueError(f"{name} has to lie side by side")
+        if x.numel() < n:
+            raise ValueError(f"{name} has to hold {n} values")
         _INT32.add(x.dtype)
     return _addr(x)
 
@@ -424,15 +441,17 @@ def kv8_append(r, q, q_out, k: tmap_t, v: tmap_t, format, k_pool: tmap_t, v_pool
                d_pos, stream=0) -> None:
     """rope_append to pools of 8-bit codes; format "int8" or "e4m3" (or the
     KV_* value)."""
+    n = _dims(k)[2]
     _check(lib().kv8_append(_ref(r), _ref(q), _ref(q_out), _ref(k), _ref(v), _format(format), _ref(k_pool), _ref(v_pool),
-                            _ref(pt), _ints(d_rows, "d_rows"), _ints(d_at, "d_at"), _ints(d_pos, "d_pos"),
-                            _addr(stream)), "kv8_append")
+                            _ref(pt), _ints(d_rows, "d_rows", n), _ints(d_at, "d_at", n),
+                            _ints(d_pos, "d_pos", n if r is not None else 0), _addr(stream)), "kv8_append")
 
 
 def kv8_read(format, k_pool: tmap_t, v_pool: tmap_t, pt: page_table_t, d_rows, d_at, k: tmap_t, v: tmap_t,
              stream=0) -> None:
-    _check(lib().kv8_read(_format(format), _ref(k_pool), _ref(v_pool), _ref(pt), _ints(d_rows, "d_rows"),
-                          _ints(d_at, "d_at"), _ref(k), _ref(v), _addr(stream)), "kv8_read")
+    n = _dims(k)[2]
+    _check(lib().kv8_read(_format(format), _ref(k_pool), _ref(v_pool), _ref(pt), _ints(d_rows, "d_rows", n),
+                          _ints(d_at, "d_at", n), _ref(k), _ref(v), _addr(stream)), "kv8_read")
 
 
 def page_table(d_table, d_lens, d_refs, pages: int, slots: int, rows: int = 0, row_pages: int = 0,
@@ -494,27 +513,27 @@ def page_keep(pt: page_table_t, pools, d_rows, d_from, d_keep, d_count, n: int, 
     """pools as page_fork.  d_keep is a 2-D tensor [n, width], or an address
     with width."""
     arr, k = _pool_array(pools)
+    n = _entries(n)
     shape = getattr(d_keep, "shape", None)
     if shape is not None:
         if len(shape) != 2 or shape[0] < n:
             raise ValueError(f"d_keep has to hold {n} rows")
         width = int(shape[1])
-    for name, x in (("d_rows", d_rows), ("d_from", d_from), ("d_count", d_count), ("d_ok", d_ok)):
-        if hasattr(x, "numel") and x.numel() < n:
-            raise ValueError(f"{name} has to hold {n} values")
-    _check(lib().page_keep(_ref(pt), arr, k, _ints(d_rows, "d_rows"), _ints(d_from, "d_from"), _ints(d_keep, "d_keep"),
-                           int(width), _ints(d_count, "d_count"), int(n), _ints(d_ok, "d_ok"), _addr(stream)),
-           "page_keep")
+    _check(lib().page_keep(_ref(pt), arr, k, _ints(d_rows, "d_rows", n), _ints(d_from, "d_from", n),
+                           _ints(d_keep, "d_keep"), _entries(width, "width"), _ints(d_count, "d_count", n), n,
+                           _ints(d_ok, "d_ok", n), _addr(stream)), "page_keep")
 
 
 def attn_workspace(q: tmap_t, k_pool: tmap_t, prefix_len: int, suffix_hint: int) -> int:
     return int(lib().attn_workspace(_ref(q), _ref(k_pool), int(prefix_len), int(suffix_hint)))
 
 
-def _check_lse(d_lse):
-    if hasattr(d_lse, "data_ptr") and (d_lse.element_size() != 4 or not d_lse.is_floating_point() or
-                                       not d_lse.is_contiguous()):
-        raise TypeError("d_lse has to be float32 values side by side")
+def _check_lse(d_lse, n: int = 0):
+    if hasattr(d_lse, "data_ptr"):
+        if d_lse.element_size() != 4 or not d_lse.is_floating_point() or not d_lse.is_contiguous():
+            raise TypeError("d_lse has to be float32 values side by side")
+        if d_lse.numel() < n:
+            raise ValueError(f"d_lse has to hold {n} values")
 
 
 def attn_shared_prefix(q: tmap_t, k_pool: tmap_t, v_pool: tmap_t, pt: page_table_t, prefix_row: int,
@@ -534,18 +553,22 @@ def attn_window(q: tmap_t, k_pool: tmap_t, v_pool: tmap_t, format, pt: page_tabl
                 sinks: int, len_hint: int, scale: float, o: tmap_t, d_lse, d_ws, stream=0, ws_bytes: int = 0) -> None:
     """format: "same", "int8" or "e4m3" (or the KV_* value); d_rows, d_count and
     d_lse may be None."""
-    _check_lse(d_lse)
-    _check(lib().attn_window(_ref(q), _ref(k_pool), _ref(v_pool), _format(format), _ref(pt), _ints(d_rows, "d_rows"),
-                             _ints(d_count, "d_count"), int(window), int(sinks), int(len_hint), float(scale), _ref(o),
-                             _addr(d_lse), _addr(d_ws), ws_bytes or _nbytes(d_ws), _addr(stream)), "attn_window")
+    _, heads, q_len, batch, _ = _dims(q)
+    _check_lse(d_lse, batch * q_len * heads)
+    _check(lib().attn_window(_ref(q), _ref(k_pool), _ref(v_pool), _format(format), _ref(pt),
+                             _ints(d_rows, "d_rows", batch), _ints(d_count, "d_count", batch), int(window), int(sinks),
+                             int(len_hint), float(scale), _ref(o), _addr(d_lse), _addr(d_ws),
+                             ws_bytes or _nbytes(d_ws), _addr(stream)), "attn_window")
 
 
 def attn_tree(q: tmap_t, k_pool: tmap_t, v_pool: tmap_t, format, pt: page_table_t, d_rows, d_count, d_parent,
               window: int, sinks: int, len_hint: int, scale: float, o: tmap_t, d_lse, d_ws, stream=0,
               ws_bytes: int = 0) -> None:
     """As attn_window; d_parent holds q_len parents for each sequence."""
-    _check_lse(d_lse)
-    _check(lib().attn_tree(_ref(q), _ref(k_pool), _ref(v_pool), _format(format), _ref(pt), _ints(d_rows, "d_rows"),
-                           _ints(d_count, "d_count"), _ints(d_parent, "d_parent"), int(window), int(sinks),
-                           int(len_hint), float(scale), _ref(o), _addr(d_lse), _addr(d_ws), ws_bytes or _nbytes(d_ws),
-                           _addr(stream)), "attn_tree")
+    _, heads, q_len, batch, _ = _dims(q)
+    _check_lse(d_lse, batch * q_len * heads)
+    _check(lib().attn_tree(_ref(q), _ref(k_pool), _ref(v_pool), _format(format), _ref(pt),
+                           _ints(d_rows, "d_rows", batch), _ints(d_count, "d_count", batch),
+                           _ints(d_parent, "d_parent", batch * q_len), int(window), int(sinks), int(len_hint),
+                           float(scale), _ref(o), _addr(d_lse), _addr(d_ws), ws_bytes or _nbytes(d_ws), _addr(stream)),
+           "attn_tree")

@@ -3,7 +3,8 @@
 // argument, so every field lands in scalar registers).
 //
 // The public header exposes tmap_t as 128 opaque bytes; this file is the only
-// place that interprets them.
+// place that interprets them, but for the dimensions, which the Python binding
+// reads to check the lengths of tensors against.
 #pragma once
 
 #include <stdint.h>
@@ -34,6 +35,7 @@ struct alignas(64) TmapImpl {
 };
 
 static_assert(sizeof(TmapImpl) == 128, "descriptor must stay 128 bytes");
+static_assert(__builtin_offsetof(TmapImpl, dim) == 40, "where the Python binding reads the dimensions");
 
 // Bit 7 of the OOB byte marks an im2col-mode descriptor (Im2colImpl below);
 // tiled entry points reject such maps.
