@@ -13,7 +13,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-import struct
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 # ATT_DEBUG=1 in the environment selects the debug build (LDS poisoning and
@@ -51,9 +50,15 @@ class TmapError(RuntimeError):
         super().__init__(msg)
 
 
-class tmap_t(ctypes.Structure):
+class _tmap_dims(ctypes.Structure):
+    """Where a descriptor holds its dimensions, 1 beyond its rank (att/tmap_impl.hpp)."""
+    _fields_ = [("head", ctypes.c_uint8 * 40), *((f"dim{i}", ctypes.c_int64) for i in range(5))]
+
+
+class tmap_t(ctypes.Union):
     """Opaque 128-byte descriptor (copied bytewise by the library)."""
-    _fields_ = [("opaque", ctypes.c_uint8 * 128)]
+    _anonymous_ = ("dims",)
+    _fields_ = [("opaque", ctypes.c_uint8 * 128), ("dims", _tmap_dims)]
 
 
 class tmap_info_t(ctypes.Structure):
@@ -157,6 +162,8 @@ def lib():
 
 
 def _addr(x) -> int:
+    if type(x) is int:
+        return x
     if x is None:
         return 0
     if hasattr(x, "data_ptr"):
@@ -340,22 +347,18 @@ def gemm_bf16_ex(A: tmap_t, B: tmap_t, d_C, M: int, N: int, K: int, ldc: int, st
 # reads or writes.
 
 
-def _ref(m):
-    return None if m is None else ctypes.byref(m)
+def _ref(m, byref=ctypes.byref):
+    return None if m is None else byref(m)
 
 
 _INT32 = set()      # element types that were seen to be 32-bit integers
-
-
-def _dims(m):
-    """Dimensions of a map, innermost first, 1 beyond its rank (att/tmap_impl.hpp)."""
-    return (1,) * 5 if m is None else struct.unpack_from("=5q", m, 40)
+_FLOAT32 = set()    # and to be 32-bit numbers
 
 
 def _entries(n, name: str = "n") -> int:
     """A count that the C ABI takes as uint32."""
     n = int(n)
-    if not 0 <= n < 1 << 32:
+    if n >> 32:
         raise ValueError(f"{name} has to be of 32 bits and not negative, not {n}")
     return n
 
@@ -381,7 +384,10 @@ def _ints(x, name: str, n: int = 0) -> int:
 def _nbytes(ws) -> int:
     """Bytes of a workspace given as a tensor (or any object with numel and
     element_size), else 0."""
-    return int(ws.numel()) * int(ws.element_size()) if hasattr(ws, "numel") else 0
+    try:
+        return ws.nbytes
+    except AttributeError:
+        return int(ws.numel()) * int(ws.element_size()) if hasattr(ws, "numel") else 0
 
 
 def tmap_array(maps):
@@ -411,16 +417,17 @@ def rope_encode(rot_dim: int, layout="half", base: float = 10000.0, scaling="non
 
 
 def rope_apply(r: rope_t, x: tmap_t, y: tmap_t, d_pos, inverse=False, stream=0) -> None:
-    _check(lib().rope_apply(ctypes.byref(r), ctypes.byref(x), ctypes.byref(y), _ints(d_pos, "d_pos"), int(inverse),
-                            _addr(stream)), "rope_apply")
+    _check(lib().rope_apply(ctypes.byref(r), ctypes.byref(x), ctypes.byref(y), _ints(d_pos, "d_pos", x.dim2),
+                            int(inverse), _addr(stream)), "rope_apply")
 
 
 def rope_append(r, q, q_out, k: tmap_t, v: tmap_t, k_pool: tmap_t, v_pool: tmap_t, pt: page_table_t, d_rows, d_at,
                 d_pos, stream=0) -> None:
     """r, and q with q_out, may be None (see kvcache.h)."""
+    n = 0 if k is None else k.dim2
     _check(lib().rope_append(_ref(r), _ref(q), _ref(q_out), _ref(k), _ref(v), _ref(k_pool), _ref(v_pool), _ref(pt),
-                             _ints(d_rows, "d_rows"), _ints(d_at, "d_at"), _ints(d_pos, "d_pos"), _addr(stream)),
-           "rope_append")
+                             _ints(d_rows, "d_rows", n), _ints(d_at, "d_at", n),
+                             _ints(d_pos, "d_pos", n if r is not None else 0), _addr(stream)), "rope_append")
 
 
 def _format(f) -> int:
@@ -441,7 +448,7 @@ def kv8_append(r, q, q_out, k: tmap_t, v: tmap_t, format, k_pool: tmap_t, v_pool
                d_pos, stream=0) -> None:
     """rope_append to pools of 8-bit codes; format "int8" or "e4m3" (or the
     KV_* value)."""
-    n = _dims(k)[2]
+    n = 0 if k is None else k.dim2
     _check(lib().kv8_append(_ref(r), _ref(q), _ref(q_out), _ref(k), _ref(v), _format(format), _ref(k_pool), _ref(v_pool),
                             _ref(pt), _ints(d_rows, "d_rows", n), _ints(d_at, "d_at", n),
                             _ints(d_pos, "d_pos", n if r is not None else 0), _addr(stream)), "kv8_append")
@@ -449,7 +456,7 @@ def kv8_append(r, q, q_out, k: tmap_t, v: tmap_t, format, k_pool: tmap_t, v_pool
 
 def kv8_read(format, k_pool: tmap_t, v_pool: tmap_t, pt: page_table_t, d_rows, d_at, k: tmap_t, v: tmap_t,
              stream=0) -> None:
-    n = _dims(k)[2]
+    n = 0 if k is None else k.dim2
     _check(lib().kv8_read(_format(format), _ref(k_pool), _ref(v_pool), _ref(pt), _ints(d_rows, "d_rows", n),
                           _ints(d_at, "d_at", n), _ref(k), _ref(v), _addr(stream)), "kv8_read")
 
@@ -478,34 +485,38 @@ def page_table(d_table, d_lens, d_refs, pages: int, slots: int, rows: int = 0, r
 
 
 def page_workspace(pt: page_table_t, n: int) -> int:
-    return int(lib().page_workspace(ctypes.byref(pt), int(n)))
+    return int(lib().page_workspace(ctypes.byref(pt), _entries(n)))
 
 
 def page_copy(pools, d_src, d_dst, n: int, stream=0) -> None:
     arr, k = _pool_array(pools)
-    _check(lib().page_copy(arr, k, _ints(d_src, "d_src"), _ints(d_dst, "d_dst"), int(n), _addr(stream)), "page_copy")
+    n = _entries(n)
+    _check(lib().page_copy(arr, k, _ints(d_src, "d_src", n), _ints(d_dst, "d_dst", n), n, _addr(stream)), "page_copy")
 
 
 def page_extend(pt: page_table_t, d_rows, d_add, n: int, d_ok, d_ws, stream=0, ws_bytes: int = 0) -> None:
     """d_ws is a tensor, or an address with ws_bytes; so in the calls below."""
-    _check(lib().page_extend(_ref(pt), _ints(d_rows, "d_rows"), _ints(d_add, "d_add"), int(n), _ints(d_ok, "d_ok"),
+    n = _entries(n)
+    _check(lib().page_extend(_ref(pt), _ints(d_rows, "d_rows", n), _ints(d_add, "d_add", n), n, _ints(d_ok, "d_ok", n),
                              _addr(d_ws), ws_bytes or _nbytes(d_ws), _addr(stream)), "page_extend")
 
 
 def page_fork(pt: page_table_t, pools, d_src, d_dst, n: int, d_ok, d_ws, stream=0, ws_bytes: int = 0) -> None:
     """pools: a map, several, or a tmap_array of them; None for the tables alone."""
     arr, k = _pool_array(pools)
-    _check(lib().page_fork(_ref(pt), arr, k, _ints(d_src, "d_src"), _ints(d_dst, "d_dst"), int(n),
-                           _ints(d_ok, "d_ok"), _addr(d_ws), ws_bytes or _nbytes(d_ws), _addr(stream)), "page_fork")
+    n = _entries(n)
+    _check(lib().page_fork(_ref(pt), arr, k, _ints(d_src, "d_src", n), _ints(d_dst, "d_dst", n), n,
+                           _ints(d_ok, "d_ok", n), _addr(d_ws), ws_bytes or _nbytes(d_ws), _addr(stream)), "page_fork")
 
 
 def page_free(pt: page_table_t, d_rows, n: int, stream=0) -> None:
-    _check(lib().page_free(_ref(pt), _ints(d_rows, "d_rows"), int(n), _addr(stream)), "page_free")
+    n = _entries(n)
+    _check(lib().page_free(_ref(pt), _ints(d_rows, "d_rows", n), n, _addr(stream)), "page_free")
 
 
 def page_compact(pt: page_table_t, pt_to: page_table_t, pools, d_used, d_ws, stream=0, ws_bytes: int = 0) -> None:
     arr, k = _pool_array(pools)
-    _check(lib().page_compact(_ref(pt), _ref(pt_to), arr, k, _ints(d_used, "d_used"), _addr(d_ws),
+    _check(lib().page_compact(_ref(pt), _ref(pt_to), arr, k, _ints(d_used, "d_used", 1), _addr(d_ws),
                               ws_bytes or _nbytes(d_ws), _addr(stream)), "page_compact")
 
 
@@ -528,21 +539,31 @@ def attn_workspace(q: tmap_t, k_pool: tmap_t, prefix_len: int, suffix_hint: int)
     return int(lib().attn_workspace(_ref(q), _ref(k_pool), int(prefix_len), int(suffix_hint)))
 
 
-def _check_lse(d_lse, n: int = 0):
-    if hasattr(d_lse, "data_ptr"):
-        if d_lse.element_size() != 4 or not d_lse.is_floating_point() or not d_lse.is_contiguous():
+def _lse(x, n: int) -> int:
+    """Address of n float32 values or more, as _ints; 0 for None."""
+    try:
+        if x.dtype in _FLOAT32 and x.is_contiguous() and x.numel() >= n:
+            return x.data_ptr()
+    except AttributeError:
+        pass
+    if hasattr(x, "data_ptr"):
+        if x.element_size() != 4 or not x.is_floating_point() or not x.is_contiguous():
             raise TypeError("d_lse has to be float32 values side by side")
-        if d_lse.numel() < n:
+        if x.numel() < n:
             raise ValueError(f"d_lse has to hold {n} values")
+        _FLOAT32.add(x.dtype)
+    return _addr(x)
 
 
 def attn_shared_prefix(q: tmap_t, k_pool: tmap_t, v_pool: tmap_t, pt: page_table_t, prefix_row: int,
                        prefix_len: int, d_rows, suffix_hint: int, scale: float, o: tmap_t, d_lse, d_ws, stream=0,
                        ws_bytes: int = 0) -> None:
-    _check_lse(d_lse)
+    batch, n = (0, 0) if q is None else (q.dim3, q.dim3 * q.dim2 * q.dim1)
+    lse = _lse(d_lse, n)
     _check(lib().attn_shared_prefix(_ref(q), _ref(k_pool), _ref(v_pool), _ref(pt), int(prefix_row), int(prefix_len),
-                                    _ints(d_rows, "d_rows"), int(suffix_hint), float(scale), _ref(o), _addr(d_lse),
-                                    _addr(d_ws), ws_bytes or _nbytes(d_ws), _addr(stream)), "attn_shared_prefix")
+                                    _ints(d_rows, "d_rows", batch), int(suffix_hint), float(scale), _ref(o),
+                                    lse, _addr(d_ws), ws_bytes or _nbytes(d_ws), _addr(stream)),
+           "attn_shared_prefix")
 
 
 def attn_cache_workspace(q: tmap_t, k_pool: tmap_t, window: int, sinks: int, len_hint: int) -> int:
@@ -553,11 +574,11 @@ def attn_window(q: tmap_t, k_pool: tmap_t, v_pool: tmap_t, format, pt: page_tabl
                 sinks: int, len_hint: int, scale: float, o: tmap_t, d_lse, d_ws, stream=0, ws_bytes: int = 0) -> None:
     """format: "same", "int8" or "e4m3" (or the KV_* value); d_rows, d_count and
     d_lse may be None."""
-    _, heads, q_len, batch, _ = _dims(q)
-    _check_lse(d_lse, batch * q_len * heads)
+    batch, n = (0, 0) if q is None else (q.dim3, q.dim3 * q.dim2 * q.dim1)
+    lse = _lse(d_lse, n)
     _check(lib().attn_window(_ref(q), _ref(k_pool), _ref(v_pool), _format(format), _ref(pt),
                              _ints(d_rows, "d_rows", batch), _ints(d_count, "d_count", batch), int(window), int(sinks),
-                             int(len_hint), float(scale), _ref(o), _addr(d_lse), _addr(d_ws),
+                             int(len_hint), float(scale), _ref(o), lse, _addr(d_ws),
                              ws_bytes or _nbytes(d_ws), _addr(stream)), "attn_window")
 
 
@@ -565,10 +586,10 @@ def attn_tree(q: tmap_t, k_pool: tmap_t, v_pool: tmap_t, format, pt: page_table_
               window: int, sinks: int, len_hint: int, scale: float, o: tmap_t, d_lse, d_ws, stream=0,
               ws_bytes: int = 0) -> None:
     """As attn_window; d_parent holds q_len parents for each sequence."""
-    _, heads, q_len, batch, _ = _dims(q)
-    _check_lse(d_lse, batch * q_len * heads)
+    batch, nodes = (0, 0) if q is None else (q.dim3, q.dim3 * q.dim2)
+    lse = _lse(d_lse, nodes * q.dim1 if nodes else 0)
     _check(lib().attn_tree(_ref(q), _ref(k_pool), _ref(v_pool), _format(format), _ref(pt),
                            _ints(d_rows, "d_rows", batch), _ints(d_count, "d_count", batch),
-                           _ints(d_parent, "d_parent", batch * q_len), int(window), int(sinks), int(len_hint),
-                           float(scale), _ref(o), _addr(d_lse), _addr(d_ws), ws_bytes or _nbytes(d_ws), _addr(stream)),
+                           _ints(d_parent, "d_parent", nodes), int(window), int(sinks), int(len_hint),
+                           float(scale), _ref(o), lse, _addr(d_ws), ws_bytes or _nbytes(d_ws), _addr(stream)),
            "attn_tree")

@@ -24,9 +24,12 @@ def short(call, name):
 @pytest.mark.parametrize("dims", [(128, 8, 1, 4), (96, 5, 77, 3), (8, 1, 1024, 1)])
 def test_map_dims(dims):
     dim, n, q_len, batch = dims
-    assert att._dims(queries(dim, n, q_len, batch)) == (*dims, 1)
-    assert att._dims(att.tmap_array([queries(), queries(dim, n, q_len, batch)])[1]) == (*dims, 1)
-    assert att._dims(heads(128, 7, 2 ** 31 - 1)) == (128, 7, 2 ** 31 - 1, 1, 1)
+    def of(m):
+        return m.dim0, m.dim1, m.dim2, m.dim3, m.dim4
+
+    assert of(queries(dim, n, q_len, batch)) == (*dims, 1)
+    assert of(att.tmap_array([queries(), queries(dim, n, q_len, batch)])[1]) == (*dims, 1)
+    assert of(heads(128, 7, 2 ** 31 - 1)) == (128, 7, 2 ** 31 - 1, 1, 1)
 
 
 # what a call of 4 sequences with 3 queries of 8 heads takes
@@ -89,3 +92,57 @@ def test_keep_counts(n):
         att.page_keep(table(), None, BASE, BASE, torch.zeros((4, 4), dtype=torch.int32), BASE, n, BASE)
     with pytest.raises(ValueError, match="width has"):
         att.page_keep(table(), None, BASE, BASE, BASE, BASE, 4, BASE, width=n)
+
+
+# ---- the calls on pages of 16 bits and behind a shared prefix --------------------------
+
+
+def test_rope():
+    r, x = att.rope_encode(64), heads()
+    refused(lambda: att.rope_apply(r, x, heads(n=9), values(16)), "ERR_UNSUPPORTED")
+    short(lambda: att.rope_apply(r, x, heads(n=9), values(15)), "d_pos")
+
+
+@pytest.mark.parametrize("name", ["d_rows", "d_at", "d_pos"])
+def test_append_same(name):
+    def call(n, r=att.rope_encode(64), d_pos=None):
+        rows, at, pos = (values(n if name == k else 16) for k in ("d_rows", "d_at", "d_pos"))
+        att.rope_append(r, None, None, heads(n=2), heads(n=2), pool(), pool(), None, rows, at,
+                        pos if d_pos is None else d_pos)
+
+    refused(lambda: call(16), "ERR_NULL")
+    short(lambda: call(15), name)
+    if name == "d_pos":
+        refused(lambda: call(16, None, values(0)), "ERR_NULL")
+
+
+def test_pages():
+    four, three = values(4), values(3)
+    ws = values(1 << 12)
+    t = table(lens=0)                                                    # refused once the library is called
+    for a, b, name in ((three, four, "d_src"), (four, three, "d_dst")):
+        short(lambda: att.page_copy(pool(), a, b, 4), name)
+        short(lambda: att.page_fork(t, None, a, b, 4, four, ws), name)
+    for a, b, c, name in ((three, four, four, "d_rows"), (four, three, four, "d_add"), (four, four, three, "d_ok")):
+        short(lambda: att.page_extend(t, a, b, 4, c, ws), name)
+    short(lambda: att.page_fork(t, None, four, four, 4, three, ws), "d_ok")
+    short(lambda: att.page_free(t, three, 4), "d_rows")
+    short(lambda: att.page_compact(t, t, None, values(0), ws), "d_used")
+    refused(lambda: att.page_extend(t, four, four, 4, four, ws), "ERR_NULL")
+    refused(lambda: att.page_fork(t, None, four, four, 4, four, ws), "ERR_NULL")
+    refused(lambda: att.page_free(t, four, 4), "ERR_NULL")
+    refused(lambda: att.page_compact(table(refs=0), t, None, values(1), ws), "ERR_NULL")
+    for call in (lambda: att.page_copy(pool(), BASE, BASE, -1), lambda: att.page_free(t, BASE, -1),
+                 lambda: att.page_extend(t, BASE, BASE, -1, BASE, ws), lambda: att.page_workspace(t, -1),
+                 lambda: att.page_fork(t, None, BASE, BASE, 2 ** 32, BASE, ws)):
+        short(call, "n has")
+
+
+def test_shared_prefix():
+    def call(rows=4, lse=96):
+        att.attn_shared_prefix(queries(q_len=3), pool(), pool(), table(), 0, 0, values(rows), 64, 0.1, queries(q_len=3),
+                               values(lse, torch.float32), 0)
+
+    refused(call, "ERR_NULL")
+    short(lambda: call(rows=3), "d_rows")
+    short(lambda: call(lse=95), "d_lse")
