@@ -500,7 +500,8 @@ __device__ __forceinline__ void tall_part(cargs& a, Shared<DP, FMT>& sh, const J
     // The threads that place the keys of a segment, one each.
     const bool places = THREADS == kSegment || tid < kSegment;
     constexpr bool CODES = FMT != KV_SAME, SPLIT = CODES && kSplitScales<T>;
-    Wave<T, DP, CODES> w;
+    using W = Wave<T, DP, CODES, true>;
+    W w;
     w.load_row(a, row.q, row.valid);
     int32_t page = -1;
     Scales scales = {0, 0};
@@ -604,7 +605,7 @@ __device__ __forceinline__ void tall_part(cargs& a, Shared<DP, FMT>& sh, const J
     // whole are added to the rows that see them, and are 0 for the product.
     auto odd_values = [&](uint32_t t, const f32x16 (&p)[2]) {
         uint8_t* const v = vals(t);
-        const bool odd = Wave<T, DP, CODES>::template odd_share<false>(v, wave, WAVES, kTile);
+        const bool odd = W::template odd_share<false>(v, wave, WAVES, kTile);
         if (odd && lane == 0) sh.odd[t % 3u] = 1u;
         wait_lgkm0();
         wg_barrier();
@@ -612,7 +613,7 @@ __device__ __forceinline__ void tall_part(cargs& a, Shared<DP, FMT>& sh, const J
         if (busy) w.template add_odd<2>(v, p, seen);
         wait_lgkm0();
         wg_barrier();
-        Wave<T, DP, CODES>::template odd_share<true>(v, wave, WAVES, kTile);
+        W::template odd_share<true>(v, wave, WAVES, kTile);
         wait_lgkm0();
         wg_barrier();
     };
@@ -642,7 +643,7 @@ __device__ __forceinline__ void tall_part(cargs& a, Shared<DP, FMT>& sh, const J
             if ((SPLIT || FMT != KV_INT8) && (BETWEEN || !seen_by_all<kTile>(x, k0 + t * kTile)))
                 odd_values(t, s[0]);                                       // an int8 code by itself is a number
             if (!busy) continue;
-            typename Wave<T, DP, CODES>::Piece z[2][DP / 32];
+            typename W::Piece z[2][DP / 32];
             w.read_values(vals(t), 0, z[0]);
             w.values(vals(t), s[0], z);
             w.scores(keys(t + 1u), s[0]);
@@ -667,6 +668,7 @@ __device__ __forceinline__ void tall_part(cargs& a, Shared<DP, FMT>& sh, const J
     cargs& e = fresh();
     const uint32_t hh = lane / 32u;
     const float l = w.total();
+    w.settle();
     if (e.direct) {
         if (!row.valid) return;
         const Row out = row_of(e, job, first_row + wave * kRows + lane % 32u, rows);
@@ -711,6 +713,7 @@ __device__ __forceinline__ void short_part(cargs& a, ShortShared<DP, FMT>& sh, c
     const Row row = row_of(a, job, first_row + n32, rows);
     constexpr uint32_t NP = Geo<DP>::cpr / 2;                             // copies of a tile's keys
     constexpr bool CODES = FMT != KV_SAME, SPLIT = CODES && kSplitScales<T>;
+    using W = Wave<T, DP, false, true>;
     // Pages of the list: those of the first tokens, then those from `low` on.
     const uint32_t few_pages = x.few ? column_of(a, x.few - 1u) + 1u : 0u, low_page = column_of(a, x.low);
     auto entry_of = [&](uint32_t column, bool few) { return few ? column : column - low_page + few_pages; };
@@ -724,7 +727,7 @@ __device__ __forceinline__ void short_part(cargs& a, ShortShared<DP, FMT>& sh, c
             if (x.n && p <= last) sh.page[i * kThreads + tid] = entries[p < few_pages ? p : p - few_pages + low_page];
         }
     };
-    Wave<T, DP> w;
+    W w;
     w.load_row(a, row.q, row.valid);
     auto first_page = [&](uint32_t i) {
         const int32_t t = token_of<kOwnTile>(x, i < x.context ? i : x.n - kOwnTile, x.n);   // of the drafted ones the first node
@@ -845,13 +848,13 @@ __device__ __forceinline__ void short_part(cargs& a, ShortShared<DP, FMT>& sh, c
             } else {
                 wait_vmcnt<0>();
             }
-            if ((SPLIT || FMT != KV_INT8) && !all && Wave<T, DP>::template odd_share<false>(vals, 0, 1, kOwnTile)) {
+            if ((SPLIT || FMT != KV_INT8) && !all && W::template odd_share<false>(vals, 0, 1, kOwnTile)) {
                 w.template add_odd<1>(vals, s, bits);
                 wait_lgkm0();
-                Wave<T, DP>::template odd_share<true>(vals, 0, 1, kOwnTile);
+                W::template odd_share<true>(vals, 0, 1, kOwnTile);
                 wait_lgkm0();
             }
-            typename Wave<T, DP>::Piece z[2][DP / 32];
+            typename W::Piece z[2][DP / 32];
             w.read_values(vals, 0, z[0]);
             w.values(vals, s, z);
             wait_lgkm0();
@@ -866,6 +869,7 @@ __device__ __forceinline__ void short_part(cargs& a, ShortShared<DP, FMT>& sh, c
     f32x4* const sums = reinterpret_cast<f32x4*>(sh.ring);
     const uint32_t working = tiles < kWaves ? tiles : kWaves;
     const float total = w.total();
+    w.settle();
     if (lane < 32u) ml[wave * 32u + lane] = make_float2(w.m, total);
     __syncthreads();
     float m = -INFINITY, l = 0.0f;

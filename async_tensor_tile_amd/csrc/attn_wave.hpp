@@ -29,6 +29,11 @@ constexpr uint32_t kOwnTile = 32;                 // keys of a wave's own tile
 constexpr uint32_t kSegment = 256;                // keys whose addresses are worked out together
 constexpr float kLazy = 8.0f;                     // powers of two by which a weight may pass 1
 constexpr float kLog2e = 1.4426950408889634f;
+// Powers of two by which weights are taken larger for f16, whose smallest number is
+// 2^-24: with it a weight vanishes below 2^-32 of the largest one, not below 2^-25
+// (131072 tokens 17.5 below the largest score are 0.3 % of a result), and the largest
+// that kLazy and a scale below 2 leave, 2^15 * (2 - 2^-7), is still a number.
+constexpr float kHead = 7.0f;
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -144,10 +149,12 @@ __device__ __forceinline__ uint64_t zero_row() { return (uint64_t)(uintptr_t)g_z
 // beside codes on their way, they do not fit into the registers, and one that comes
 // back from memory waits for the codes too (2048 queries of 32768 e4m3 tokens: 1247 us,
 // this 1165).
-template <typename T, uint32_t DP, bool AGAIN = false>
+// HEAD: f16 weights are taken 2^kHead times as large.
+template <typename T, uint32_t DP, bool AGAIN = false, bool HEAD = false>
 struct Wave {
     typedef typename Vec<T>::v8 v8;
     typedef typename Vec<T>::v4 v4;
+    static constexpr float head = HEAD && std::is_same<T, _Float16>::value ? kHead : 0.0f;
     static constexpr uint32_t NK = DP / 16, NO = DP / 32;
     v8 q[NK];
     f32x16 o[NO];
@@ -258,8 +265,11 @@ struct Wave {
 #pragma unroll
             for (uint32_t i = 0; i < NO; ++i) o[i] *= fade;
         }
-        return m == -INFINITY ? 0.0f : m;
+        return m == -INFINITY ? 0.0f : m - head;
     }
+
+    // All keys are in: m is what the sums are relative to.
+    __device__ __forceinline__ void settle() { m -= head; }
 
     // Weights of the scores, in place.
     template <uint32_t NB>

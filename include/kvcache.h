@@ -250,7 +250,8 @@ uint64_t attn_cache_workspace(const tmap_t* q, const tmap_t* k_pool, uint32_t wi
  * them: query j stands at p = d_lens[r] - n + j and sees the tokens t <= p that
  * are within the window, t > p - window, or among the first `sinks` ones
  * (window 0: every t <= p).  o, lse, heads, types, scale and the rounding as
- * attn_shared_prefix; a query that sees nothing gets o = 0 and lse = -inf, and
+ * attn_shared_prefix, but that an f16 weight vanishes below 2^-32 of the largest
+ * (there below 2^-25); a query that sees nothing gets o = 0 and lse = -inf, and
  * what a query does not see does not reach it, whatever it holds.  The pools are
  * of the queries' type (KV_SAME) or hold codes; a key is c * s, and so is a value
  * (f16: one beyond the type's numbers is an infinity, one below its normal
