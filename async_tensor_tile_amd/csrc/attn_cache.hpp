@@ -18,9 +18,10 @@
 // Codes.  Keys go to the matrix cores as they are (a code is exact in 16 bits)
 // and the fp32 scores are multiplied by the keys' scales.  So do values for bf16,
 // whose scales multiply the fp32 weights before their rounding.  f16 has no room for
-// a weight times any scale: there the power of two in the scale goes to the code,
-// exactly, and the rest of it to the weight.  Either way a weight is rounded once
-// and a value not at all.
+// a weight times any scale: there the power of two in the scale goes to the code and
+// the rest of it to the weight.  Either way a weight is rounded once; a value is not,
+// but for an f16 code times its power of two that leaves the type's normal numbers:
+// an infinity above them, rounded to the steps of the smallest ones below.
 //
 // What bounds it.  Few rows: HBM.  64 sequences' next tokens, window 8192, 32 heads
 // over 8 of 128 elements: bf16 384 us (2.15 GB, 5.6 TB/s), e4m3 230 (1.09 GB, 4.7).

@@ -254,10 +254,11 @@ uint64_t attn_cache_workspace(const tmap_t* q, const tmap_t* k_pool, uint32_t wi
  * (there below 2^-25); a query that sees nothing gets o = 0 and lse = -inf, and
  * what a query does not see does not reach it, whatever it holds.  The pools are
  * of the queries' type (KV_SAME) or hold codes; a key is c * s, and so is a value
- * (f16: one beyond the type's numbers is an infinity, one below its normal
- * numbers is rounded to a step of theirs).  len_hint is the length that the work
- * is split for (any value is right).  A count or row out of range is recorded: no
- * query is there, or none sees a token.  Errors as attn_shared_prefix, and
+ * (f16: where c times the power of two in s is beyond the type's numbers it is an
+ * infinity, and below its normal numbers it is rounded to a step of theirs; c * s
+ * itself may pass them).  len_hint is the length that the work is split for (any
+ * value is right).  A count or row out of range is recorded: no query is there, or
+ * none sees a token.  Errors as attn_shared_prefix, and
  * UNSUPPORTED for pools that are not of the format and for more than 2^31 - 1
  * pairs of a query and a head of its group, or 2^24 - 1 workgroups (one at most
  * for each sequence, key / value head and 32 such pairs, or 512 in all). */
