@@ -260,8 +260,9 @@ uint64_t attn_cache_workspace(const tmap_t* q, const tmap_t* k_pool, uint32_t wi
  * value is right).  A count or row out of range is recorded: no query is there, or
  * none sees a token.  Errors as attn_shared_prefix, and
  * UNSUPPORTED for pools that are not of the format and for more than 2^31 - 1
- * pairs of a query and a head of its group, or 2^24 - 1 workgroups (one at most
- * for each sequence, key / value head and 32 such pairs, or 512 in all). */
+ * pairs of a query and a head of its group, or 2^24 - 1 workgroups (four at most
+ * for each sequence, key / value head and 32 such pairs, or 1280 in all;
+ * attn_cache_workspace says 0 where there are more). */
 tmap_status attn_window(const tmap_t* q, const tmap_t* k_pool, const tmap_t* v_pool, int32_t format,
                         const page_table_t* pt, const int32_t* d_rows, const int32_t* d_count, uint32_t window,
                         uint32_t sinks, uint32_t len_hint, float scale, const tmap_t* o, float* d_lse, void* d_ws,

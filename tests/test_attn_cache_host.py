@@ -105,3 +105,21 @@ def test_oracle_attention():
     o, lse, _, _, seen = ok.attend(q, k, v, np.array([[True, False], [False, False]]), 1.0)
     assert o[0, 0].tolist() == [2.0, 4.0] and o[1, 0].tolist() == [0.0, 0.0]
     assert lse[0, 0] == 1.0 and np.isneginf(lse[1, 0]) and seen[:, 0].tolist() == [1, 0]
+
+
+def test_workgroups_of_a_call():
+    """Few rows: a part of partial results for each workgroup, [dim rounded up, 32] sums and 32 pairs of 8 bytes."""
+    most = 0
+    for batch in (1, 2, 3, 7, 16, 31, 32, 40, 63, 64, 65, 100, 128, 129, 200, 300, 511, 512, 513, 700, 5000):
+        for kv in (1, 2, 8):
+            for group in (1, 4, 32):
+                for hint in (0, 500, 2047, 2048, 3000, 8192, 20000, 1 << 20, 2 ** 32 - 1):
+                    for window in (0, 4096):
+                        got = att.attn_cache_workspace(queries(dim=64, n=kv * group, batch=batch), pool(dim=64, n=kv),
+                                                       window, 4, hint)
+                        parts = (got - 16) // (64 * 32 * 4 + 32 * 8)
+                        assert (got - 16) % (64 * 32 * 4 + 32 * 8) == 0
+                        units = batch * kv
+                        assert parts <= max(4 * units, 1280) and parts % units == 0
+                        most = max(most, parts / units if units > 256 else 0)
+    assert most > 1                                                      # more than one a unit, and than 512 in all
