@@ -25,11 +25,17 @@
 //
 // What bounds it.  Few rows: HBM.  64 sequences' next tokens, window 8192, 32 heads
 // over 8 of 128 elements: bf16 384 us (2.15 GB, 5.6 TB/s), e4m3 230 (1.09 GB, 4.7).
-// Many rows: matrix products beside the weights' arithmetic, which take turns on a
-// SIMD.  2048 queries of 32768 tokens: bf16 985 us (1.08 Pflop/s, matrix cores busy 51 %
-// of the time, vector units 50 %), e4m3 1145 to 1190 and int8 beside f16 1240 to 1290 (36 to
-// 38 %, vector units 53 to 56 %: codes into elements, scales).  A few short sequences:
-// the launch and a chain of reads, row, length, page, keys: 9.1 us.
+// Many rows: neither the matrix products nor the weights' arithmetic, but how little
+// the two overlap.  2048 queries of 32768 tokens: bf16 985 us (1.08 Pflop/s, matrix cores
+// busy 51 % of the time, vector units 50 %), e4m3 1145 to 1190 and int8 beside f16 1240 to
+// 1290 (36 to 38 %, vector units 53 to 56 %: codes into elements, scales).  With 32 rows a
+// wave each product takes an LDS read and a wait of its own.  Short windows: a
+// workgroup's start and end, about 15 us, then 2.4 us a tile (5 x 777 queries of int8,
+// dim 80: window 1 17 us, 300 30, 600 40).  A few short sequences: the launch and a
+// chain of reads, row, length, page, keys: 9.1 us.
+// Registers that do not fit go to memory: at dim 128 36 to 68 bytes a lane of the
+// kernels for many rows of codes, 28 to 48 of those for few, 12 of the eight waves' in
+// 16 bits; at dim 256 116 to 164, 312 for bf16 beside int8; none elsewhere.
 #pragma once
 
 #include <hip/hip_runtime.h>

@@ -119,9 +119,12 @@ static uint64_t plan(CacheArgs* a, uint32_t hint, bool codes) {
     const bool few = rows <= kRows || (shorts <= 2 * cus && shorts * keys_of(kRows) <= (codes ? 1u << 19 : 1u << 18));
     // Waves of a workgroup with many rows.  Eight share a tile's copies, and the work
     // of turning codes into elements (2048 queries of 32768 tokens: 972 us, with four
-    // waves 1055; int8 1626 and 1973), but mask more where they see few keys (8192
-    // queries, window 128: 98 and 88 us, window 1024 200 and 197) and wait for each
-    // other where half of them have no rows (16 trees of 120 rows: 75 and 69 us).
+    // waves 1055; int8 beside f16 1234 and 1545, e4m3 1147 and 1329).  In 16 bits they
+    // mask more where they see few keys (8192 queries, window 128: 98 and 88 us, window
+    // 1024 200 and 197) and wait for each other where half of them have no rows (16 trees
+    // of 120 rows: 75 and 69 us).  Codes cost more than that with any window (8192
+    // queries, window 128: int8 124 and 134 us, e4m3 112 and 135; 5 x 777 queries, window
+    // 300, of 20 heads over 4 of 80: 30 and 43, of 40 over 8 of 128: 30.7 and 31.6).
     // Above dim 128 a wave needs the registers of two; the twelve groups of a tile's copies
     // at dim 96 are no whole number for each of eight.
     const bool many = codes || (dp != 96 && rows > 4 * kRows && keys_of(8 * kRows) >= 2048);

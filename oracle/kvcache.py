@@ -13,7 +13,8 @@ import numpy as np
 def to_f64(bits: np.ndarray, dtype: str) -> np.ndarray:
     """Values of an array that holds a type's bits (u16 for f16 and bf16)."""
     if dtype == "bf16":
-        return (bits.astype(np.uint32) << 16).view(np.float32).astype(np.float64)
+        with np.errstate(invalid="ignore"):                              # a signalling NaN becomes a quiet one
+            return (bits.astype(np.uint32) << 16).view(np.float32).astype(np.float64)
     return bits.view({"f16": np.float16, "f32": np.float32}[dtype]).astype(np.float64)
 
 
