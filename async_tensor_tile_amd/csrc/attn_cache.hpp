@@ -675,7 +675,6 @@ __device__ __forceinline__ void tall_part(cargs& a, Shared<DP, FMT>& sh, const J
     cargs& e = fresh();
     const uint32_t hh = lane / 32u;
     const float l = w.total();
-    w.settle();
     if (e.direct) {
         if (!row.valid) return;
         const Row out = row_of(e, job, first_row + wave * kRows + lane % 32u, rows);
@@ -876,7 +875,6 @@ __device__ __forceinline__ void short_part(cargs& a, ShortShared<DP, FMT>& sh, c
     f32x4* const sums = reinterpret_cast<f32x4*>(sh.ring);
     const uint32_t working = tiles < kWaves ? tiles : kWaves;
     const float total = w.total();
-    w.settle();
     if (lane < 32u) ml[wave * 32u + lane] = make_float2(w.m, total);
     __syncthreads();
     float m = -INFINITY, l = 0.0f;

@@ -31,9 +31,11 @@ constexpr float kLazy = 8.0f;                     // powers of two by which a we
 constexpr float kLog2e = 1.4426950408889634f;
 // Powers of two by which weights are taken larger for f16, whose smallest number is
 // 2^-24: with it a weight vanishes below 2^-32 of the largest one, not below 2^-25
-// (131072 tokens 17.5 below the largest score are 0.3 % of a result), and the largest
-// that kLazy and a scale below 2 leave, 2^15 * (2 - 2^-7), is still a number.
+// (131072 tokens 17.5 below the largest score are 0.3 % of a result).  They may pass the
+// largest of before by 2^7 then, not by 2^kLazy: 2^14 times the rest of a scale, below
+// 2, leaves a factor of two for the roundings of scores, in powers of two, up to 2^24.
 constexpr float kHead = 7.0f;
+constexpr float kHeadLazy = 7.0f;
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -154,11 +156,12 @@ template <typename T, uint32_t DP, bool AGAIN = false, bool HEAD = false>
 struct Wave {
     typedef typename Vec<T>::v8 v8;
     typedef typename Vec<T>::v4 v4;
-    static constexpr float head = HEAD && std::is_same<T, _Float16>::value ? kHead : 0.0f;
+    static constexpr bool headed = HEAD && std::is_same<T, _Float16>::value;
+    static constexpr float head = headed ? kHead : 0.0f, most = headed ? kHead + kHeadLazy : kLazy;
     static constexpr uint32_t NK = DP / 16, NO = DP / 32;
     v8 q[NK];
     f32x16 o[NO];
-    float m, l;                      // largest score seen in powers of two (or below by kLazy at most), sum of weights
+    float m, l;                      // largest score seen, in powers of two, less head (or less: lazily), sum of weights
 
     __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -252,24 +255,21 @@ struct Wave {
     }
 
     // The sums are only rescaled when a score passes the largest of before by
-    // 2^kLazy; weights then stay below 2^kLazy, which both types hold.
+    // 2^kLazy; weights then stay below 2^most, which both types hold.
     // Returns what weights are taken relative to.  Each query goes by its own
     // scores, so its result does not depend on the others of the wave.  A top
     // that is NaN (no score is a number) makes the sums NaN, as it has to.
     __device__ __forceinline__ float rescale(float top) {
-        const bool pass = !(top <= m + kLazy);
+        const bool pass = !(top <= m + most);
         if (__any(pass)) {
-            const float fade = pass ? __builtin_amdgcn_exp2f(m - top) : 1.0f;
-            m = pass ? top : m;
+            const float next = top - head, fade = pass ? __builtin_amdgcn_exp2f(m - next) : 1.0f;
+            m = pass ? next : m;
             l *= fade;
 #pragma unroll
             for (uint32_t i = 0; i < NO; ++i) o[i] *= fade;
         }
-        return m == -INFINITY ? 0.0f : m - head;
+        return m == -INFINITY ? 0.0f : m;
     }
-
-    // All keys are in: m is what the sums are relative to.
-    __device__ __forceinline__ void settle() { m -= head; }
 
     // Weights of the scores, in place.
     template <uint32_t NB>

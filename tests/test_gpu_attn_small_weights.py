@@ -109,3 +109,45 @@ def test_scores_of_all_sizes(q_len, hint, dim, fmt):
     check(s, 0, 0, None, 5 / math.sqrt(dim), hint)
     check(s, 120, 3, None, -3 / math.sqrt(dim), hint)
     check(s, 0, 0, parents_of(g, 2, q_len, "near"), 5 / math.sqrt(dim), hint)
+
+
+def scales_of(p, s, scale):
+    """All scales of a pool of codes."""
+    x = p if s.heads_first else p.transpose(1, 2)
+    tail = torch.zeros((*x.shape[:2], (x.shape[2] - s.slots) * s.dim), dtype=torch.uint8)
+    tail[..., :2 * s.slots] = torch.full((*x.shape[:2], s.slots), scale).bfloat16().view(torch.uint8)
+    x[:, :, s.slots:] = tail.view(*x.shape[:2], -1, s.dim).cuda()
+
+
+@pytest.mark.parametrize("fmt", ["same", "int8", "e4m3"])
+@pytest.mark.parametrize("q_len,heads,tile", [(1, 1, 128), (40, 1, 128), (200, 16, 64)])
+@pytest.mark.parametrize("power", [12, 14, 16, 17, 18, 20, 23])
+def test_scores_so_large_that_their_roundings_count(power, q_len, heads, tile, fmt):
+    """Scores of 2^power that pass the largest of before by about 2^8, tile after tile (every fourth of 32, or each of 64):
+    every weight is a number that f16 holds, beside the largest rest of a value's scale too, and a result lies among the
+    values."""
+    n, units = 1500, 2.0 ** np.arange(15, -9, -4)
+    s = Setup(gen(803), "f16", fmt, [n] * 6, None, q_len, heads, 1, 64, 16)
+    scale = max(1.0, 2.0 ** (power - 17))
+    x = torch.rand((6, n), generator=gen(804)).numpy()
+    want = (2.0 ** power + 8 * (np.arange(n) // tile) + 0.1 * (x - 0.5)) * math.log(2) / scale
+    s.q.zero_()
+    s.q[..., :6] = torch.from_numpy(units).half().cuda()
+    for b, r in enumerate(s.rows):
+        rest, digits = want[b], np.zeros((n, 6))
+        for d, unit in enumerate(units):                                 # 0 .. 15, which every format holds
+            digits[:, d] = np.floor(rest / unit)
+            rest = rest - digits[:, d] * unit
+        assert digits.min() >= 0 and digits.max() < 16
+        page, slot = s.table[r].cpu().numpy()[np.arange(n) // 16], np.arange(n) % 16
+        code = torch.from_numpy(digits)
+        code = code.half() if fmt == "same" else code.to(torch.int8).view(torch.uint8) if fmt == "int8" else \
+            code.float().to(torch.float8_e4m3fn).view(torch.uint8)
+        s.k[page, slot] = 0
+        s.k[page, slot, 0, :6] = code.cuda()
+    if fmt != "same":
+        scales_of(s.k, s, 1.0), scales_of(s.v, s, 1.9921875 / 64)
+    got, lse = s.run(0, 0, None, scale, hint=100)
+    assert np.isfinite(got).all() and np.isfinite(lse).all()
+    for b in range(6):
+        assert (np.abs(got[b]) <= np.abs(s.tokens(s.v, b)).max() * (1 + 2.0 ** -9)).all()
