@@ -123,8 +123,8 @@ static uint64_t plan(CacheArgs* a, uint32_t hint, bool codes) {
     // mask more where they see few keys (8192 queries, window 128: 98 and 88 us, window
     // 1024 200 and 197) and wait for each other where half of them have no rows (16 trees
     // of 120 rows: 75 and 69 us).  Codes cost more than that with any window (8192
-    // queries, window 128: int8 124 and 134 us, e4m3 112 and 135; 5 x 777 queries, window
-    // 300, of 20 heads over 4 of 80: 30 and 43, of 40 over 8 of 128: 30.7 and 31.6).
+    // queries, window 128: int8 124 and 134 us, e4m3 112 and 135; window 300: 5 x 777 queries
+    // of 20 heads over 4 of 80 30 and 43, 777 of 40 over 8 of 128 30.7 and 31.6).
     // Above dim 128 a wave needs the registers of two; the twelve groups of a tile's copies
     // at dim 96 are no whole number for each of eight.
     const bool many = codes || (dp != 96 && rows > 4 * kRows && keys_of(8 * kRows) >= 2048);

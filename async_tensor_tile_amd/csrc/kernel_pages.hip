@@ -14,7 +14,7 @@
 // 10.8 us (6.1 TB/s, partly from the caches).  A small fork is its launches: free
 // 2.6, hand out 5.3, rows and pages 4.4, extend 3.8 us.  So is keeping accepted tokens:
 // 128 entries of up to 8 of 64 tokens in 16 pools take 9.4 us and 4.4 for the rows'
-// ends, 2 entries of 13 in 4 pools 5.5 to 6.1 in one launch.
+// ends, 2 entries of 13 in 4 pools 5.5 in one launch.
 #include <hip/hip_runtime.h>
 
 #include <cstring>
